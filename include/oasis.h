@@ -650,6 +650,172 @@ OASIS_API oasis_status oasis_set_agreement(const oasis_shape* shape, const int32
 OASIS_API size_t oasis_trace_bytes(int32_t capacity);
 OASIS_API oasis_status oasis_trace_set(void* dev_buf, int32_t capacity);
 
+/*
+ * Paged KV cache in 8 bits (the pages have no counterpart: the dense part of a
+ * model that serves beside the sparse path - the prompt's own attention, layers
+ * that stay dense, and a whole context kept in HBM).  Four operators share it:
+ *
+ *   oasis_extend_tables         pages for new tokens, and every new token's slot
+ *   oasis_store_kv_q8           new K/V rows, quantised into their pages
+ *   oasis_paged_decode_attn_q8  attention of one query token per request
+ *   oasis_prompt_attn           causal attention over packed prompts (bf16 K/V)
+ *
+ * A page holds bs = 16 tokens of one layer, all KV heads:
+ *   kv_pages  device e4m3 [n_pages][Hkv][2][bs][d]   [..][0] keys, [..][1] values
+ *   kv_scale  device float [n_pages][Hkv][2]         value = e4m3 * scale
+ * A scale is a power of two, 2^e with e in [-60, 119]: the format's relative
+ * precision does not depend on it, and moving a page to a larger scale is exact
+ * but for values that become subnormal.  e is the least one with
+ * amax <= 448 * 2^e, amax over the page's tokens of that head's keys (values).
+ *   block_table  device int32 [B][nb_max]   page of request b's block x (tokens
+ *                16x .. 16x+15), the same for every layer and head; entries of
+ *                blocks past the request's length are never read
+ *
+ * Shape (oasis_paged_shape):
+ *   B        requests (rows of the table)      (1 .. 65535)
+ *   Hq       query heads, Hq = G * Hkv, G in 1 .. 8
+ *   Hkv      KV heads                          B * Hkv <= 2^20
+ *   d, bs    must be 128 and 16
+ *   nb_max   blocks per request                (1 .. 2^24)
+ *   n_pages  pages of one layer's pool         (1 .. 2^27 - 1)
+ * Row strides are in elements, between consecutive tokens (requests); heads and
+ * dimensions are contiguous inside a row, and rows start on 16-byte boundaries,
+ * so slices of a fused projection's buffer can be passed as they are.
+ */
+typedef struct oasis_paged_shape {
+  int32_t B, Hq, Hkv, d, bs, nb_max, n_pages;
+} oasis_paged_shape;
+
+/*
+ * Block tables and slots of new tokens, from lengths on the GPU.
+ *   Request b grows from old_len[b] to new_len[b] tokens; it needs
+ *   need_b = ceil(new_len[b]/bs) - ceil(old_len[b]/bs) pages.  Pages are taken
+ *   from the end of the free list in request order: the k-th page of the call is
+ *   free_pages[n_free - 1 - k].  The new tokens of all requests form rows in
+ *   (request, position) order; slot_map[row] = page * bs + position % bs.
+ *   A request gets nothing - its rows' slots are -1, its table entries stay, and
+ *   len_out[b] = old_len[b] - when its pages are not all there (need_b > 0 and the
+ *   running total of need passes *n_free: OASIS_EW_NO_SLOT), when its rows do not
+ *   fit in n_rows, or when its lengths are bad (OASIS_EW_BAD_COUNT; need
+ *   0 <= old_len <= new_len <= nb_max*bs; such a request has no rows).
+ * Arguments:
+ *   old_len, new_len  device int32 [B]
+ *   free_pages  device int32 [n_pages]; entries 0 .. *n_free - 1 are free pages
+ *               (read only).  A listed page outside [0, n_pages) gives -1 in the
+ *               table and in the slots, and OASIS_EW_BAD_BLOCK.
+ *   n_free      device int32 [1]
+ *   block_table device int32 [B][nb_max]     in/out: new blocks' entries written
+ *   len_out     device int32 [B]             out: lengths that the tables now hold
+ *   n_free_out  device int32 [1]             out
+ *   row_start   device int32 [B+1]           out: first row of each request, and
+ *               their number; rows of failed requests count
+ *   slot_map    device int32 [n_rows]        out; rows past row_start[B] get -1,
+ *               so a batch padded to a fixed size needs no other mask
+ *   err_word    device uint32 [1] or NULL
+ * len_out and n_free_out must not overlap the inputs: several thread blocks read
+ * those while one writes the outputs.  The inputs stay as they were, so a plan
+ * that is not taken costs nothing.
+ */
+OASIS_API oasis_status oasis_extend_tables(const oasis_paged_shape* shape, const int32_t* old_len,
+                                           const int32_t* new_len, const int32_t* free_pages,
+                                           const int32_t* n_free, int32_t* block_table,
+                                           int32_t* len_out, int32_t* n_free_out,
+                                           int32_t* row_start, int32_t* slot_map, int32_t n_rows,
+                                           uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Returns pages to the free list: request b keeps ceil(keep_len[b]/bs) of its
+ * ceil(len[b]/bs) blocks; the pages of the others are written to
+ * free_pages[*n_free ...] in (request, block) order, and n_free_out = *n_free +
+ * their number.  Table entries are left as they were (they lie past the length).
+ * 0 <= keep_len <= len <= nb_max*bs, else the request releases nothing and
+ * OASIS_EW_BAD_COUNT is set; pages that do not fit in the list (more than
+ * n_pages) are dropped with OASIS_EW_NO_SLOT; an entry outside [0, n_pages) is
+ * listed as -1 with OASIS_EW_BAD_BLOCK.  n_free_out must not be n_free.
+ */
+OASIS_API oasis_status oasis_release_tables(const oasis_paged_shape* shape, const int32_t* len,
+                                            const int32_t* keep_len, const int32_t* block_table,
+                                            int32_t* free_pages, const int32_t* n_free,
+                                            int32_t* n_free_out, uint32_t* err_word,
+                                            oasis_stream_t stream);
+
+/*
+ * Quantises K/V rows into their pages.  The rows of one page must be adjacent,
+ * in consecutive positions, and in one call no page may appear in two places (the
+ * order that oasis_extend_tables gives).  Positions of the page below the first
+ * new one are taken as held: if the new rows need a larger scale, those tokens
+ * are moved to it (rounded to nearest even); a page whose first new position is 0
+ * starts anew.  Positions above the last new one are not written.
+ *   k, v       device bf16, n_rows rows of [Hkv][d], strides k_stride, v_stride
+ *   slot_map   device int32 [n_rows]; -1 = the row is skipped; another slot
+ *              outside [0, n_pages*bs) is skipped with OASIS_EW_BAD_SLOT; a row
+ *              that is on its predecessor's page but not in the next position is
+ *              skipped with OASIS_EW_BAD_COUNT
+ *   kv_pages, kv_scale   one layer's, in/out
+ *   err_word   device uint32 [1] or NULL
+ * n_rows may be 0.  A non-finite input saturates the page's scale (e = 119).
+ */
+OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const void* k, size_t k_stride,
+                                         const void* v, size_t v_stride, const int32_t* slot_map,
+                                         int32_t n_rows, void* kv_pages, float* kv_scale,
+                                         uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Decode attention over the 8-bit pages.  With A_bh the blocks x < ceil(ctx/bs)
+ * of request b (sel NULL), or those that sel lists for (b, h), and query head
+ * hq = h*G + g:
+ *   out[b][hq] = sum over tokens t < ctx_len[b] of A_bh of softmax_t(scale * q.k_t) v_t,
+ *   or zero when A_bh has no valid token.
+ * Arguments:
+ *   q         device bf16, B rows of [Hq][d], stride q_stride
+ *   kv_pages, kv_scale, block_table   as above (read only)
+ *   ctx_len   device int32 [B]; clamped to [0, nb_max*bs]
+ *   sel, nsel device int32 [B][Hkv][sel_max], [B][Hkv], or both NULL: distinct
+ *             blocks in any order, as oasis_topk_select writes them (sel_max = its
+ *             Kb, 1 .. 65536).  nsel outside [0, sel_max] is clamped
+ *             (OASIS_EW_BAD_COUNT); a block outside the request is skipped
+ *             (OASIS_EW_BAD_BLOCK), a page outside the pool too (OASIS_EW_BAD_SLOT).
+ *   scale     softmax scale, > 0 and finite
+ *   workspace device scratch, 16-byte aligned, ws_bytes >=
+ *             oasis_paged_attn_workspace_bytes(shape); contents on entry are
+ *             ignored; calls that may overlap need different ones
+ *   out       device bf16 [B][Hq][d], 16-byte aligned: the activation type that the
+ *             output projection reads
+ *   err_word  device uint32 [1] or NULL
+ */
+OASIS_API size_t oasis_paged_attn_workspace_bytes(const oasis_paged_shape* shape);
+
+OASIS_API oasis_status oasis_paged_decode_attn_q8(const oasis_paged_shape* shape, const void* q,
+                                                  size_t q_stride, const void* kv_pages,
+                                                  const float* kv_scale, const int32_t* block_table,
+                                                  const int32_t* ctx_len, const int32_t* sel,
+                                                  const int32_t* nsel, int32_t sel_max, float scale,
+                                                  void* workspace, size_t ws_bytes, void* out,
+                                                  uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Causal attention over packed prompts.  Sequence b owns rows row_start[b] ..
+ * row_start[b+1] - 1; for row i of it and query head hq = h*G + g:
+ *   out[i][hq] = sum over rows j <= i of sequence b of softmax_j(scale * q_i.k_j) v_j.
+ * Rows that belong to no sequence are not written, and what they hold (NaN
+ * included) does not matter.
+ *   q, k, v    device bf16, n_rows rows of [Hq][d], [Hkv][d], [Hkv][d], with strides
+ *   row_start  device int32 [B+1], not decreasing, inside [0, n_rows] (the row_start
+ *              of oasis_extend_tables when every old_len is 0); a sequence that
+ *              breaks this is skipped with OASIS_EW_BAD_COUNT
+ *   n_rows     0 .. 2^28
+ *   scale      softmax scale, > 0 and finite
+ *   out        device bf16, n_rows rows of [Hq][d], stride out_stride
+ *   err_word   device uint32 [1] or NULL
+ * Only B, Hq, Hkv and d of the shape are used; the others are checked as for
+ * every call.
+ */
+OASIS_API oasis_status oasis_prompt_attn(const oasis_paged_shape* shape, const void* q, size_t q_stride,
+                                         const void* k, size_t k_stride, const void* v,
+                                         size_t v_stride, const int32_t* row_start, int32_t n_rows,
+                                         float scale, void* out, size_t out_stride,
+                                         uint32_t* err_word, oasis_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -46,7 +46,18 @@ class Shape(ctypes.Structure):
         return tuple(getattr(self, n) for n, _ in self._fields_)
 
 
+class PagedShape(ctypes.Structure):
+    """Sizes of a paged 8-bit cache (oasis_paged_shape)."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "d", "bs", "nb_max", "n_pages")]
+
+    @classmethod
+    def of(cls, B, Hq, Hkv, nb_max, n_pages, d=128, bs=16) -> "PagedShape":
+        return cls(B, Hq, Hkv, d, bs, nb_max, n_pages)
+
+
 _VP = ctypes.c_void_p
+_PS = ctypes.POINTER(PagedShape)
 _SIGS = {
     "oasis_version": ([], ctypes.c_char_p),
     "oasis_last_error": ([], ctypes.c_char_p),
@@ -92,6 +103,16 @@ _SIGS = {
                                           ctypes.c_float, _VP, _VP], ctypes.c_int),
     "oasis_append_kv": ([ctypes.POINTER(Shape), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32,
                          _VP, _VP], ctypes.c_int),
+    "oasis_extend_tables": ([_PS, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP],
+                            ctypes.c_int),
+    "oasis_release_tables": ([_PS, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], ctypes.c_int),
+    "oasis_store_kv_q8": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP, _VP, _VP, _VP],
+                          ctypes.c_int),
+    "oasis_paged_attn_workspace_bytes": ([_PS], ctypes.c_size_t),
+    "oasis_paged_decode_attn_q8": ([_PS, _VP, ctypes.c_size_t, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32,
+                                    ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP, _VP], ctypes.c_int),
+    "oasis_prompt_attn": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP,
+                           ctypes.c_int32, ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP], ctypes.c_int),
 }
 
 _lib = None
@@ -355,3 +376,49 @@ def oasis_sparse_decode_attn_noalloc(shape: Shape, q, k_pool, v_pool, sel, nsel,
     _check("oasis_sparse_decode_attn_noalloc", load().oasis_sparse_decode_attn_noalloc(
         ctypes.byref(shape), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(sel), _ptr(nsel),
         _ptr(blk2slot), _ptr(ctx_len), float(scale), _ptr(out), _stream(stream)))
+
+
+def oasis_extend_tables(shape: PagedShape, old_len, new_len, free_pages, n_free, block_table, len_out, n_free_out,
+                        row_start, slot_map, n_rows: int, err_word=None, stream=None):
+    """Pages for every request's new tokens (table entries), and each token's slot."""
+    _check("oasis_extend_tables", load().oasis_extend_tables(
+        ctypes.byref(shape), _ptr(old_len), _ptr(new_len), _ptr(free_pages), _ptr(n_free), _ptr(block_table),
+        _ptr(len_out), _ptr(n_free_out), _ptr(row_start), _ptr(slot_map), n_rows, _ptr(err_word), _stream(stream)))
+
+
+def oasis_release_tables(shape: PagedShape, length, keep_len, block_table, free_pages, n_free, n_free_out,
+                         err_word=None, stream=None):
+    """The pages of blocks past keep_len go back to the free list."""
+    _check("oasis_release_tables", load().oasis_release_tables(
+        ctypes.byref(shape), _ptr(length), _ptr(keep_len), _ptr(block_table), _ptr(free_pages), _ptr(n_free),
+        _ptr(n_free_out), _ptr(err_word), _stream(stream)))
+
+
+def oasis_store_kv_q8(shape: PagedShape, k, k_stride: int, v, v_stride: int, slot_map, n_rows: int, kv_pages,
+                      kv_scale, err_word=None, stream=None):
+    """bf16 K/V rows into 8-bit pages with one power-of-two scale per page, head and K or V."""
+    _check("oasis_store_kv_q8", load().oasis_store_kv_q8(
+        ctypes.byref(shape), _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slot_map), n_rows, _ptr(kv_pages),
+        _ptr(kv_scale), _ptr(err_word), _stream(stream)))
+
+
+def oasis_paged_attn_workspace_bytes(shape: PagedShape) -> int:
+    return int(load().oasis_paged_attn_workspace_bytes(ctypes.byref(shape)))
+
+
+def oasis_paged_decode_attn_q8(shape: PagedShape, q, q_stride: int, kv_pages, kv_scale, block_table, ctx_len, sel,
+                               nsel, sel_max: int, scale: float, workspace, ws_bytes: int, out, err_word=None,
+                               stream=None):
+    """Attention of one query token per request over its 8-bit pages (sel/nsel None: all of them)."""
+    _check("oasis_paged_decode_attn_q8", load().oasis_paged_decode_attn_q8(
+        ctypes.byref(shape), _ptr(q), q_stride, _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len),
+        _ptr(sel), _ptr(nsel), sel_max, scale, _ptr(workspace), ws_bytes, _ptr(out), _ptr(err_word),
+        _stream(stream)))
+
+
+def oasis_prompt_attn(shape: PagedShape, q, q_stride: int, k, k_stride: int, v, v_stride: int, row_start,
+                      n_rows: int, scale: float, out, out_stride: int, err_word=None, stream=None):
+    """Causal attention over packed prompts (bf16 in and out)."""
+    _check("oasis_prompt_attn", load().oasis_prompt_attn(
+        ctypes.byref(shape), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(row_start), n_rows, scale,
+        _ptr(out), out_stride, _ptr(err_word), _stream(stream)))

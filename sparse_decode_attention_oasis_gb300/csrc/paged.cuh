@@ -1,0 +1,43 @@
+// Types and device helpers shared by the paged 8-bit cache's kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace oasis {
+
+struct PagedShape {
+  int B, Hq, Hkv, nb_max, n_pages;
+  __host__ __device__ int G() const { return Hq / Hkv; }
+};
+
+// Exponent range of a page's scale 2^e (what amax <= 448 * 2^e needs for any
+// finite bf16 is at most 119; below -60 a page's values are as good as zero).
+constexpr int kScaleELow = -60, kScaleEHigh = 119;
+constexpr long long kHeadPageBytes = 2LL * kBS * kD;  // keys and values of one head in one page
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
+
+// Two e4m3 (low 16 bits of w) -> two halves, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Two floats -> two e4m3 (round to nearest even, saturating); lo in bits 0..7.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void set_err(unsigned* err, unsigned bits) {
+  if (err != nullptr && bits) atomicOr(err, bits);
+}
+
+}  // namespace oasis

@@ -1,0 +1,500 @@
+// Decode attention over 8-bit pages (oasis_paged_decode_attn_q8).
+//
+// Mathematics: a softmax over tokens with a running reference M, one per query
+// row: w_t = 2^(c s_t + lv_t - M), o = sum w_t v8_t / sum w_t 2^-lv_t, where
+// s_t = q . k8_t * 2^lk_t, lk and lv the exponents of the page's key and value scale
+// and c = scale * log2(e).  Taking lv into the exponent keeps the weights of pages
+// with different scales inside one fp16 range; M moves only when a score passes it
+// by more than 2^8, so most pages need no rescaling of the accumulators.
+//
+// Work: one warp takes one page (16 tokens of one KV head) at a time, straight from
+// global memory into mma.sync fragments, without shared memory:
+//   S^T[16 tokens x 8 rows]  = K[16 x 128] Q^T       8 x m16n8k16, K the A operand
+//   O^T[128 dims x 8 rows]  += V^T[128 x 16] W^T     8 x m16n8k16, V^T the A operand
+// The query rows are the narrow side (n = 8 >= G), so nothing is padded to 16 rows.
+// The order of dimensions inside a fragment is free as long as both operands share
+// it: a lane's 16-byte loads are its fragments' dimensions, every load instruction
+// covers whole 32-byte sectors, and V's pairs of tokens need one byte permute each.
+// e4m3 converts to fp16 exactly; q is scaled by a power of two for each row so that
+// its largest value lies in [2^14, 2^15), then converts to fp16 without rounding
+// (bf16 has 8 significant bits, fp16 11; values 2^29 below the row's largest lose
+// bits, 2^-40 of the score).  Roundings: w to fp16 (2^-12 each) for the product
+// with V, the output to bf16 (2^-9 of its value, which dominates); s, w, the sums and
+// the accumulators are fp32.
+//
+// Split: the pages of all (request, KV head) pairs form one sequence, cut into equal
+// ranges for the thread blocks and again for their warps, whatever the lengths are.
+// A warp writes a pair that lies wholly inside its range; pieces are joined in shared
+// memory, and pieces of pairs that cross thread blocks by a second kernel from the
+// workspace (two pieces at most for each block, so its size does not depend on the
+// context).  Bound: HBM, 4 KiB + 8 B for a page and head.
+#include "paged.cuh"
+
+namespace oasis {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCtasPerSm = 2;
+constexpr int kMinPages = 16;  // pages a thread block gets at least, when there are so few
+constexpr int kRowFloats = kD + 2;
+constexpr float kSlack = 8.0f;  // log2 of the largest weight
+
+struct Args {
+  const uint16_t* q;
+  size_t q_stride;
+  const uint8_t* pages;
+  const float* scales;
+  const int* table;
+  const int* ctx_len;
+  const int* sel;
+  const int* nsel;
+  int sel_max;
+  float scale_log2;
+  float* parts;  // [grid][2][G][kRowFloats]
+  int2* tails;   // [grid]: the pair whose first piece is a block's tail (-1: none), its last block
+  uint16_t* out;
+  unsigned* err;
+};
+
+__device__ __forceinline__ void mma_f16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Pages of pair e = b * Hkv + h.
+__device__ __forceinline__ int pair_pages(const PagedShape& s, const Args& a, int e, unsigned* bits) {
+  if (a.sel == nullptr) return clamp_nb(a.ctx_len[e / s.Hkv], s.nb_max);
+  const int n = a.nsel[e];
+  if (n < 0 || n > a.sel_max) {
+    *bits |= OASIS_EW_BAD_COUNT;
+    return n < 0 ? 0 : a.sel_max;
+  }
+  return n;
+}
+
+// The running state of one warp: rows r0 = 2 (lane % 4) and r0 + 1, dimensions
+// 16 (lane / 4) .. + 15 (acc[m][0], [2] and [1], [3]: dimensions 2m, 2m + 1 of the rows).
+struct State {
+  float acc[8][4];
+  float top[2];  // M
+  float sum[2];  // this lane's tokens only
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    top[0] = top[1] = neg_inf();
+    sum[0] = sum[1] = 0.f;
+  }
+};
+
+struct Rows {  // a lane's 16-byte pieces of a page's keys and values
+  uint4 v[4];
+};
+
+// Keys: rows lane / 4 and + 8, dimensions 16 (lane % 4) .. and 64 + 16 (lane % 4) ..
+__device__ __forceinline__ void load_keys(Rows& k, const uint8_t* page, int lane) {
+  const uint8_t* p = page + (lane >> 2) * kD + (lane & 3) * 16;
+  k.v[0] = ldg_stream(p);
+  k.v[1] = ldg_stream(p + 64);
+  k.v[2] = ldg_stream(p + 8 * kD);
+  k.v[3] = ldg_stream(p + 8 * kD + 64);
+}
+
+// Values: tokens 2 (lane % 4), + 1, + 8, + 9, dimensions 16 (lane / 4) ..
+__device__ __forceinline__ void load_values(Rows& v, const uint8_t* page, int lane) {
+  const uint8_t* p = page + kBS * kD + (lane & 3) * 2 * kD + (lane >> 2) * 16;
+  v.v[0] = ldg_stream(p);
+  v.v[1] = ldg_stream(p + kD);
+  v.v[2] = ldg_stream(p + 8 * kD);
+  v.v[3] = ldg_stream(p + 9 * kD);
+}
+
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+paged_decode_attn_kernel(PagedShape s, Args a) {
+  extern __shared__ float slots[];  // [kWarps][2][G][kRowFloats]
+  __shared__ long long chunk_start[kThreads];
+  __shared__ long long warp_sums[kWarps];
+  __shared__ long long slot_lo[kWarps][2], slot_hi[kWarps][2];
+  __shared__ int slot_pair[kWarps][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = s.Hq / s.Hkv;
+  const int pairs = s.B * s.Hkv;
+  const int per = (pairs + kThreads - 1) / kThreads;
+  unsigned bits = 0;
+
+  // prefix of the pairs' pages; pairs without pages get their zero rows here
+  long long n = 0;
+  for (int e = min(tid * per, pairs); e < min((tid + 1) * per, pairs); ++e) {
+    const int c = pair_pages(s, a, e, &bits);
+    n += c;
+    if (c == 0 && e % (int)gridDim.x == (int)blockIdx.x)
+      for (int i = 0; i < G * kD / 8; ++i)
+        reinterpret_cast<uint4*>(a.out + (long long)e * G * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  long long x = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  if (lane < 2) slot_pair[warp][lane] = -1;
+  __syncthreads();
+  long long total = 0, off = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    off += w < warp ? warp_sums[w] : 0;
+    total += warp_sums[w];
+  }
+  chunk_start[tid] = off + x - n;
+  __syncthreads();
+  const long long wanted = (total + kMinPages - 1) / kMinPages;
+  const int blocks = wanted < (long long)gridDim.x ? (int)wanted : (int)gridDim.x;
+  if ((int)blockIdx.x >= blocks) {
+    if (tid == 0) a.tails[blockIdx.x] = make_int2(-1, 0);
+    if (blockIdx.x == 0) set_err(a.err, bits);
+    return;
+  }
+  const long long c_lo = blockIdx.x * total / blocks, c_hi = (blockIdx.x + 1) * total / blocks;
+  const long long w_lo = c_lo + warp * (c_hi - c_lo) / kWarps, w_hi = c_lo + (warp + 1) * (c_hi - c_lo) / kWarps;
+
+  if (w_lo < w_hi) {
+    // the pair that holds page w_lo: the last chunk of pairs that starts at or before it, then a walk
+    int i = 0, j = kThreads - 1;
+    while (i < j) {
+      const int m = (i + j + 1) >> 1;
+      if (chunk_start[m] <= w_lo) i = m; else j = m - 1;
+    }
+    int e = i * per;
+    long long e_lo = chunk_start[i];
+    int count = pair_pages(s, a, e, &bits);
+    while (e_lo + count <= w_lo) {
+      e_lo += count;
+      count = pair_pages(s, a, ++e, &bits);
+    }
+    long long p = w_lo;
+    while (true) {
+      const int b = e / s.Hkv, h = e - b * s.Hkv;
+      const int ctx = (int)min((long long)max(a.ctx_len[b], 0), (long long)s.nb_max * kBS);
+      const int nb = (ctx + kBS - 1) / kBS;
+      const int first = (int)(p - e_lo), last = (int)min((long long)count, w_hi - e_lo);  // pages of the pair
+
+      // ---- the query rows, lane / 4 their number
+      uint32_t qf[16];
+      float fac[2];
+      {
+        const int g = lane >> 2;
+        uint4 w[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
+        if (g < G) {
+          const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + g) * kD + (lane & 3) * 16;
+          w[0] = ldg_nc(src);
+          w[1] = ldg_nc(src + 8);
+          w[2] = ldg_nc(src + 64);
+          w[3] = ldg_nc(src + 72);
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t v = word(w[c], d) & 0x7fff7fffu;
+            m = max(m, max(v & 0xffffu, v >> 16));
+          }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int ex = max((int)(m >> 7) - 127, -112);  // exponent of the row's largest value
+        const float f = pow2f(14 - ex);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t v = word(w[c >> 2], c & 3);
+          qf[c] = pack_f16x2(bf_lo(v) * f, bf_hi(v) * f);
+        }
+        const float mine = a.scale_log2 * pow2f(ex - 14);
+        fac[0] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8);
+        fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
+      }
+
+      State st;
+      st.clear();
+      Rows kr, vr;
+      int my_page = -1, my_valid = 0;  // of page (group of 32) + lane
+      float2 my_scale = make_float2(1.f, 1.f);
+      const long long head_stride = kHeadPageBytes;
+      auto lookup = [&](int at) {  // tables of pages at .. at + 31
+        my_page = -1;
+        my_valid = 0;
+        const int idx = at + lane;
+        if (idx < last) {
+          int blk = idx;
+          if (a.sel != nullptr) {
+            blk = a.sel[(long long)e * a.sel_max + idx];
+            if (blk < 0 || blk >= nb) {
+              blk = -1;
+              bits |= OASIS_EW_BAD_BLOCK;
+            }
+          }
+          if (blk >= 0) {
+            const int pg = a.table[(long long)b * s.nb_max + blk];
+            if (pg >= 0 && pg < s.n_pages) {
+              my_page = pg;
+              my_valid = min(kBS, ctx - blk * kBS);
+              my_scale = *reinterpret_cast<const float2*>(a.scales + ((long long)pg * s.Hkv + h) * 2);
+            } else {
+              bits |= OASIS_EW_BAD_SLOT;
+            }
+          }
+        }
+      };
+      auto head_page = [&](int page) { return a.pages + ((long long)page * s.Hkv + h) * head_stride; };
+
+      lookup(first);
+      int page = __shfl_sync(0xffffffffu, my_page, 0);
+      if (page >= 0) {
+        load_keys(kr, head_page(page), lane);
+        load_values(vr, head_page(page), lane);
+      }
+      for (int at = first; at < last; ++at) {
+        const int in = (at - first) & 31;
+        const int valid = __shfl_sync(0xffffffffu, my_valid, in);
+        const float ks = __shfl_sync(0xffffffffu, my_scale.x, in), vs = __shfl_sync(0xffffffffu, my_scale.y, in);
+        const bool here = page >= 0;
+        if (in == 31) lookup(at + 1);
+        page = at + 1 < last ? __shfl_sync(0xffffffffu, my_page, (at + 1 - first) & 31) : -1;
+        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (here) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const uint32_t lo = word(kr.v[m >> 2], m & 3), hi = word(kr.v[2 + (m >> 2)], m & 3);
+            mma_f16_16816(sc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_hi_to_f16x2(lo),
+                          e4m3x2_hi_to_f16x2(hi), qf[2 * m], qf[2 * m + 1]);
+          }
+        }
+        if (page >= 0) load_keys(kr, head_page(page), lane);
+        if (here) {
+          const int g = lane >> 2;
+          const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 0xff) - 127);
+          const float f0 = fac[0] * ks, f1 = fac[1] * ks;
+          float s0 = fmaf(sc[0], f0, lv), s1 = fmaf(sc[1], f1, lv);
+          float s2 = fmaf(sc[2], f0, lv), s3 = fmaf(sc[3], f1, lv);
+          if (valid < kBS) {
+            if (g >= valid) s0 = s1 = neg_inf();
+            if (g + 8 >= valid) s2 = s3 = neg_inf();
+            // what lies behind the last token may be NaN: zero times it is not zero
+            const int t = (lane & 3) * 2;
+            if (t >= valid) vr.v[0] = make_uint4(0u, 0u, 0u, 0u);
+            if (t + 1 >= valid) vr.v[1] = make_uint4(0u, 0u, 0u, 0u);
+            if (t + 8 >= valid) vr.v[2] = make_uint4(0u, 0u, 0u, 0u);
+            if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          float m0 = fmaxf(s0, s2), m1 = fmaxf(s1, s3);
+          if (__any_sync(0xffffffffu, m0 > st.top[0] + kSlack || m1 > st.top[1] + kSlack)) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+              m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+            }
+            const float n0 = fmaxf(st.top[0], m0), n1 = fmaxf(st.top[1], m1);
+            const float c0 = st.top[0] == neg_inf() ? 0.f : exp2f(st.top[0] - n0);
+            const float c1 = st.top[1] == neg_inf() ? 0.f : exp2f(st.top[1] - n1);
+            st.top[0] = n0;
+            st.top[1] = n1;
+            st.sum[0] *= c0;
+            st.sum[1] *= c1;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              st.acc[m][0] *= c0;
+              st.acc[m][1] *= c1;
+              st.acc[m][2] *= c0;
+              st.acc[m][3] *= c1;
+            }
+          }
+          const float r0 = st.top[0] == neg_inf() ? 0.f : st.top[0], r1 = st.top[1] == neg_inf() ? 0.f : st.top[1];
+          const float w0 = exp2f(s0 - r0), w1 = exp2f(s1 - r1), w2 = exp2f(s2 - r0), w3 = exp2f(s3 - r1);
+          const float iv = pow2f(-(int)lv);
+          st.sum[0] = fmaf(w0 + w2, iv, st.sum[0]);
+          st.sum[1] = fmaf(w1 + w3, iv, st.sum[1]);
+          const uint32_t b0 = transpose_8x8(pack_f16x2(w0, w1)), b1 = transpose_8x8(pack_f16x2(w2, w3));
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t t0 = word(vr.v[0], m), t1 = word(vr.v[1], m), t8 = word(vr.v[2], m), t9 = word(vr.v[3], m);
+            const uint32_t p0 = __byte_perm(t0, t1, 0x5140), p1 = __byte_perm(t8, t9, 0x5140);
+            const uint32_t p2 = __byte_perm(t0, t1, 0x7362), p3 = __byte_perm(t8, t9, 0x7362);
+            mma_f16_16816(st.acc[2 * m], e4m3x2_to_f16x2(p0), e4m3x2_hi_to_f16x2(p0), e4m3x2_to_f16x2(p1),
+                          e4m3x2_hi_to_f16x2(p1), b0, b1);
+            mma_f16_16816(st.acc[2 * m + 1], e4m3x2_to_f16x2(p2), e4m3x2_hi_to_f16x2(p2), e4m3x2_to_f16x2(p3),
+                          e4m3x2_hi_to_f16x2(p3), b0, b1);
+          }
+        }
+        if (page >= 0) load_values(vr, head_page(page), lane);
+      }
+
+      // ---- the pair's piece: the output if it is all of it, else a slot
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        st.sum[0] += __shfl_xor_sync(0xffffffffu, st.sum[0], o);
+        st.sum[1] += __shfl_xor_sync(0xffffffffu, st.sum[1], o);
+      }
+      const bool whole = first == 0 && last == count;
+      const int which = first == 0 ? 1 : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = (lane & 3) * 2 + i;
+        if (r >= G) continue;
+        if (whole) {
+          const float inv = st.sum[i] > 0.f ? 1.0f / st.sum[i] : 0.f;
+          uint32_t w[8];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(st.acc[m][i] * inv, st.acc[m][2 + i] * inv);
+          uint4* dst = reinterpret_cast<uint4*>(a.out + ((long long)e * G + r) * kD + (lane >> 2) * 16);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+          float* row = slots + ((warp * 2 + which) * G + r) * kRowFloats;
+#pragma unroll
+          for (int m = 0; m < 8; ++m)
+            *reinterpret_cast<float2*>(row + (lane >> 2) * 16 + 2 * m) = make_float2(st.acc[m][i], st.acc[m][2 + i]);
+          if (lane < 4) *reinterpret_cast<float2*>(row + kD) = make_float2(st.top[i], st.sum[i]);
+        }
+      }
+      if (!whole && lane == 0) {
+        slot_pair[warp][which] = e;
+        slot_lo[warp][which] = e_lo;
+        slot_hi[warp][which] = e_lo + count;
+      }
+      p = e_lo + last;
+      if (p >= w_hi) break;
+      do {
+        e_lo += count;
+        count = pair_pages(s, a, ++e, &bits);
+      } while (count == 0);
+    }
+  }
+  set_err(a.err, bits);
+  __syncthreads();
+
+  // ---- join the warps' pieces of a pair
+  int2 tail = make_int2(-1, 0);
+  for (int i = 0; i < 2 * kWarps;) {
+    const int e = slot_pair[i >> 1][i & 1];
+    if (e < 0) {
+      ++i;
+      continue;
+    }
+    int end = i + 1;
+    while (end < 2 * kWarps && (slot_pair[end >> 1][end & 1] == e || slot_pair[end >> 1][end & 1] < 0)) ++end;
+    const long long e_lo = slot_lo[i >> 1][i & 1], e_hi = slot_hi[i >> 1][i & 1];
+    const bool whole = e_lo >= c_lo && e_hi <= c_hi;
+    float* part = a.parts + ((long long)blockIdx.x * 2 + (e_lo >= c_lo ? 1 : 0)) * G * kRowFloats;
+    for (int idx = tid; idx < G * (kD / 2); idx += kThreads) {
+      const int r = idx / (kD / 2), d = idx % (kD / 2) * 2;
+      float top = neg_inf();
+      for (int j = i; j < end; ++j)
+        if (slot_pair[j >> 1][j & 1] == e) top = fmaxf(top, slots[(j * G + r) * kRowFloats + kD]);
+      float sum = 0.f, o0 = 0.f, o1 = 0.f;
+      if (top != neg_inf()) {
+        for (int j = i; j < end; ++j) {
+          if (slot_pair[j >> 1][j & 1] != e) continue;
+          const float* row = slots + (j * G + r) * kRowFloats;
+          const float f = exp2f(row[kD] - top);
+          sum = fmaf(f, row[kD + 1], sum);
+          o0 = fmaf(f, row[d], o0);
+          o1 = fmaf(f, row[d + 1], o1);
+        }
+      }
+      if (whole) {
+        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        *reinterpret_cast<uint32_t*>(a.out + ((long long)e * G + r) * kD + d) = pack_bf16x2(o0 * inv, o1 * inv);
+      } else {
+        *reinterpret_cast<float2*>(part + r * kRowFloats + d) = make_float2(o0, o1);
+        if (d == 0) *reinterpret_cast<float2*>(part + r * kRowFloats + kD) = make_float2(top, sum);
+      }
+    }
+    if (e_lo >= c_lo && e_hi > c_hi) {
+      // its last piece is in the last block whose range starts before e_hi
+      tail = make_int2(e, (int)((e_hi * blocks + total - 1) / total - 1));
+    }
+    i = end;
+  }
+  if (tid == 0) a.tails[blockIdx.x] = tail;
+}
+
+// Joins the pieces of a pair that starts in block blockIdx.x and ends in a later one.
+__global__ void __launch_bounds__(kD)
+paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const int2* __restrict__ tails,
+                         uint16_t* __restrict__ out) {
+  const int2 t = tails[blockIdx.x];
+  if (t.x < 0) return;
+  const int G = s.Hq / s.Hkv;
+  const int first = blockIdx.x, d = threadIdx.x;
+  for (int r = 0; r < G; ++r) {
+    const float* row0 = parts + ((long long)first * 2 + 1) * G * kRowFloats + r * kRowFloats;
+    float top = row0[kD], sum = row0[kD + 1], o = row0[d];
+    for (int c = first + 1; c <= t.y; ++c) {
+      const float* row = parts + (long long)c * 2 * G * kRowFloats + r * kRowFloats;
+      const float m = row[kD];
+      if (m == neg_inf()) continue;
+      const float next = fmaxf(top, m);
+      const float f0 = top == neg_inf() ? 0.f : exp2f(top - next), f1 = exp2f(m - next);
+      o = fmaf(o, f0, row[d] * f1);
+      sum = fmaf(sum, f0, row[kD + 1] * f1);
+      top = next;
+    }
+    const float v = sum > 0.f ? o / sum : 0.f;
+    out[((long long)t.x * G + r) * kD + d] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
+  }
+}
+
+int most_blocks() { return kCtasPerSm * sm_count(); }
+
+}  // namespace
+
+size_t paged_attn_workspace_bytes(const PagedShape& s) {
+  const size_t n = (size_t)most_blocks();
+  return n * 2 * s.G() * kRowFloats * sizeof(float) + n * sizeof(int2);
+}
+
+cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint8_t* pages,
+                                     const float* scales, const int* table, const int* ctx, const int* sel,
+                                     const int* nsel, int sel_max, float scale, void* ws, uint16_t* out,
+                                     unsigned* err, cudaStream_t stream) {
+  const int most = most_blocks();
+  const long long pages_max = (long long)s.B * s.Hkv * (sel ? sel_max : s.nb_max);
+  const long long blocks = (pages_max + kMinPages - 1) / kMinPages;
+  const int grid = blocks < most ? (int)blocks : most;
+  float* parts = static_cast<float*>(ws);
+  Args a{q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, scale * 1.4426950408889634f, parts,
+         reinterpret_cast<int2*>(parts + (size_t)most * 2 * s.G() * kRowFloats), out, err};
+  const size_t smem = (size_t)kWarps * 2 * s.G() * kRowFloats * sizeof(float);
+  static int attr_cache[kMaxDevicesCached] = {};
+  cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel, smem, attr_cache);
+  if (e != cudaSuccess) return e;
+  paged_decode_attn_kernel<<<grid, kThreads, smem, stream>>>(s, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (grid > 1) paged_decode_join_kernel<<<grid, kD, 0, stream>>>(s, parts, a.tails, out);
+  return cudaGetLastError();
+}
+
+}  // namespace oasis

@@ -1,0 +1,225 @@
+"""A KV cache in 8-bit pages: tables, store, decode attention, and the prompt's attention.
+
+PyTorch owns the memory and the streams; every step runs in liboasis.so through
+:mod:`binding`.  One :class:`PagedKV` serves a model of several layers whose requests
+share the tables:
+
+  kv     uint8   [layers][n_pages][Hkv][2][16][128]   e4m3 keys, values
+  scale  float32 [layers][n_pages][Hkv][2]            powers of two
+  table  int32   [batch][nb_max]                      page of each request's blocks
+  free   int32   [n_pages]                            free pages, the first n_free of them
+  lens   int32   [batch]                              tokens that each request holds
+  err    int32   [1]                                  error word (OASIS_EW_* bits)
+
+A prompt's pass, layer by layer, and a decode step::
+
+    plan = cache.extend(lens, n_rows)                  # pages and slots of the new tokens
+    out = prompt_attn(q, k, v, plan.row_start)         # requests that held nothing before
+    cache.store(k, v, plan.slot_map, layer)
+    cache.commit(plan)
+    ...
+    plan = cache.extend(cache.lens + 1, batch)
+    cache.store(k, v, plan.slot_map, layer)
+    out = cache.decode(q, plan.lens, layer)            # sel, nsel: only the selected blocks
+    cache.commit(plan)
+
+Calls run on the current stream of the tensors' device and can be captured into a CUDA
+graph; nothing is kept between calls but the tensors above.  Scratch comes from
+PyTorch's allocator in each call, so calls on two streams, and two captured graphs, never
+share it.
+"""
+from __future__ import annotations
+
+import contextlib
+import math
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import binding as B
+
+D = 128
+BS = 16
+_SCALE = 1.0 / math.sqrt(D)
+
+
+class Plan(NamedTuple):
+    """What :meth:`PagedKV.extend` gives: it takes effect with :meth:`PagedKV.commit`."""
+
+    lens: torch.Tensor       # int32 [batch]: lengths that the tables now hold
+    n_free: torch.Tensor     # int32 [1]
+    row_start: torch.Tensor  # int32 [batch + 1]: first new row of each request
+    slot_map: torch.Tensor   # int32 [n_rows]: page * 16 + position, -1 for rows of no request
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _device(t: torch.Tensor):
+    """The context in which t's device is the current one."""
+    if not t.is_cuda:
+        raise ValueError("CUDA tensors are needed (there is no CPU path)")
+    return _NO_GUARD if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _rows(name: str, t: torch.Tensor, heads: int, n: int, device) -> int:
+    """Checks bf16 rows [n][heads][128], contiguous inside a row; returns the row stride."""
+    if t.dtype is not torch.bfloat16 or t.shape != (n, heads, D) or t.device != device:
+        raise ValueError(f"{name} must be bfloat16 [{n}, {heads}, {D}] on {device}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+    stride, inner, one = t.stride()
+    if n <= 1:
+        stride = heads * D
+    if one != 1 or (inner != D and heads > 1) or stride < heads * D or stride % 8:
+        raise ValueError(f"{name}: a row's heads and dimensions must be contiguous, rows a multiple of 8 elements "
+                         f"and at least {heads * D} apart (strides {t.stride()})")
+    return stride
+
+
+def _ints(name: str, t: torch.Tensor, shape, device) -> torch.Tensor:
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
+    return t
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
+                scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                err: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention over packed prompts: q [rows, Hq, 128], k and v [rows, Hkv, 128] in
+    bf16 (slices of one buffer as well), sequence b in rows row_start[b] .. row_start[b+1] - 1.
+    Rows of no sequence are left as they are in out (zero where out is allocated here)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [rows, heads, 128]")
+    n, hq, hkv, device = q.shape[0], q.shape[1], k.shape[1], q.device
+    with _device(q):
+        strides = [_rows("q", q, hq, n, device), _rows("k", k, hkv, n, device), _rows("v", v, hkv, n, device)]
+        if row_start.dim() != 1 or row_start.shape[0] < 2:
+            raise ValueError("row_start must be int32 [sequences + 1]")
+        _ints("row_start", row_start, row_start.shape, device)
+        if err is not None:
+            _ints("err", err, (1,), device)
+        if out is None:
+            out = torch.zeros((n, hq, D), dtype=torch.bfloat16, device=device)
+        out_stride = _rows("out", out, hq, n, device)
+        shape = B.PagedShape(row_start.shape[0] - 1, hq, hkv, D, BS, 1, 1)
+        B.oasis_prompt_attn(shape, q, strides[0], k, strides[1], v, strides[2], row_start, n,
+                            _SCALE if scale is None else float(scale), out, out_stride, err)
+    return out
+
+
+class PagedKV:
+    def __init__(self, n_pages: int, batch: int, nb_max: int, n_q_heads: int, n_kv_heads: int, layers: int = 1,
+                 device="cuda"):
+        self.shape = B.PagedShape.of(batch, n_q_heads, n_kv_heads, nb_max, n_pages)
+        self.ws_bytes = B.oasis_paged_attn_workspace_bytes(self.shape)  # also checks the shape
+        if not self.ws_bytes:
+            raise B.OasisError("oasis_paged_attn_workspace_bytes", 1, B.oasis_last_error())
+        if layers < 1:
+            raise ValueError("layers must be >= 1")
+        self.batch, self.n_q_heads, self.n_kv_heads, self.layers = batch, n_q_heads, n_kv_heads, layers
+        self.kv = torch.zeros((layers, n_pages, n_kv_heads, 2, BS, D), dtype=torch.uint8, device=device)
+        self.scale = torch.ones((layers, n_pages, n_kv_heads, 2), dtype=torch.float32, device=device)
+        self.table = torch.full((batch, nb_max), -1, dtype=torch.int32, device=device)
+        self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 is taken first
+        self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = self.kv.device
+
+    def adopt(self, **tensors: torch.Tensor) -> None:
+        """Use the caller's tensors in place of kv, scale, table, free, n_free or lens (same
+        shape, type and device): a pool that the program owns already, or a saved state."""
+        for name, t in tensors.items():
+            if name not in ("kv", "scale", "table", "free", "n_free", "lens"):
+                raise ValueError(f"no tensor {name}")
+            mine = getattr(self, name)
+            if t.dtype != mine.dtype or t.shape != mine.shape or t.device != mine.device or not t.is_contiguous() \
+                    or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be contiguous, 16-byte aligned {mine.dtype} {tuple(mine.shape)} on "
+                                 f"{mine.device}")
+        for name, t in tensors.items():
+            setattr(self, name, t)
+
+    def extend(self, new_len: torch.Tensor, n_rows: int) -> Plan:
+        """Pages for requests that grow to new_len tokens and slots for their new rows (at most
+        n_rows).  Only new table entries are written: lens and n_free change with commit."""
+        b = self.batch
+        _ints("new_len", new_len, (b,), self.device)
+        n_rows = int(n_rows)
+        if n_rows < 0:
+            raise ValueError("n_rows must be >= 0")
+        with _device(new_len):
+            buf = torch.empty(2 * b + 2 + n_rows, dtype=torch.int32, device=self.device)
+            plan = Plan(buf[:b], buf[b:b + 1], buf[b + 1:2 * b + 2], buf[2 * b + 2:])
+            at = buf.data_ptr()
+            B.oasis_extend_tables(self.shape, self.lens, new_len, self.free, self.n_free, self.table, at, at + 4 * b,
+                                  at + 4 * (b + 1), at + 4 * (2 * b + 2), n_rows, self.err)
+        return plan
+
+    def commit(self, plan: Plan) -> None:
+        """The plan's lengths and free count become the cache's."""
+        with _device(self.lens):
+            self.lens.copy_(plan.lens)
+            self.n_free.copy_(plan.n_free)
+
+    def release(self, keep_len: torch.Tensor) -> None:
+        """Requests keep their first keep_len tokens (0: the request is done); the pages of the
+        others are free again."""
+        _ints("keep_len", keep_len, (self.batch,), self.device)
+        with _device(keep_len):
+            left = torch.empty_like(self.n_free)
+            B.oasis_release_tables(self.shape, self.lens, keep_len, self.table, self.free, self.n_free, left, self.err)
+            self.n_free.copy_(left)
+            kept = (keep_len >= 0) & (keep_len <= self.lens)  # the others released nothing
+            self.lens.copy_(torch.where(kept, keep_len, self.lens))
+
+    def store(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, layer: int = 0) -> None:
+        """Rows k, v [rows, Hkv, 128] (bf16) into the layer's pages at slot_map's slots."""
+        n, h = slot_map.shape[0], self.n_kv_heads
+        ks, vs = _rows("k", k, h, n, self.device), _rows("v", v, h, n, self.device)
+        _ints("slot_map", slot_map, (n,), self.device)
+        with _device(k):
+            B.oasis_store_kv_q8(self.shape, k, ks, v, vs, slot_map, n, self._layer(self.kv, layer),
+                                self._layer(self.scale, layer), self.err)
+
+    def decode(self, q: torch.Tensor, ctx_len: Optional[torch.Tensor] = None, layer: int = 0,
+               sel: Optional[torch.Tensor] = None, nsel: Optional[torch.Tensor] = None,
+               scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Attention of q [batch, Hq, 128] (bf16) over the first ctx_len tokens of every request
+        (lens by default), or over the blocks that sel [batch, Hkv, most], nsel [batch, Hkv] list."""
+        b, hq, device = self.batch, self.n_q_heads, self.device
+        stride = _rows("q", q, hq, b, device)
+        ctx_len = _ints("ctx_len", self.lens if ctx_len is None else ctx_len, (b,), device)
+        most = 0
+        if sel is not None or nsel is not None:
+            if sel is None or nsel is None or sel.dim() != 3:
+                raise ValueError("sel [batch, Hkv, most] and nsel [batch, Hkv] must be given together")
+            most = sel.shape[2]
+            _ints("sel", sel, (b, self.n_kv_heads, most), device)
+            _ints("nsel", nsel, (b, self.n_kv_heads), device)
+        with _device(q):
+            if out is None:
+                out = torch.empty((b, hq, D), dtype=torch.bfloat16, device=device)
+            elif out.dtype is not torch.bfloat16 or out.shape != (b, hq, D) or out.device != device \
+                    or not out.is_contiguous():
+                raise ValueError(f"out must be contiguous bfloat16 [{b}, {hq}, {D}] on {device}")
+            ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+            B.oasis_paged_decode_attn_q8(self.shape, q, stride, self._layer(self.kv, layer),
+                                         self._layer(self.scale, layer), self.table, ctx_len, sel, nsel, most,
+                                         _SCALE if scale is None else float(scale), ws, self.ws_bytes, out, self.err)
+        return out
+
+    def check(self) -> None:
+        """Waits for the device and raises if a kernel reported an error; clears the word."""
+        bits = int(self.err.item())
+        if bits:
+            self.err.zero_()
+            names = [n for n in ("BAD_BLOCK", "BAD_SLOT", "NO_SLOT", "BAD_COUNT", "TIMEOUT")
+                     if bits & getattr(B, "EW_" + n)]
+            raise B.OasisError("paged cache", 1, "device error word: " + ", ".join(names))
+
+    def _layer(self, t: torch.Tensor, layer: int) -> int:
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of {self.layers}")
+        return t.data_ptr() + layer * t.stride(0) * t.element_size()

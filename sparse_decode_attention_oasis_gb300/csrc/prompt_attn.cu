@@ -1,170 +1,601 @@
-// Causal attention over packed prompts (oasis_prompt_attn).
+// Causal attention over packed prompts (oasis_prompt_attn): TMA -> shared memory ->
+// tcgen05.mma -> TMEM, one persistent thread block per SM.
 //
-// Mathematics: one pass over the keys with the running maximum and sum of a
-// softmax, o = sum_j 2^(c s_j - M) v_j / sum_j 2^(c s_j - M), c = scale * log2(e).
+// Mathematics: one pass over the keys with a running reference M and sum of a
+// softmax, w_j = 2^(c s_j - M), o = sum_j w_j v_j / sum_j w_j, c = scale * log2(e).  M moves
+// only when a row's scores pass it by more than 2^8 (weights stay below 256, which
+// costs no precision in fp32 or bf16), so the accumulators are rescaled a few times in a
+// whole row, not at every tile.
 //
 // Rows: the G query heads of a KV head and consecutive tokens are packed into the
 // rows of a tile (row = token * G + head), so that every K/V tile is read once for
 // the whole group and a tile of short sequences is not mostly empty.
-// Roundings: weights to bf16 for the product with V (2^-9 each, the sums are of the
-// unrounded fp32 weights), the output to bf16; scores, maxima, sums and
-// accumulators are fp32.
+// Roundings: weights to bf16 for the product with V (2^-9 each at most; the sums are of the
+// unrounded fp32 weights), the output to bf16; scores, maxima, sums and accumulators
+// are fp32.  fp16 weights would keep 3 bits more, but both operands of an MMA have one
+// type, and bf16 values do not fit fp16's range.
+//
+// Roles (352 threads):
+//   warps 0..3, 4..7  softmax of row tile 0 and 1: one row to a thread, its 128 scores read
+//                     from TMEM, the weights written back to TMEM in bf16 over the scores,
+//                     the output row at the end;
+//   warp 8            one lane issues the MMAs, S_i = Q_i K_j^T, then O_i += P_i V_j with P_i from
+//                     TMEM.  While one tile's softmax runs, the tensor cores work for the other;
+//   warp 9            TMA producer: Q tiles, and K and V tiles of 128 tokens in a ring of 5;
+//   warp 10           scheduler: finds this block's work items and hands them to the others.
+// TMEM: two S/P and two O tiles of 128 columns, all 512.  Shared memory: 64 KB of Q and a ring
+// of 160 KB.  V rows behind a sequence's last token (another sequence's, or padding that
+// may hold NaN) are zeroed in shared memory before the product: zero times NaN is not zero.
+// Every wait is bounded: on expiry the block raises OASIS_EW_TIMEOUT, waits (bounded)
+// for its own copies and MMAs, frees TMEM and returns.
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace oasis {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTileRows = kWarps * 16;
-constexpr int kTileKeys = 32;
-constexpr int kPitch = kD + 8;  // shared-memory row pitch in elements
+using namespace tc;
 
-__device__ __forceinline__ void ldsm_x4(uint32_t* r, const uint16_t* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"((uint32_t)__cvta_generic_to_shared(p)));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t* r, const uint16_t* p) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"((uint32_t)__cvta_generic_to_shared(p)));
+constexpr int kTile = 128;                   // rows of a query tile, tokens of a K/V tile
+constexpr uint32_t kHalf = kTile * 128;      // bytes of 128 rows x 64 columns
+constexpr uint32_t kTileBytes = 2 * kHalf;
+constexpr int kRing = 5;
+constexpr int kItems = 4;                    // items that the scheduler may be ahead
+constexpr int kThreads = 352;
+constexpr int kConsumers = 10;               // warps that read an item: softmax, MMA, producer
+constexpr float kSlack = 8.0f;
+
+struct Item {
+  int row0;   // first row of the sequence, -1: no more items
+  int len;    // its tokens
+  int tok0;   // first token of query tile 0
+  int h;      // KV head
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t tail, done;
+  Item items[kItems];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars);
+
+// V operand: rows are tokens (the contraction), 64 columns of dimensions to a 128-byte
+// row: 8-token groups 1,024 B apart (SBO), the second 64 dimensions kHalf apart (LBO).
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kHalf >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
-prompt_attn_kernel(PagedShape s, const uint16_t* __restrict__ q, size_t q_stride, const uint16_t* __restrict__ k,
-                   size_t k_stride, const uint16_t* __restrict__ v, size_t v_stride,
-                   const int* __restrict__ row_start, int n_rows, float scale_log2, uint16_t* __restrict__ out,
-                   size_t out_stride, unsigned* __restrict__ err) {
-  __shared__ __align__(16) uint16_t ks[kTileKeys * kPitch], vs[kTileKeys * kPitch];
-  __shared__ int found[3];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = s.Hq / s.Hkv, per = kTileRows / G;  // tokens in a tile
-  const int h = blockIdx.y;
-  if (tid == 0) {
-    int tile = blockIdx.x;
-    found[0] = -1;
-    for (int b = 0; b < s.B; ++b) {
-      const int a = row_start[b], z = row_start[b + 1];
-      if (a < 0 || z < a || z > n_rows) {
-        if (blockIdx.x == 0 && blockIdx.y == 0) set_err(err, OASIS_EW_BAD_COUNT);
-        continue;
+__device__ __forceinline__ void mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+#define OASIS_R32(r)                                                                                             \
+  r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[11], r[12], r[13], r[14], r[15], r[16],   \
+      r[17], r[18], r[19], r[20], r[21], r[22], r[23], r[24], r[25], r[26], r[27], r[28], r[29], r[30], r[31]
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// K/V tiles that query tile i of an item reads (0: the tile has no token).
+__device__ __forceinline__ int kv_tiles(const Item& it, int i, int per) {
+  const int t0 = it.tok0 + i * per;
+  return t0 < it.len ? (min(it.len, t0 + per) + kTile - 1) / kTile : 0;
+}
+
+// Work items: two query tiles of one sequence and KV head.  Up to 320 sequences are kept in one
+// warp's registers and the items are ordered by their place in the sequence, the last
+// (the ones with the most keys) first, so that every block gets an equal share; more sequences are
+// walked in their order, 32 at a time.
+struct Schedule {
+  static constexpr int kKept = 10;  // sequences to a lane
+  const int* row_start;
+  int B, n_rows, pair;              // pair: tokens of an item
+  int lane;
+  bool sorted;
+  int n[kKept];                     // items of sequence lane + 32 i
+  int most;                         // the most items of a sequence
+  int window;                       // unsorted: first sequence of the window, items before it
+  long long before;
+  unsigned bits;
+
+  __device__ int items_of(int b, bool flag) {
+    const int a = row_start[b], z = row_start[b + 1];
+    if (a < 0 || z < a || z > n_rows) {
+      if (flag) bits |= OASIS_EW_BAD_COUNT;
+      return 0;
+    }
+    return (z - a + pair - 1) / pair;
+  }
+  __device__ void init(const int* rs, int b_, int rows, int pr, int ln) {
+    row_start = rs;
+    B = b_;
+    n_rows = rows;
+    pair = pr;
+    lane = ln;
+    bits = 0;
+    sorted = B <= 32 * kKept;
+    window = 0;
+    before = 0;
+    most = 0;
+    if (sorted) {
+#pragma unroll
+      for (int i = 0; i < kKept; ++i) {
+        const int b = lane + 32 * i;
+        n[i] = b < B ? items_of(b, true) : 0;
+        most = max(most, n[i]);
       }
-      const int n = (z - a + per - 1) / per;
-      if (tile < n) {
-        found[0] = a;
-        found[1] = z;
-        found[2] = tile * per;
+      most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+    }
+  }
+  __device__ int at_or_above(int level) const {  // items whose place in their sequence is >= level
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) c += max(n[i] - level, 0);
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+  // Sequence and place of item idx (calls with rising idx); false: there are no more.
+  __device__ bool find(long long idx, int& b, int& place) {
+    if (sorted) {
+      if (idx >= at_or_above(0)) return false;
+      int lo = 0, hi = most - 1;  // the highest level with more than idx items at or above it
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (at_or_above(m) > idx) lo = m; else hi = m - 1;
+      }
+      int rank = (int)idx - at_or_above(lo + 1);
+      place = lo;
+      b = -1;
+#pragma unroll
+      for (int i = 0; i < kKept; ++i) {
+        const unsigned has = __ballot_sync(0xffffffffu, n[i] > lo);
+        const int c = __popc(has);
+        if (b < 0) {
+          if (rank < c) b = 32 * i + __fns(has, 0, rank + 1);
+          rank -= c;
+        }
+      }
+      return true;
+    }
+    while (window < B) {
+      const int s = window + lane;
+      const int c = s < B ? items_of(s, true) : 0;
+      int x = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const int all = __shfl_sync(0xffffffffu, x, 31);
+      if (idx < before + all) {
+        const int local = (int)(idx - before);
+        const unsigned has = __ballot_sync(0xffffffffu, x > local);
+        const int w = __ffs(has) - 1;
+        b = window + w;
+        place = local - __shfl_sync(0xffffffffu, x - c, w);
+        return true;
+      }
+      before += all;
+      window += 32;
+    }
+    return false;
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, PagedShape s, const int* __restrict__ row_start,
+                   int n_rows, float scale_log2, uint16_t* __restrict__ out, size_t out_stride,
+                   unsigned* __restrict__ err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + 2 * kTileBytes;
+  Bars* bars = reinterpret_cast<Bars*>(ring + kRing * (size_t)kTileBytes);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = s.Hq / s.Hkv, per = kTile / G;  // per: tokens of a query tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->o_full[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bars->kv_full[i], 1);
+      mbar_init(&bars->kv_empty[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], kConsumers);
+    }
+    mbar_init(&bars->tail, 1);
+    mbar_init(&bars->done, 1);
+    bars->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  bool timed_out = false;
+
+  // Item k of this block, for the warps that consume items: false at the end or on a time-out.
+  auto take = [&](int k, Item& it) {
+    const int st = k % kItems;
+    const bool ok = mbar_wait(&bars->item_full[st], (k / kItems) & 1, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) {
+      timed_out = true;
+      return false;
+    }
+    it = bars->items[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[st]);
+    return it.row0 >= 0;
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax and output
+    const int i = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + (uint32_t)i * 128, o_addr = tmem + lanes + 256u + (uint32_t)i * 128;
+    const int g = row % G, tok_in = row / G;
+    unsigned turn = 0, outputs = 0;
+    Item it;
+    for (int k = 0; take(k, it); ++k) {
+      const int n = kv_tiles(it, i, per);
+      if (n == 0) continue;
+      const int t0 = it.tok0 + i * per, tok = t0 + tok_in;
+      float ref = 0.f;
+      uint64_t sum_a = 0, sum_b = 0;
+      for (int j = 0; j < n; ++j, ++turn) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[i], turn & 1, abort_flag))) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t x[128];
+        tmem_ld32(s_addr, x);
+        tmem_ld32(s_addr + 32, x + 32);
+        tmem_ld32(s_addr + 64, x + 64);
+        tmem_ld32(s_addr + 96, x + 96);
+        tmem_wait_ld();
+        if (j * kTile + kTile - 1 > t0 || (j + 1) * kTile > it.len) {  // keys in the future or behind the sequence
+          const int last = min(tok, it.len - 1) - j * kTile;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > last) x[c] = 0xff800000u;
+        }
+        float m[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m[c] = __uint_as_float(x[c]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 16)
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            m[d] = c + 8 < 128 ? max3(m[d], __uint_as_float(x[c + d]), __uint_as_float(x[(c + 8 < 128 ? c + 8 : c) + d]))
+                               : fmaxf(m[d], __uint_as_float(x[c + d]));
+        const float big = scale_log2 * max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+        if (j == 0) {
+          ref = big == neg_inf() ? 0.f : big;
+        } else if (__any_sync(0xffffffffu, big > ref + kSlack)) {
+          // S_j is there, so the product with V_(j-1) is complete and O is at rest until P_j is handed over
+          const float next = fmaxf(ref, big), f = ex2(ref - next);
+          ref = next;
+          float a, b;
+          unpack2(sum_a, a, b);
+          sum_a = pack2(a * f, b * f);
+          unpack2(sum_b, a, b);
+          sum_b = pack2(a * f, b * f);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int d = 0; d < 32; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
+            tmem_st32(o_addr + c, o);
+          }
+        }
+        const uint64_t sc2 = pack2(scale_log2, scale_log2), ref2 = pack2(-ref, -ref);
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+          float a, b, d, e;
+          unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, ref2), a, b);
+          unpack2(fma2(pack2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2, ref2), d, e);
+          a = ex2(a);
+          b = ex2(b);
+          d = ex2(d);
+          e = ex2(e);
+          sum_a = add2(sum_a, pack2(a, b));
+          sum_b = add2(sum_b, pack2(d, e));
+          x[c / 2] = pack_bf16x2(a, b);
+          x[c / 2 + 1] = pack_bf16x2(d, e);
+          if (c == 60) tmem_st32(s_addr, x);
+        }
+        tmem_st32(s_addr + 32, x + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[i]);
+      }
+      if (timed_out) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full[i], outputs & 1, abort_flag))) {
+        timed_out = true;
         break;
       }
-      tile -= n;
+      ++outputs;
+      tc_fence_after();
+      float a, b, d, e;
+      unpack2(sum_a, a, b);
+      unpack2(sum_b, d, e);
+      const float total = (a + b) + (d + e);
+      const float inv = total > 0.f ? 1.0f / total : 0.f;
+      const bool live = row < per * G && tok < it.len;
+      uint16_t* dst = out + (size_t)(it.row0 + (live ? tok : 0)) * out_stride + (size_t)(it.h * G + g) * kD;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + c, o);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 8)
+            *reinterpret_cast<uint4*>(dst + c + q) =
+                make_uint4(pack_bf16x2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv),
+                           pack_bf16x2(__uint_as_float(o[q + 2]) * inv, __uint_as_float(o[q + 3]) * inv),
+                           pack_bf16x2(__uint_as_float(o[q + 4]) * inv, __uint_as_float(o[q + 5]) * inv),
+                           pack_bf16x2(__uint_as_float(o[q + 6]) * inv, __uint_as_float(o[q + 7]) * inv));
+        }
+      }
+      tc_fence_before();
     }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t id_s = instr_desc(kTile), id_o = instr_desc(kTile) | (1u << 16);
+    const uint32_t q0 = smem_u32(smem), kv0 = smem_u32(ring);
+    unsigned slot = 0;                      // ring position of K_j: slots are used in the order K_0 V_0 K_1 V_1 ..
+    unsigned q_uses[2] = {0, 0}, turns[2] = {0, 0};  // Q tiles, S tiles so far
+    Item it;
+    for (int k = 0; take(k, it) && !timed_out; ++k) {
+      const int n0 = kv_tiles(it, 0, per), n1 = kv_tiles(it, 1, per);
+      const int n = max(n0, n1);
+      if (lane == 0) {
+        for (int j = 0; j <= n && !timed_out; ++j) {
+          const unsigned ks = slot + 2 * j, vs = slot + 2 * j - 1;  // K_j, V_(j-1)
+          if (j < n && !mbar_wait(&bars->kv_full[ks % kRing], (ks / kRing) & 1, abort_flag)) {
+            timed_out = true;
+            break;
+          }
+          if (j > 0 && !mbar_wait(&bars->kv_full[vs % kRing], (vs / kRing) & 1, abort_flag)) {
+            timed_out = true;
+            break;
+          }
+          for (int i = 0; i < 2 && !timed_out; ++i) {
+            const int ni = i ? n1 : n0;
+            const uint32_t s_addr = tmem + (uint32_t)i * 128, o_addr = tmem + 256u + (uint32_t)i * 128;
+            if (j > 0 && j <= ni) {
+              if (!mbar_wait(&bars->p_full[i], (turns[i] - 1) & 1, abort_flag)) {
+                timed_out = true;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t vb = kv0 + (vs % kRing) * kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_bf16_ta(o_addr, s_addr + kk * 8, v_desc(vb + kk * 2048), id_o, j > 1 || kk > 0 ? 1u : 0u);
+              if (j == ni) mma_commit(&bars->o_full[i]);
+            }
+            if (j < ni) {
+              if (j == 0) {
+                if (!mbar_wait(&bars->q_full[i], q_uses[i] & 1, abort_flag)) {
+                  timed_out = true;
+                  break;
+                }
+                ++q_uses[i];
+              }
+              tc_fence_after();
+              const uint32_t kb = kv0 + (ks % kRing) * kTileBytes, qb = q0 + (uint32_t)i * kTileBytes;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
+                mma_bf16(s_addr, smem_desc(qb + off), smem_desc(kb + off), id_s, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&bars->s_full[i]);
+              if (j == ni - 1) mma_commit(&bars->q_empty[i]);
+              ++turns[i];
+            }
+          }
+          if (timed_out) break;
+          if (j > 0) mma_commit(&bars->kv_empty[vs % kRing]);
+          if (j < n) mma_commit(&bars->kv_empty[ks % kRing]);
+        }
+        slot += 2 * n;
+      }
+      timed_out = __any_sync(0xffffffffu, timed_out);
+      if (timed_out) break;
+    }
+    if (lane == 0) {  // nothing of this block is in flight on the tensor cores when it leaves
+      mma_commit(&bars->done);
+      mbar_drain(&bars->done, 0);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ TMA producer
+    unsigned slot = 0, q_uses[2] = {0, 0}, tails = 0;
+    const uint32_t q_bytes = 2u * 128u * (uint32_t)(per * G);
+    Item it;
+    for (int k = 0; take(k, it) && !timed_out; ++k) {
+      const int n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
+      for (int j = 0; j < n && !timed_out; ++j) {
+        for (int part = 0; part < 2 && !timed_out; ++part, ++slot) {  // K_j, V_j
+          const bool q_here = j == 0 && kv_tiles(it, part, per) > 0;   // Q_0 before K_0, Q_1 before V_0
+          const bool tail = part == 1 && (j + 1) * kTile > it.len;
+          uint8_t* buf = ring + (size_t)(slot % kRing) * kTileBytes;
+          bool ok = true;
+          if (lane == 0) {
+            if (q_here) {
+              ok = mbar_wait(&bars->q_empty[part], (q_uses[part] & 1) ^ 1, abort_flag);
+              if (ok) {
+                uint8_t* qb = smem + (size_t)part * kTileBytes;
+                mbar_expect_tx(&bars->q_full[part], q_bytes);
+                tma_load_3d(qb, &map_q, 0, it.h * G, it.row0 + it.tok0 + part * per, &bars->q_full[part]);
+                tma_load_3d(qb + kHalf, &map_q, 64, it.h * G, it.row0 + it.tok0 + part * per, &bars->q_full[part]);
+              }
+            }
+            ok = ok && mbar_wait(&bars->kv_empty[slot % kRing], ((slot / kRing) & 1) ^ 1, abort_flag);
+            if (ok) {
+              uint64_t* bar = tail ? &bars->tail : &bars->kv_full[slot % kRing];
+              const CUtensorMap* map = part ? &map_v : &map_k;
+              mbar_expect_tx(bar, kTileBytes);
+              tma_load_3d(buf, map, 0, it.h, it.row0 + j * kTile, bar);
+              tma_load_3d(buf + kHalf, map, 64, it.h, it.row0 + j * kTile, bar);
+            }
+          }
+          if (q_here) ++q_uses[part];
+          timed_out = !__all_sync(0xffffffffu, ok);
+          if (tail && !timed_out) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->tail, tails & 1, abort_flag))) {
+              timed_out = true;
+              mbar_drain(&bars->tail, tails & 1);
+              break;
+            }
+            ++tails;
+            const int first = it.len - j * kTile;  // 1 .. 127: rows from here on belong to no key of the sequence
+            for (int c = lane; c < (kTile - first) * 8; c += 32) {
+              *reinterpret_cast<uint4*>(buf + first * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(buf + kHalf + first * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->kv_full[slot % kRing]);
+          }
+        }
+      }
+    }
+    if (timed_out && lane == 0) {  // copies that were issued have to land before the block leaves
+      for (unsigned u = slot > kRing ? slot - kRing : 0; u < slot; ++u) mbar_drain(&bars->kv_full[u % kRing], (u / kRing) & 1);
+      for (int i = 0; i < 2; ++i)
+        if (q_uses[i]) mbar_drain(&bars->q_full[i], (q_uses[i] - 1) & 1);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ scheduler
+    Schedule sch;
+    sch.init(row_start, s.B, n_rows, 2 * per, lane);
+    for (int k = 0;; ++k) {
+      // rounds of gridDim.x items, every second one in the other direction
+      const long long at = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      int b = 0, place = 0;
+      Item it{-1, 0, 0, 0};
+      if (sch.find(at / s.Hkv, b, place)) {
+        const int a = row_start[b];
+        it = Item{a, row_start[b + 1] - a, place * 2 * per, (int)(at % s.Hkv)};
+      }
+      const int st = k % kItems;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[st], ((k / kItems) & 1) ^ 1, abort_flag))) {
+        timed_out = true;
+        break;
+      }
+      if (lane == 0) {
+        bars->items[st] = it;
+        mbar_arrive(&bars->item_full[st]);
+      }
+      __syncwarp();
+      if (it.row0 < 0) break;
+    }
+    set_err(err, sch.bits);
   }
-  __syncthreads();
-  if (found[0] < 0) return;
-  const int a = found[0], len = found[1] - a, t0 = found[2];
 
-  const int row[2] = {warp * 16 + (lane >> 2), warp * 16 + (lane >> 2) + 8};
-  int tok[2];
-  bool live[2];
-  uint32_t qf[8][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    tok[i] = t0 + row[i] / G;
-    live[i] = row[i] < per * G && tok[i] < len;
-    const uint16_t* src = q + (size_t)(a + tok[i]) * q_stride + (size_t)(h * G + row[i] % G) * kD + (lane & 3) * 2;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      qf[m][i] = live[i] ? *reinterpret_cast<const uint32_t*>(src + m * 16) : 0u;
-      qf[m][2 + i] = live[i] ? *reinterpret_cast<const uint32_t*>(src + m * 16 + 8) : 0u;
-    }
+  if (timed_out) {
+    *abort_flag = 1;
+    if (lane == 0) set_err(err, OASIS_EW_TIMEOUT);
   }
-  float acc[16][4] = {};
-  float top[2] = {neg_inf(), neg_inf()}, sum[2] = {0.f, 0.f};
-  const int keys = min(len, t0 + per);
-  for (int j0 = 0; j0 < keys; j0 += kTileKeys) {
-    __syncthreads();
-    for (int i = tid; i < kTileKeys * 16; i += kWarps * 32) {
-      const int r = i >> 4, c = (i & 15) * 8;
-      const bool in = j0 + r < len;
-      const size_t at = (size_t)(a + j0 + r);
-      *reinterpret_cast<uint4*>(ks + r * kPitch + c) =
-          in ? ldg_nc(k + at * k_stride + (size_t)h * kD + c) : make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(vs + r * kPitch + c) =
-          in ? ldg_nc(v + at * v_stride + (size_t)h * kD + c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    __syncthreads();
-    float sc[4][4] = {};
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int n = 0; n < 4; n += 2) {
-        uint32_t r[4];
-        ldsm_x4(r, ks + (n * 8 + (lane & 7) + (lane & 16 ? 8 : 0)) * kPitch + m * 16 + (lane & 8));
-        mma_bf16_16816(sc[n][0], sc[n][1], sc[n][2], sc[n][3], qf[m][0], qf[m][1], qf[m][2], qf[m][3], r[0], r[1]);
-        mma_bf16_16816(sc[n + 1][0], sc[n + 1][1], sc[n + 1][2], sc[n + 1][3], qf[m][0], qf[m][1], qf[m][2], qf[m][3],
-                       r[2], r[3]);
-      }
-    float big[2] = {neg_inf(), neg_inf()};
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int j = j0 + n * 8 + (lane & 3) * 2 + (c & 1);
-        sc[n][c] = j <= tok[c >> 1] && j < len ? sc[n][c] * scale_log2 : neg_inf();
-        big[c >> 1] = fmaxf(big[c >> 1], sc[n][c]);
-      }
-    float f[2], ref[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 1));
-      big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 2));
-      const float next = fmaxf(top[i], big[i]);
-      f[i] = top[i] == neg_inf() ? 0.f : exp2f(top[i] - next);
-      top[i] = next;
-      ref[i] = next == neg_inf() ? 0.f : next;
-      sum[i] *= f[i];
-    }
-    uint32_t p[4][2];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        sc[n][c] = exp2f(sc[n][c] - ref[c >> 1]);
-        sum[c >> 1] += sc[n][c];
-      }
-      p[n][0] = pack_bf16x2(sc[n][0], sc[n][1]);
-      p[n][1] = pack_bf16x2(sc[n][2], sc[n][3]);
-    }
-#pragma unroll
-    for (int d = 0; d < 16; ++d) {
-      acc[d][0] *= f[0];
-      acc[d][1] *= f[0];
-      acc[d][2] *= f[1];
-      acc[d][3] *= f[1];
-    }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int d = 0; d < 16; d += 2) {
-        uint32_t r[4];
-        ldsm_x4_t(r, vs + (kk * 16 + (lane & 15)) * kPitch + d * 8 + (lane & 16 ? 8 : 0));
-        mma_bf16_16816(acc[d][0], acc[d][1], acc[d][2], acc[d][3], p[2 * kk][0], p[2 * kk][1], p[2 * kk + 1][0],
-                       p[2 * kk + 1][1], r[0], r[1]);
-        mma_bf16_16816(acc[d + 1][0], acc[d + 1][1], acc[d + 1][2], acc[d + 1][3], p[2 * kk][0], p[2 * kk][1],
-                       p[2 * kk + 1][0], p[2 * kk + 1][1], r[2], r[3]);
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-    if (!live[i]) continue;
-    const float inv = sum[i] > 0.f ? 1.0f / sum[i] : 0.f;
-    uint16_t* dst = out + (size_t)(a + tok[i]) * out_stride + (size_t)(h * G + row[i] % G) * kD + (lane & 3) * 2;
-#pragma unroll
-    for (int d = 0; d < 16; ++d)
-      *reinterpret_cast<uint32_t*>(dst + d * 8) = pack_bf16x2(acc[d][2 * i] * inv, acc[d][2 * i + 1] * inv);
-  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+bool rows_map(CUtensorMap* m, const uint16_t* p, int heads, int n_rows, size_t stride, int box_heads, int box_rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)heads, (cuuint64_t)n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -173,12 +604,21 @@ cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_
                                size_t k_stride, const uint16_t* v, size_t v_stride, const int* row_start, int n_rows,
                                float scale, uint16_t* out, size_t out_stride, unsigned* err, cudaStream_t stream) {
   if (n_rows == 0) return cudaSuccess;
-  const int per = kTileRows / s.G();
-  // tiles of all sequences: at most one partly filled tile for each
-  const long long tiles = (long long)n_rows / per + (s.B < n_rows ? s.B : n_rows);
-  dim3 grid((unsigned)tiles, (unsigned)s.Hkv);
-  prompt_attn_kernel<<<grid, kWarps * 32, 0, stream>>>(s, q, q_stride, k, k_stride, v, v_stride, row_start, n_rows,
-                                                       scale * 1.4426950408889634f, out, out_stride, err);
+  if (!encode_fn()) return cudaErrorNotSupported;
+  const int G = s.G(), per = kTile / G;
+  CUtensorMap mq, mk, mv;
+  if (!rows_map(&mq, q, s.Hq, n_rows, q_stride, G, per) || !rows_map(&mk, k, s.Hkv, n_rows, k_stride, 1, kTile) ||
+      !rows_map(&mv, v, s.Hkv, n_rows, v_stride, 1, kTile))
+    return cudaErrorInvalidValue;
+  // items of all sequences: at most one partly filled one for each
+  const long long items = ((long long)n_rows / (2 * per) + (s.B < n_rows ? s.B : n_rows)) * s.Hkv;
+  const int sms = sm_count();
+  const int grid = items < sms ? (int)items : sms;
+  static int attr_cache[kMaxDevicesCached] = {};
+  cudaError_t e = ensure_dyn_smem((const void*)prompt_attn_kernel, kSmemBytes, attr_cache);
+  if (e != cudaSuccess) return e;
+  prompt_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(mq, mk, mv, s, row_start, n_rows,
+                                                             scale * 1.4426950408889634f, out, out_stride, err);
   return cudaGetLastError();
 }
 

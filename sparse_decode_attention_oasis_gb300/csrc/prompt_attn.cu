@@ -15,7 +15,7 @@
 // are fp32.  fp16 weights would keep 3 bits more, but both operands of an MMA have one
 // type, and bf16 values do not fit fp16's range.
 //
-// Roles (352 threads):
+// Roles (384 threads):
 //   warps 0..3, 4..7  softmax of row tile 0 and 1: one row to a thread, its 128 scores read
 //                     from TMEM, the weights written back to TMEM in bf16 over the scores,
 //                     the output row at the end;
@@ -41,7 +41,9 @@ constexpr uint32_t kHalf = kTile * 128;      // bytes of 128 rows x 64 columns
 constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr int kRing = 5;
 constexpr int kItems = 4;                    // items that the scheduler may be ahead
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
+// 168 registers a thread at launch (64,512 in all): 8 warps of 208 and 4 of 88 use them up
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kConsumers = 10;               // warps that read an item: softmax, MMA, producer
 constexpr float kSlack = 8.0f;
 
@@ -65,27 +67,33 @@ struct Bars {
 
 constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars);
 
-// V operand: rows are tokens (the contraction), 64 columns of dimensions to a 128-byte
-// row: 8-token groups 1,024 B apart (SBO), the second 64 dimensions kHalf apart (LBO).
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kHalf >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Shared-memory operand descriptors, low word: address and leading offset, high word: the rest.
+// Q, K: K-major 128-byte rows, 8-row groups 1,024 B apart.  V: rows are tokens (the contraction),
+// 64 dimensions to a 128-byte row: 8-token groups 1,024 B apart, the second 64 dimensions kHalf apart.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t qk_desc_low(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t v_desc_low(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((kHalf >> 4) << 16); }
+
+// One elected lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.b32 %0, 1, 0, P;\n}\n" : "=r"(ok));
+  return ok != 0;
 }
 
-__device__ __forceinline__ void mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D (+)= A B, operands given as the low words of their descriptors.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-      ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(acc ? 1u : 0u), "n"(kDescHigh));
 }
-
-#define OASIS_R32(r)                                                                                             \
-  r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7], r[8], r[9], r[10], r[11], r[12], r[13], r[14], r[15], r[16],   \
-      r[17], r[18], r[19], r[20], r[21], r[22], r[23], r[24], r[25], r[26], r[27], r[28], r[29], r[30], r[31]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+      "r"(acc ? 1u : 0u), "n"(kDescHigh));
+}
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -304,8 +312,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     return it.row0 >= 0;
   };
 
+  // A whole warp waits: the same answer for all lanes.
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+  };
+
   if (warp < 8) {
     // ------------------------------------------------------------ softmax and output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -421,7 +435,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       }
       tc_fence_before();
     }
-  } else if (warp == 8) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  }
+  if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t id_s = instr_desc(kTile), id_o = instr_desc(kTile) | (1u << 16);
     const uint32_t q0 = smem_u32(smem), kv0 = smem_u32(ring);
@@ -431,66 +448,55 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     for (int k = 0; take(k, it) && !timed_out; ++k) {
       const int n0 = kv_tiles(it, 0, per), n1 = kv_tiles(it, 1, per);
       const int n = max(n0, n1);
-      if (lane == 0) {
-        for (int j = 0; j <= n && !timed_out; ++j) {
-          const unsigned ks = slot + 2 * j, vs = slot + 2 * j - 1;  // K_j, V_(j-1)
-          if (j < n && !mbar_wait(&bars->kv_full[ks % kRing], (ks / kRing) & 1, abort_flag)) {
-            timed_out = true;
-            break;
-          }
-          if (j > 0 && !mbar_wait(&bars->kv_full[vs % kRing], (vs / kRing) & 1, abort_flag)) {
-            timed_out = true;
-            break;
-          }
-          for (int i = 0; i < 2 && !timed_out; ++i) {
-            const int ni = i ? n1 : n0;
-            const uint32_t s_addr = tmem + (uint32_t)i * 128, o_addr = tmem + 256u + (uint32_t)i * 128;
-            if (j > 0 && j <= ni) {
-              if (!mbar_wait(&bars->p_full[i], (turns[i] - 1) & 1, abort_flag)) {
-                timed_out = true;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t vb = kv0 + (vs % kRing) * kTileBytes;
+      // the whole warp walks and waits, so that the operands stay warp-uniform; one lane issues
+      for (int j = 0; j <= n && !timed_out; ++j) {
+        const unsigned ks = (slot + 2 * j) % kRing, vs = (slot + 2 * j - 1) % kRing;  // K_j, V_(j-1)
+        if (j < n) timed_out |= !wait_all(&bars->kv_full[ks], ((slot + 2 * j) / kRing) & 1);
+        if (j > 0) timed_out |= !wait_all(&bars->kv_full[vs], ((slot + 2 * j - 1) / kRing) & 1);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ta(o_addr, s_addr + kk * 8, v_desc(vb + kk * 2048), id_o, j > 1 || kk > 0 ? 1u : 0u);
+        for (int i = 0; i < 2; ++i) {
+          const int ni = i ? n1 : n0;
+          const uint32_t s_addr = tmem + (uint32_t)i * 128, o_addr = tmem + 256u + (uint32_t)i * 128;
+          if (j > 0 && j <= ni && !timed_out) {
+            timed_out |= !wait_all(&bars->p_full[i], (turns[i] - 1) & 1);
+            tc_fence_after();
+            const uint32_t vb = v_desc_low(kv0 + vs * kTileBytes);
+            if (!timed_out && elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
               if (j == ni) mma_commit(&bars->o_full[i]);
             }
-            if (j < ni) {
-              if (j == 0) {
-                if (!mbar_wait(&bars->q_full[i], q_uses[i] & 1, abort_flag)) {
-                  timed_out = true;
-                  break;
-                }
-                ++q_uses[i];
-              }
-              tc_fence_after();
-              const uint32_t kb = kv0 + (ks % kRing) * kTileBytes, qb = q0 + (uint32_t)i * kTileBytes;
+            __syncwarp();
+          }
+          if (j < ni && !timed_out) {
+            if (j == 0) timed_out |= !wait_all(&bars->q_full[i], q_uses[i]++ & 1);
+            tc_fence_after();
+            const uint32_t qb = qk_desc_low(q0 + (uint32_t)i * kTileBytes), kb = qk_desc_low(kv0 + ks * kTileBytes);
+            if (!timed_out && elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
-                mma_bf16(s_addr, smem_desc(qb + off), smem_desc(kb + off), id_s, kk > 0 ? 1u : 0u);
+                const uint32_t off = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+                mma_ss(s_addr, qb + off, kb + off, id_s, kk > 0);
               }
               mma_commit(&bars->s_full[i]);
               if (j == ni - 1) mma_commit(&bars->q_empty[i]);
-              ++turns[i];
             }
+            __syncwarp();
+            ++turns[i];
           }
-          if (timed_out) break;
-          if (j > 0) mma_commit(&bars->kv_empty[vs % kRing]);
-          if (j < n) mma_commit(&bars->kv_empty[ks % kRing]);
         }
-        slot += 2 * n;
+        if (!timed_out && elect_one()) {
+          if (j > 0) mma_commit(&bars->kv_empty[vs]);
+          if (j < n) mma_commit(&bars->kv_empty[ks]);
+        }
+        __syncwarp();
       }
-      timed_out = __any_sync(0xffffffffu, timed_out);
-      if (timed_out) break;
+      slot += 2 * n;
     }
-    if (lane == 0) {  // nothing of this block is in flight on the tensor cores when it leaves
-      mma_commit(&bars->done);
-      mbar_drain(&bars->done, 0);
-    }
+    // nothing of this block is in flight on the tensor cores when it leaves
+    if (elect_one()) mma_commit(&bars->done);
     __syncwarp();
+    mbar_drain(&bars->done, 0);
   } else if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
     unsigned slot = 0, q_uses[2] = {0, 0}, tails = 0;
@@ -550,7 +556,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (q_uses[i]) mbar_drain(&bars->q_full[i], (q_uses[i] - 1) & 1);
     }
     __syncwarp();
-  } else {
+  } else if (warp == 10) {
     // ------------------------------------------------------------ scheduler
     Schedule sch;
     sch.init(row_start, s.B, n_rows, 2 * per, lane);

@@ -440,30 +440,54 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
   if (tid == 0) a.tails[blockIdx.x] = tail;
 }
 
-// Joins the pieces of a pair that starts in block blockIdx.x and ends in a later one.
-__global__ void __launch_bounds__(kD)
+// Joins the pieces of a pair that starts in block blockIdx.x and ends in a later one, one query
+// row to a thread block: its warps take every kWarps-th piece, a lane four dimensions.
+__global__ void __launch_bounds__(kThreads)
 paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const int2* __restrict__ tails,
                          uint16_t* __restrict__ out) {
-  const int2 t = tails[blockIdx.x];
+  __shared__ float rows[kWarps][kRowFloats];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = s.Hq / s.Hkv, r = blockIdx.y, first = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  const int2 t = tails[first];
   if (t.x < 0) return;
-  const int G = s.Hq / s.Hkv;
-  const int first = blockIdx.x, d = threadIdx.x;
-  for (int r = 0; r < G; ++r) {
-    const float* row0 = parts + ((long long)first * 2 + 1) * G * kRowFloats + r * kRowFloats;
-    float top = row0[kD], sum = row0[kD + 1], o = row0[d];
-    for (int c = first + 1; c <= t.y; ++c) {
-      const float* row = parts + (long long)c * 2 * G * kRowFloats + r * kRowFloats;
-      const float m = row[kD];
-      if (m == neg_inf()) continue;
-      const float next = fmaxf(top, m);
-      const float f0 = top == neg_inf() ? 0.f : exp2f(top - next), f1 = exp2f(m - next);
-      o = fmaf(o, f0, row[d] * f1);
-      sum = fmaf(sum, f0, row[kD + 1] * f1);
-      top = next;
-    }
-    const float v = sum > 0.f ? o / sum : 0.f;
-    out[((long long)t.x * G + r) * kD + d] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
+  const int n = t.y - first + 1;
+  float top = neg_inf(), sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int c = warp; c < n; c += kWarps) {
+    const float* row = parts + (((long long)first + c) * 2 + (c == 0 ? 1 : 0)) * G * kRowFloats + r * kRowFloats;
+    const float2 ml = *reinterpret_cast<const float2*>(row + kD);
+    const float2 a = *reinterpret_cast<const float2*>(row + lane * 4), b = *reinterpret_cast<const float2*>(row + lane * 4 + 2);
+    const float next = fmaxf(top, ml.x);
+    const float f0 = top == neg_inf() ? 0.f : exp2f(top - next), f1 = ml.x == neg_inf() ? 0.f : exp2f(ml.x - next);
+    o[0] = fmaf(o[0], f0, a.x * f1);
+    o[1] = fmaf(o[1], f0, a.y * f1);
+    o[2] = fmaf(o[2], f0, b.x * f1);
+    o[3] = fmaf(o[3], f0, b.y * f1);
+    sum = fmaf(sum, f0, ml.y * f1);
+    top = next;
   }
+  for (int i = 0; i < 4; ++i) rows[warp][lane * 4 + i] = o[i];
+  if (lane == 0) {
+    rows[warp][kD] = top;
+    rows[warp][kD + 1] = sum;
+  }
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= kD / 2) return;
+  float m = neg_inf();
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, rows[w][kD]);
+  float l = 0.f, o0 = 0.f, o1 = 0.f;
+  if (m != neg_inf()) {
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f(rows[w][kD] - m);
+      l = fmaf(f, rows[w][kD + 1], l);
+      o0 = fmaf(f, rows[w][2 * d], o0);
+      o1 = fmaf(f, rows[w][2 * d + 1], o1);
+    }
+  }
+  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  *reinterpret_cast<uint32_t*>(out + ((long long)t.x * G + r) * kD + 2 * d) = pack_bf16x2(o0 * inv, o1 * inv);
 }
 
 int most_blocks() { return kCtasPerSm * sm_count(); }
@@ -493,8 +517,18 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   paged_decode_attn_kernel<<<grid, kThreads, smem, stream>>>(s, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (grid > 1) paged_decode_join_kernel<<<grid, kD, 0, stream>>>(s, parts, a.tails, out);
-  return cudaGetLastError();
+  if (grid == 1) return cudaSuccess;
+  // launched while the first kernel drains; it waits for that kernel's end before it reads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, s.G());
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel, s, (const float*)parts, (const int2*)a.tails, out);
 }
 
 }  // namespace oasis

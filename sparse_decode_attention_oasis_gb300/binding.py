@@ -137,14 +137,16 @@ def load(path: Optional[str] = None):
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
+    if isinstance(x, int):
+        return int(x)
     return x.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
+    if type(stream) is int:
+        return stream
     if stream is None:
         import torch
 

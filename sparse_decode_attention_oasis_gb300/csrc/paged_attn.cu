@@ -138,6 +138,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
   __shared__ int slot_pair[kWarps][2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = s.Hq / s.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;");  // the join's launch overlaps this kernel
   const int pairs = s.B * s.Hkv;
   const int per = (pairs + kThreads - 1) / kThreads;
   unsigned bits = 0;

@@ -24,13 +24,16 @@ A prompt's pass, layer by layer, and a decode step::
     cache.commit(plan)
 
 Calls run on the current stream of the tensors' device and can be captured into a CUDA
-graph; nothing is kept between calls but the tensors above.  Scratch comes from
-PyTorch's allocator in each call, so calls on two streams, and two captured graphs, never
-share it.
+graph; nothing is kept between calls but the tensors above and decode's scratch, one for
+each stream (calls on one stream follow each other).  A captured call takes scratch of its
+own from the graph's memory pool, so graphs, and calls on other streams, never share it.
+
+The methods call the library directly with addresses and sizes: for a decode step's small
+kernels the host's share of a call is what counts.
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 import math
 from typing import NamedTuple, Optional
 
@@ -41,6 +44,7 @@ from . import binding as B
 D = 128
 BS = 16
 _SCALE = 1.0 / math.sqrt(D)
+_BF16, _INT32 = torch.bfloat16, torch.int32
 
 
 class Plan(NamedTuple):
@@ -52,19 +56,31 @@ class Plan(NamedTuple):
     slot_map: torch.Tensor   # int32 [n_rows]: page * 16 + position, -1 for rows of no request
 
 
-_NO_GUARD = contextlib.nullcontext()
+class _On:
+    """`with _On(device) as stream`: the device is the current one inside; the raw handle of its
+    current stream.  Lighter than torch.cuda.device + current_stream (3 us of a 10 us call)."""
 
+    __slots__ = ("index", "back")
 
-def _device(t: torch.Tensor):
-    """The context in which t's device is the current one."""
-    if not t.is_cuda:
-        raise ValueError("CUDA tensors are needed (there is no CPU path)")
-    return _NO_GUARD if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError("CUDA tensors are needed (there is no CPU path)")
+        self.index = device.index
+
+    def __enter__(self) -> int:
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
 
 
 def _rows(name: str, t: torch.Tensor, heads: int, n: int, device) -> int:
     """Checks bf16 rows [n][heads][128], contiguous inside a row; returns the row stride."""
-    if t.dtype is not torch.bfloat16 or t.shape != (n, heads, D) or t.device != device:
+    if t.dtype is not _BF16 or t.shape != (n, heads, D) or t.device != device:
         raise ValueError(f"{name} must be bfloat16 [{n}, {heads}, {D}] on {device}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
     stride, inner, one = t.stride()
@@ -77,7 +93,7 @@ def _rows(name: str, t: torch.Tensor, heads: int, n: int, device) -> int:
 
 
 def _ints(name: str, t: torch.Tensor, shape, device) -> torch.Tensor:
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
     return t
@@ -92,19 +108,22 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: to
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [rows, heads, 128]")
     n, hq, hkv, device = q.shape[0], q.shape[1], k.shape[1], q.device
-    with _device(q):
-        strides = [_rows("q", q, hq, n, device), _rows("k", k, hkv, n, device), _rows("v", v, hkv, n, device)]
+    with _On(device) as stream:
+        qs, ks, vs = _rows("q", q, hq, n, device), _rows("k", k, hkv, n, device), _rows("v", v, hkv, n, device)
         if row_start.dim() != 1 or row_start.shape[0] < 2:
             raise ValueError("row_start must be int32 [sequences + 1]")
         _ints("row_start", row_start, row_start.shape, device)
         if err is not None:
             _ints("err", err, (1,), device)
         if out is None:
-            out = torch.zeros((n, hq, D), dtype=torch.bfloat16, device=device)
-        out_stride = _rows("out", out, hq, n, device)
+            out = torch.zeros((n, hq, D), dtype=_BF16, device=device)
         shape = B.PagedShape(row_start.shape[0] - 1, hq, hkv, D, BS, 1, 1)
-        B.oasis_prompt_attn(shape, q, strides[0], k, strides[1], v, strides[2], row_start, n,
-                            _SCALE if scale is None else float(scale), out, out_stride, err)
+        st = B.load().oasis_prompt_attn(
+            ctypes.byref(shape), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, row_start.data_ptr(), n,
+            _SCALE if scale is None else scale, out.data_ptr(), _rows("out", out, hq, n, device),
+            None if err is None else err.data_ptr(), stream)
+        if st:
+            B._check("oasis_prompt_attn", st)
     return out
 
 
@@ -126,6 +145,8 @@ class PagedKV:
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         self.device = self.kv.device
+        self._shape = ctypes.byref(self.shape)
+        self._scratch = {}  # decode's, by stream
 
     def adopt(self, **tensors: torch.Tensor) -> None:
         """Use the caller's tensors in place of kv, scale, table, free, n_free or lens (same
@@ -149,17 +170,20 @@ class PagedKV:
         n_rows = int(n_rows)
         if n_rows < 0:
             raise ValueError("n_rows must be >= 0")
-        with _device(new_len):
-            buf = torch.empty(2 * b + 2 + n_rows, dtype=torch.int32, device=self.device)
-            plan = Plan(buf[:b], buf[b:b + 1], buf[b + 1:2 * b + 2], buf[2 * b + 2:])
-            at = buf.data_ptr()
-            B.oasis_extend_tables(self.shape, self.lens, new_len, self.free, self.n_free, self.table, at, at + 4 * b,
-                                  at + 4 * (b + 1), at + 4 * (2 * b + 2), n_rows, self.err)
+        with _On(self.device) as stream:
+            # four allocations: views of one cost more on the host than the launch
+            plan = Plan(*[torch.empty(n, dtype=_INT32, device=self.device) for n in (b, 1, b + 1, n_rows)])
+            st = B.load().oasis_extend_tables(
+                self._shape, self.lens.data_ptr(), new_len.data_ptr(), self.free.data_ptr(), self.n_free.data_ptr(),
+                self.table.data_ptr(), plan.lens.data_ptr(), plan.n_free.data_ptr(), plan.row_start.data_ptr(),
+                plan.slot_map.data_ptr(), n_rows, self.err.data_ptr(), stream)
+            if st:
+                B._check("oasis_extend_tables", st)
         return plan
 
     def commit(self, plan: Plan) -> None:
         """The plan's lengths and free count become the cache's."""
-        with _device(self.lens):
+        with _On(self.device):
             self.lens.copy_(plan.lens)
             self.n_free.copy_(plan.n_free)
 
@@ -167,9 +191,10 @@ class PagedKV:
         """Requests keep their first keep_len tokens (0: the request is done); the pages of the
         others are free again."""
         _ints("keep_len", keep_len, (self.batch,), self.device)
-        with _device(keep_len):
+        with _On(self.device) as stream:
             left = torch.empty_like(self.n_free)
-            B.oasis_release_tables(self.shape, self.lens, keep_len, self.table, self.free, self.n_free, left, self.err)
+            B.oasis_release_tables(self.shape, self.lens, keep_len, self.table, self.free, self.n_free, left, self.err,
+                                   stream)
             self.n_free.copy_(left)
             kept = (keep_len >= 0) & (keep_len <= self.lens)  # the others released nothing
             self.lens.copy_(torch.where(kept, keep_len, self.lens))
@@ -179,9 +204,12 @@ class PagedKV:
         n, h = slot_map.shape[0], self.n_kv_heads
         ks, vs = _rows("k", k, h, n, self.device), _rows("v", v, h, n, self.device)
         _ints("slot_map", slot_map, (n,), self.device)
-        with _device(k):
-            B.oasis_store_kv_q8(self.shape, k, ks, v, vs, slot_map, n, self._layer(self.kv, layer),
-                                self._layer(self.scale, layer), self.err)
+        with _On(self.device) as stream:
+            st = B.load().oasis_store_kv_q8(
+                self._shape, k.data_ptr(), ks, v.data_ptr(), vs, slot_map.data_ptr(), n, self._layer(self.kv, layer),
+                self._layer(self.scale, layer), self.err.data_ptr(), stream)
+            if st:
+                B._check("oasis_store_kv_q8", st)
 
     def decode(self, q: torch.Tensor, ctx_len: Optional[torch.Tensor] = None, layer: int = 0,
                sel: Optional[torch.Tensor] = None, nsel: Optional[torch.Tensor] = None,
@@ -198,16 +226,23 @@ class PagedKV:
             most = sel.shape[2]
             _ints("sel", sel, (b, self.n_kv_heads, most), device)
             _ints("nsel", nsel, (b, self.n_kv_heads), device)
-        with _device(q):
+        with _On(device) as stream:
             if out is None:
-                out = torch.empty((b, hq, D), dtype=torch.bfloat16, device=device)
-            elif out.dtype is not torch.bfloat16 or out.shape != (b, hq, D) or out.device != device \
-                    or not out.is_contiguous():
+                out = torch.empty((b, hq, D), dtype=_BF16, device=device)
+            elif out.dtype is not _BF16 or out.shape != (b, hq, D) or out.device != device or not out.is_contiguous():
                 raise ValueError(f"out must be contiguous bfloat16 [{b}, {hq}, {D}] on {device}")
-            ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-            B.oasis_paged_decode_attn_q8(self.shape, q, stride, self._layer(self.kv, layer),
-                                         self._layer(self.scale, layer), self.table, ctx_len, sel, nsel, most,
-                                         _SCALE if scale is None else float(scale), ws, self.ws_bytes, out, self.err)
+            ws = None if torch._C._cuda_isCurrentStreamCapturing() else self._scratch.get(stream)
+            if ws is None:
+                ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+                if not torch._C._cuda_isCurrentStreamCapturing():
+                    self._scratch[stream] = ws
+            st = B.load().oasis_paged_decode_attn_q8(
+                self._shape, q.data_ptr(), stride, self._layer(self.kv, layer), self._layer(self.scale, layer),
+                self.table.data_ptr(), ctx_len.data_ptr(), None if sel is None else sel.data_ptr(),
+                None if sel is None else nsel.data_ptr(), most, _SCALE if scale is None else scale, ws.data_ptr(),
+                self.ws_bytes, out.data_ptr(), self.err.data_ptr(), stream)
+            if st:
+                B._check("oasis_paged_decode_attn_q8", st)
         return out
 
     def check(self) -> None:

@@ -36,7 +36,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kMinPages = 16;  // pages a thread block gets at least, when there are so few
+constexpr int kMinPages = 8;  // pages a thread block gets at least, when there are so few
+constexpr int kJoinWarps = 4;
+constexpr int kMaxG = 8;
 constexpr int kRowFloats = kD + 2;
 constexpr float kSlack = 8.0f;  // log2 of the largest weight
 
@@ -129,13 +131,18 @@ __device__ __forceinline__ void load_values(Rows& v, const uint8_t* page, int la
   v.v[3] = ldg_stream(p + 9 * kD);
 }
 
+struct Shared {
+  float2 top_sum[2 * kWarps][kMaxG];  // of a piece's rows
+  long long chunk_start[kThreads + 1];
+  long long warp_sums[kWarps];
+  long long slot_lo[2 * kWarps], slot_hi[2 * kWarps];
+  int slot_pair[2 * kWarps];
+};
+
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_decode_attn_kernel(PagedShape s, Args a) {
-  extern __shared__ float slots[];  // [kWarps][2][G][kRowFloats]
-  __shared__ long long chunk_start[kThreads];
-  __shared__ long long warp_sums[kWarps];
-  __shared__ long long slot_lo[kWarps][2], slot_hi[kWarps][2];
-  __shared__ int slot_pair[kWarps][2];
+  extern __shared__ __align__(16) float slot_rows[];  // [2 * kWarps][G][kD]
+  __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = s.Hq / s.Hkv;
   asm volatile("griddepcontrol.launch_dependents;");  // the join's launch overlaps this kernel
@@ -158,16 +165,17 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) warp_sums[warp] = x;
-  if (lane < 2) slot_pair[warp][lane] = -1;
+  if (lane == 31) sh.warp_sums[warp] = x;
+  if (lane < 2) sh.slot_pair[warp * 2 + lane] = -1;
   __syncthreads();
   long long total = 0, off = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    off += w < warp ? warp_sums[w] : 0;
-    total += warp_sums[w];
+    off += w < warp ? sh.warp_sums[w] : 0;
+    total += sh.warp_sums[w];
   }
-  chunk_start[tid] = off + x - n;
+  sh.chunk_start[tid] = off + x - n;
+  if (tid == 0) sh.chunk_start[kThreads] = total;
   __syncthreads();
   const long long wanted = (total + kMinPages - 1) / kMinPages;
   const int blocks = wanted < (long long)gridDim.x ? (int)wanted : (int)gridDim.x;
@@ -184,14 +192,18 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     int i = 0, j = kThreads - 1;
     while (i < j) {
       const int m = (i + j + 1) >> 1;
-      if (chunk_start[m] <= w_lo) i = m; else j = m - 1;
+      if (sh.chunk_start[m] <= w_lo) i = m; else j = m - 1;
     }
     int e = i * per;
-    long long e_lo = chunk_start[i];
-    int count = pair_pages(s, a, e, &bits);
+    long long e_lo = sh.chunk_start[i];
+    // with one pair to a chunk the prefix holds its pages
+    auto pages_of = [&](int pair) {
+      return per == 1 ? (int)(sh.chunk_start[pair + 1] - sh.chunk_start[pair]) : pair_pages(s, a, pair, &bits);
+    };
+    int count = pages_of(e);
     while (e_lo + count <= w_lo) {
       e_lo += count;
-      count = pair_pages(s, a, ++e, &bits);
+      count = pages_of(++e);
     }
     long long p = w_lo;
     while (true) {
@@ -200,21 +212,19 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
       const int nb = (ctx + kBS - 1) / kBS;
       const int first = (int)(p - e_lo), last = (int)min((long long)count, w_hi - e_lo);  // pages of the pair
 
-      // ---- the query rows, lane / 4 their number
       uint32_t qf[16];
       float fac[2];
       {
-        const int g = lane >> 2;
         uint4 w[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
-        if (g < G) {
-          const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + g) * kD + (lane & 3) * 16;
-          w[0] = ldg_nc(src);
-          w[1] = ldg_nc(src + 8);
-          w[2] = ldg_nc(src + 64);
-          w[3] = ldg_nc(src + 72);
-        }
+      for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
+      if ((lane >> 2) < G) {
+        const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * 16;
+        w[0] = ldg_nc(src);
+        w[1] = ldg_nc(src + 8);
+        w[2] = ldg_nc(src + 64);
+        w[3] = ldg_nc(src + 72);
+      }
         uint32_t m = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -237,8 +247,6 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
       }
 
-      State st;
-      st.clear();
       Rows kr, vr;
       int my_page = -1, my_valid = 0;  // of page (group of 32) + lane
       float2 my_scale = make_float2(1.f, 1.f);
@@ -276,6 +284,8 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         load_keys(kr, head_page(page), lane);
         load_values(vr, head_page(page), lane);
       }
+      State st;
+      st.clear();
       for (int at = first; at < last; ++at) {
         const int in = (at - first) & 31;
         const int valid = __shfl_sync(0xffffffffu, my_valid, in);
@@ -358,7 +368,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         st.sum[1] += __shfl_xor_sync(0xffffffffu, st.sum[1], o);
       }
       const bool whole = first == 0 && last == count;
-      const int which = first == 0 ? 1 : 0;
+      const int which = first == 0 ? 1 : 0, slot = warp * 2 + which;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = (lane & 3) * 2 + i;
@@ -372,81 +382,82 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
           dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
           dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-          float* row = slots + ((warp * 2 + which) * G + r) * kRowFloats;
+          float* row = slot_rows + ((size_t)slot * G + r) * kD + (lane >> 2) * 16;
 #pragma unroll
-          for (int m = 0; m < 8; ++m)
-            *reinterpret_cast<float2*>(row + (lane >> 2) * 16 + 2 * m) = make_float2(st.acc[m][i], st.acc[m][2 + i]);
-          if (lane < 4) *reinterpret_cast<float2*>(row + kD) = make_float2(st.top[i], st.sum[i]);
+          for (int m = 0; m < 8; m += 2)
+            *reinterpret_cast<float4*>(row + 2 * m) =
+                make_float4(st.acc[m][i], st.acc[m][2 + i], st.acc[m + 1][i], st.acc[m + 1][2 + i]);
+          if (lane < 4) sh.top_sum[slot][r] = make_float2(st.top[i], st.sum[i]);
         }
       }
       if (!whole && lane == 0) {
-        slot_pair[warp][which] = e;
-        slot_lo[warp][which] = e_lo;
-        slot_hi[warp][which] = e_lo + count;
+        sh.slot_pair[slot] = e;
+        sh.slot_lo[slot] = e_lo;
+        sh.slot_hi[slot] = e_lo + count;
       }
       p = e_lo + last;
       if (p >= w_hi) break;
       do {
         e_lo += count;
-        count = pair_pages(s, a, ++e, &bits);
+        count = pages_of(++e);
       } while (count == 0);
     }
   }
   set_err(a.err, bits);
   __syncthreads();
 
-  // ---- join the warps' pieces of a pair
+  // ---- join the warps' pieces: a row of a pair to a warp, four dimensions to a lane
+  const int my_pair = lane < 2 * kWarps ? sh.slot_pair[lane] : -1;
+  const unsigned same = __match_any_sync(0xffffffffu, my_pair);
+  const unsigned leads = __ballot_sync(0xffffffffu, my_pair >= 0 && __ffs(same) - 1 == lane);
+  const int units = __popc(leads) * G;
   int2 tail = make_int2(-1, 0);
-  for (int i = 0; i < 2 * kWarps;) {
-    const int e = slot_pair[i >> 1][i & 1];
-    if (e < 0) {
-      ++i;
-      continue;
-    }
-    int end = i + 1;
-    while (end < 2 * kWarps && (slot_pair[end >> 1][end & 1] == e || slot_pair[end >> 1][end & 1] < 0)) ++end;
-    const long long e_lo = slot_lo[i >> 1][i & 1], e_hi = slot_hi[i >> 1][i & 1];
-    const bool whole = e_lo >= c_lo && e_hi <= c_hi;
-    float* part = a.parts + ((long long)blockIdx.x * 2 + (e_lo >= c_lo ? 1 : 0)) * G * kRowFloats;
-    for (int idx = tid; idx < G * (kD / 2); idx += kThreads) {
-      const int r = idx / (kD / 2), d = idx % (kD / 2) * 2;
-      float top = neg_inf();
-      for (int j = i; j < end; ++j)
-        if (slot_pair[j >> 1][j & 1] == e) top = fmaxf(top, slots[(j * G + r) * kRowFloats + kD]);
-      float sum = 0.f, o0 = 0.f, o1 = 0.f;
-      if (top != neg_inf()) {
-        for (int j = i; j < end; ++j) {
-          if (slot_pair[j >> 1][j & 1] != e) continue;
-          const float* row = slots + (j * G + r) * kRowFloats;
-          const float f = exp2f(row[kD] - top);
-          sum = fmaf(f, row[kD + 1], sum);
-          o0 = fmaf(f, row[d], o0);
-          o1 = fmaf(f, row[d + 1], o1);
-        }
-      }
-      if (whole) {
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        *reinterpret_cast<uint32_t*>(a.out + ((long long)e * G + r) * kD + d) = pack_bf16x2(o0 * inv, o1 * inv);
-      } else {
-        *reinterpret_cast<float2*>(part + r * kRowFloats + d) = make_float2(o0, o1);
-        if (d == 0) *reinterpret_cast<float2*>(part + r * kRowFloats + kD) = make_float2(top, sum);
-      }
-    }
-    if (e_lo >= c_lo && e_hi > c_hi) {
-      // its last piece is in the last block whose range starts before e_hi
-      tail = make_int2(e, (int)((e_hi * blocks + total - 1) / total - 1));
-    }
-    i = end;
+  if (leads) {  // only the last pair can go on in the next block
+    const int lead = 31 - __clz(leads);
+    const long long e_hi = sh.slot_hi[lead];
+    // its last piece is in the last block whose range starts before e_hi
+    if (sh.slot_lo[lead] >= c_lo && e_hi > c_hi)
+      tail = make_int2(sh.slot_pair[lead], (int)((e_hi * blocks + total - 1) / total - 1));
   }
   if (tid == 0) a.tails[blockIdx.x] = tail;
+  for (int u = warp; u < units; u += kWarps) {
+    const int lead = __fns(leads, 0, u / G + 1), r = u % G;
+    const unsigned mask = __shfl_sync(0xffffffffu, same, lead);
+    const float2 ts = mask >> lane & 1 ? sh.top_sum[lane][r] : make_float2(neg_inf(), 0.f);
+    const float top = warp_max(ts.x);
+    const float f = ts.x == neg_inf() ? 0.f : exp2f(ts.x - top);
+    const float sum = warp_sum(f * ts.y);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (unsigned left = mask; left; left &= left - 1) {
+      const int j = __ffs(left) - 1;
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float4 v = reinterpret_cast<const float4*>(slot_rows + ((size_t)j * G + r) * kD)[lane];
+      o.x = fmaf(fj, v.x, o.x);
+      o.y = fmaf(fj, v.y, o.y);
+      o.z = fmaf(fj, v.z, o.z);
+      o.w = fmaf(fj, v.w, o.w);
+    }
+    const int e = sh.slot_pair[lead];
+    const bool starts = sh.slot_lo[lead] >= c_lo;
+    if (starts && sh.slot_hi[lead] <= c_hi) {
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+      reinterpret_cast<uint2*>(a.out + ((long long)e * G + r) * kD)[lane] =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    } else {
+      float* row = a.parts + (((long long)blockIdx.x * 2 + (starts ? 1 : 0)) * G + r) * kRowFloats;
+      *reinterpret_cast<float2*>(row + lane * 4) = make_float2(o.x, o.y);
+      *reinterpret_cast<float2*>(row + lane * 4 + 2) = make_float2(o.z, o.w);
+      if (lane == 0) *reinterpret_cast<float2*>(row + kD) = make_float2(top, sum);
+    }
+  }
 }
 
 // Joins the pieces of a pair that starts in block blockIdx.x and ends in a later one, one query
 // row to a thread block: its warps take every kWarps-th piece, a lane four dimensions.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const int2* __restrict__ tails,
                          uint16_t* __restrict__ out) {
-  __shared__ float rows[kWarps][kRowFloats];
+  __shared__ float rows[kJoinWarps][kRowFloats];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = s.Hq / s.Hkv, r = blockIdx.y, first = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
@@ -455,7 +466,7 @@ paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const in
   const int n = t.y - first + 1;
   float top = neg_inf(), sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int c = warp; c < n; c += kWarps) {
+  for (int c = warp; c < n; c += kJoinWarps) {
     const float* row = parts + (((long long)first + c) * 2 + (c == 0 ? 1 : 0)) * G * kRowFloats + r * kRowFloats;
     const float2 ml = *reinterpret_cast<const float2*>(row + kD);
     const float2 a = *reinterpret_cast<const float2*>(row + lane * 4), b = *reinterpret_cast<const float2*>(row + lane * 4 + 2);
@@ -477,10 +488,10 @@ paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const in
   const int d = threadIdx.x;
   if (d >= kD / 2) return;
   float m = neg_inf();
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, rows[w][kD]);
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, rows[w][kD]);
   float l = 0.f, o0 = 0.f, o1 = 0.f;
   if (m != neg_inf()) {
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
       const float f = exp2f(rows[w][kD] - m);
       l = fmaf(f, rows[w][kD + 1], l);
       o0 = fmaf(f, rows[w][2 * d], o0);
@@ -511,7 +522,7 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   float* parts = static_cast<float*>(ws);
   Args a{q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, scale * 1.4426950408889634f, parts,
          reinterpret_cast<int2*>(parts + (size_t)most * 2 * s.G() * kRowFloats), out, err};
-  const size_t smem = (size_t)kWarps * 2 * s.G() * kRowFloats * sizeof(float);
+  const size_t smem = (size_t)2 * kWarps * s.G() * kD * sizeof(float);
   static int attr_cache[kMaxDevicesCached] = {};
   cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel, smem, attr_cache);
   if (e != cudaSuccess) return e;
@@ -522,7 +533,7 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   // launched while the first kernel drains; it waits for that kernel's end before it reads
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, s.G());
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

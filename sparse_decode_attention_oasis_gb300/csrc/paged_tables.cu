@@ -61,9 +61,10 @@ __device__ __forceinline__ Growth growth(const PagedShape& s, const int* old_len
 }
 
 struct RowSpan {  // a request with rows in this thread block's range
-  long long first;  // its first row in the call
+  int first;   // its first row, from the range's start (negative: before it)
   int b;
-  int page0;  // its first page's place in the call, -1: the request got nothing
+  int held;    // tokens that it holds
+  int page0;   // its first new page's place in the call, -1: the request got nothing
 };
 
 __global__ void __launch_bounds__(kThreads)
@@ -122,7 +123,7 @@ extend_tables_kernel(PagedShape s, const int* __restrict__ old_len, const int* _
       const int n = g.new_len - g.old_len;
       if (n > 0 && rw < hi && rw + n > lo) {
         const bool ok = !(g.need > 0 && nd + g.need > n_free) && rw + n <= n_rows;
-        spans[at++] = RowSpan{rw, b, ok ? (int)min(nd, (long long)n_free) : -1};
+        spans[at++] = RowSpan{(int)(rw - lo), b, g.old_len, ok ? (int)nd : -1};
       }
       nd += g.need;
       rw += n;
@@ -140,9 +141,16 @@ extend_tables_kernel(PagedShape s, const int* __restrict__ old_len, const int* _
     row_start[s.B] = (int)min(rows_all, (long long)n_rows);
   }
 
-  for (long long r = lo + tid; r < hi; r += kThreads) {
-    int slot = -1;
-    if (r < rows_all) {
+  // this block's rows, all of a thread's loads on their way before the first is used
+  constexpr int kEach = kRowsPerCta / kThreads;
+  const int rows_here = (int)max(0LL, min(hi, rows_all) - lo);  // of requests; the others get -1
+  int page[kEach], pos[kEach], entry[kEach];
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int r = tid + q * kThreads;
+    page[q] = -1;
+    entry[q] = -2;  // no row of a request that got its pages
+    if (r < rows_here) {
       int i = 0, j = (int)listed - 1;  // the last span that starts at or before r
       while (i < j) {
         const int m = (i + j + 1) >> 1;
@@ -150,21 +158,27 @@ extend_tables_kernel(PagedShape s, const int* __restrict__ old_len, const int* _
       }
       const RowSpan sp = spans[i];
       if (sp.page0 >= 0) {
-        const int held_tokens = old_len[sp.b];
-        const int pos = held_tokens + (int)(r - sp.first);
-        const int x = pos / kBS;
-        const int held = (int)(((long long)held_tokens + kBS - 1) / kBS);
-        int* entry = table + (long long)sp.b * s.nb_max + x;
-        int page = x < held ? *entry : free_pages[n_free - 1 - (sp.page0 + x - held)];
-        if (page < 0 || page >= s.n_pages) {
-          page = -1;
-          bits |= OASIS_EW_BAD_BLOCK;
-        }
-        if (x >= held && pos % kBS == 0) *entry = page;
-        if (page >= 0) slot = page * kBS + pos % kBS;
+        pos[q] = sp.held + r - sp.first;
+        const int x = pos[q] / kBS, held = (int)(((long long)sp.held + kBS - 1) / kBS);
+        const bool fresh = x >= held;
+        page[q] = fresh ? free_pages[n_free - 1 - (sp.page0 + x - held)] : table[(long long)sp.b * s.nb_max + x];
+        entry[q] = fresh && pos[q] % kBS == 0 ? sp.b : -1;  // the row that writes the new block's entry
       }
     }
-    slot_map[r] = slot;
+  }
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int r = tid + q * kThreads;
+    int slot = -1;
+    if (entry[q] != -2) {
+      if (page[q] < 0 || page[q] >= s.n_pages) {
+        page[q] = -1;
+        bits |= OASIS_EW_BAD_BLOCK;
+      }
+      if (entry[q] >= 0) table[(long long)entry[q] * s.nb_max + pos[q] / kBS] = page[q];
+      if (page[q] >= 0) slot = page[q] * kBS + pos[q] % kBS;
+    }
+    if (lo + r < hi) slot_map[lo + r] = slot;
   }
   set_err(err, bits);
 }

@@ -76,7 +76,8 @@ store_kv_q8_kernel(PagedShape s, const uint16_t* __restrict__ k, size_t k_stride
     const int slot_a = __shfl_sync(0xffffffffu, slot, first);
     const int page = slot_a / kBS, pos = slot_a % kBS;
     // its length: rows in consecutive positions up to the page's end
-    const int next = row_a + lane < n_rows ? slot_map[row_a + lane] : -1;
+    int next = __shfl_sync(0xffffffffu, slot, (first + lane) & 31);
+    if (first + kBS > 32) next = row_a + lane < n_rows ? slot_map[row_a + lane] : -1;  // not all of them are at hand
     const unsigned cont = __ballot_sync(0xffffffffu, lane < kBS - pos && next == slot_a + lane);
     const int len = __ffs(~cont) - 1;
 

@@ -19,8 +19,10 @@
 //   warps 0..3, 4..7  softmax of row tile 0 and 1: one row to a thread, its 128 scores read
 //                     from TMEM, the weights written back to TMEM in bf16 over the scores,
 //                     the output row at the end;
-//   warp 8            one lane issues the MMAs, S_i = Q_i K_j^T, then O_i += P_i V_j with P_i from
-//                     TMEM.  While one tile's softmax runs, the tensor cores work for the other;
+//   warps 8, 11       one lane each issues the MMAs of row tile 0 and 1: S_i = Q_i K_j^T, then O_i += P_i V_j
+//                     with P_i from TMEM.  While one tile's softmax runs, the tensor cores work for the
+//                     other.  One issuing warp for both tiles was the bottleneck: about 70 cycles an MMA
+//                     of 64, and the waits between them;
 //   warp 9            TMA producer: Q tiles, and K and V tiles of 128 tokens in a ring of 5;
 //   warp 10           scheduler: finds this block's work items and hands them to the others.
 // TMEM: two S/P and two O tiles of 128 columns, all 512.  Shared memory: 64 KB of Q and a ring
@@ -44,7 +46,7 @@ constexpr int kItems = 4;                    // items that the scheduler may be 
 constexpr int kThreads = 384;
 // 168 registers a thread at launch (64,512 in all): 8 warps of 208 and 4 of 88 use them up
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr int kConsumers = 10;               // warps that read an item: softmax, MMA, producer
+constexpr int kConsumers = 11;               // warps that read an item: softmax, MMA, producer
 constexpr float kSlack = 8.0f;
 
 struct Item {
@@ -59,7 +61,7 @@ struct Bars {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t tail, done;
+  uint64_t tail, done[2];
   Item items[kItems];
   uint32_t tmem_base;
   int abort_flag;
@@ -276,14 +278,15 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_empty[i], 1);
+      mbar_init(&bars->kv_empty[i], 2);  // both tiles' MMAs
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
       mbar_init(&bars->item_empty[i], kConsumers);
     }
     mbar_init(&bars->tail, 1);
-    mbar_init(&bars->done, 1);
+    mbar_init(&bars->done[0], 1);
+    mbar_init(&bars->done[1], 1);
     bars->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -438,65 +441,74 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
-  if (warp == 8) {
-    // ------------------------------------------------------------ MMA issuer
+  if (warp == 8 || warp == 11) {
+    // ------------------------------------------------------------ MMA issuer of one row tile
+    const int i = warp == 8 ? 0 : 1;
     const uint32_t id_s = instr_desc(kTile), id_o = instr_desc(kTile) | (1u << 16);
-    const uint32_t q0 = smem_u32(smem), kv0 = smem_u32(ring);
-    unsigned slot = 0;                      // ring position of K_j: slots are used in the order K_0 V_0 K_1 V_1 ..
-    unsigned q_uses[2] = {0, 0}, turns[2] = {0, 0};  // Q tiles, S tiles so far
+    const uint32_t q_low = qk_desc_low(smem_u32(smem) + (uint32_t)i * kTileBytes), kv0 = smem_u32(ring);
+    const uint32_t s_addr = tmem + (uint32_t)i * 128, o_addr = tmem + 256u + (uint32_t)i * 128;
+    unsigned ks = 0, k_phase = 0;   // ring place of K_j and its phase; V_j follows in the next place
+    unsigned vs = 0, v_phase = 0;   // of V_(j-1)
+    unsigned items = 0, turns = 0;  // Q tiles, S tiles so far
     Item it;
     for (int k = 0; take(k, it) && !timed_out; ++k) {
-      const int n0 = kv_tiles(it, 0, per), n1 = kv_tiles(it, 1, per);
-      const int n = max(n0, n1);
+      const int ni = kv_tiles(it, i, per), n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
       // the whole warp walks and waits, so that the operands stay warp-uniform; one lane issues
-      for (int j = 0; j <= n && !timed_out; ++j) {
-        const unsigned ks = (slot + 2 * j) % kRing, vs = (slot + 2 * j - 1) % kRing;  // K_j, V_(j-1)
-        if (j < n) timed_out |= !wait_all(&bars->kv_full[ks], ((slot + 2 * j) / kRing) & 1);
-        if (j > 0) timed_out |= !wait_all(&bars->kv_full[vs], ((slot + 2 * j - 1) / kRing) & 1);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int ni = i ? n1 : n0;
-          const uint32_t s_addr = tmem + (uint32_t)i * 128, o_addr = tmem + 256u + (uint32_t)i * 128;
-          if (j > 0 && j <= ni && !timed_out) {
-            timed_out |= !wait_all(&bars->p_full[i], (turns[i] - 1) & 1);
-            tc_fence_after();
-            const uint32_t vb = v_desc_low(kv0 + vs * kTileBytes);
-            if (!timed_out && elect_one()) {
+      for (int j = 0; j <= n; ++j) {
+        // also for tiles that this row tile does not read: their places are given back in step with the ring
+        if (j == 0 && ni > 0) timed_out |= !wait_all(&bars->q_full[i], items++ & 1);
+        if (j < n) timed_out |= !wait_all(&bars->kv_full[ks], k_phase);
+        if (j > 0) timed_out |= !wait_all(&bars->kv_full[vs], v_phase);
+        if (j > 0 && j <= ni) timed_out |= !wait_all(&bars->p_full[i], (turns - 1) & 1);
+        if (timed_out) break;
+        tc_fence_after();
+        const uint32_t vb = v_desc_low(kv0 + vs * kTileBytes), kb = qk_desc_low(kv0 + ks * kTileBytes);
+        if (elect_one()) {
+          if (j > 0) {
+            if (j <= ni) {
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
               if (j == ni) mma_commit(&bars->o_full[i]);
+              mma_commit(&bars->kv_empty[vs]);
+            } else {
+              mbar_arrive(&bars->kv_empty[vs]);  // a tile that this row tile does not read
             }
-            __syncwarp();
           }
-          if (j < ni && !timed_out) {
-            if (j == 0) timed_out |= !wait_all(&bars->q_full[i], q_uses[i]++ & 1);
-            tc_fence_after();
-            const uint32_t qb = qk_desc_low(q0 + (uint32_t)i * kTileBytes), kb = qk_desc_low(kv0 + ks * kTileBytes);
-            if (!timed_out && elect_one()) {
+          if (j < ni) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
-                mma_ss(s_addr, qb + off, kb + off, id_s, kk > 0);
-              }
-              mma_commit(&bars->s_full[i]);
-              if (j == ni - 1) mma_commit(&bars->q_empty[i]);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+              mma_ss(s_addr, q_low + off, kb + off, id_s, kk > 0);
             }
-            __syncwarp();
-            ++turns[i];
+            mma_commit(&bars->s_full[i]);
+            if (j == ni - 1) mma_commit(&bars->q_empty[i]);
+            mma_commit(&bars->kv_empty[ks]);
+          } else if (j < n) {
+            mbar_arrive(&bars->kv_empty[ks]);
           }
-        }
-        if (!timed_out && elect_one()) {
-          if (j > 0) mma_commit(&bars->kv_empty[vs]);
-          if (j < n) mma_commit(&bars->kv_empty[ks]);
         }
         __syncwarp();
+        if (j < ni) ++turns;
+        if (j < n) {  // K_j, then V_j, then K_(j+1)
+          vs = ks;
+          v_phase = k_phase;
+          if (++vs == kRing) {
+            vs = 0;
+            v_phase ^= 1;
+          }
+          ks = vs;
+          k_phase = v_phase;
+          if (++ks == kRing) {
+            ks = 0;
+            k_phase ^= 1;
+          }
+        }
       }
-      slot += 2 * n;
     }
-    // nothing of this block is in flight on the tensor cores when it leaves
-    if (elect_one()) mma_commit(&bars->done);
+    // nothing of this warp is in flight on the tensor cores when it leaves
+    if (elect_one()) mma_commit(&bars->done[i]);
     __syncwarp();
-    mbar_drain(&bars->done, 0);
+    mbar_drain(&bars->done[i], 0);
   } else if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
     unsigned slot = 0, q_uses[2] = {0, 0}, tails = 0;

@@ -59,7 +59,7 @@ struct Item {
 struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kRing], kv_empty[kRing];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: the weights of a tile's first and second 64 tokens
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t tail, done[2];
   Item items[kItems];
@@ -273,7 +273,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->p_full[i][0], 4);
+      mbar_init(&bars->p_full[i][1], 4);
       mbar_init(&bars->o_full[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -399,13 +400,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
           sum_b = add2(sum_b, pack2(d, e));
           x[c / 2] = pack_bf16x2(a, b);
           x[c / 2 + 1] = pack_bf16x2(d, e);
-          if (c == 60) tmem_st32(s_addr, x);
+          if (c % 64 == 60) {  // the product with the first 64 tokens starts while the others' weights are formed
+            tmem_st32(s_addr + c / 64 * 32, x + c / 64 * 32);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[i][c / 64]);
+          }
         }
-        tmem_st32(s_addr + 32, x + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[i]);
       }
       if (timed_out) break;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full[i], outputs & 1, abort_flag))) {
@@ -459,15 +461,25 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (j == 0 && ni > 0) timed_out |= !wait_all(&bars->q_full[i], items++ & 1);
         if (j < n) timed_out |= !wait_all(&bars->kv_full[ks], k_phase);
         if (j > 0) timed_out |= !wait_all(&bars->kv_full[vs], v_phase);
-        if (j > 0 && j <= ni) timed_out |= !wait_all(&bars->p_full[i], (turns - 1) & 1);
+        const uint32_t vb = v_desc_low(kv0 + vs * kTileBytes), kb = qk_desc_low(kv0 + ks * kTileBytes);
+        if (j > 0 && j <= ni) {
+          timed_out |= !wait_all(&bars->p_full[i][0], (turns - 1) & 1);
+          if (timed_out) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
+          }
+          __syncwarp();
+          timed_out |= !wait_all(&bars->p_full[i][1], (turns - 1) & 1);
+        }
         if (timed_out) break;
         tc_fence_after();
-        const uint32_t vb = v_desc_low(kv0 + vs * kTileBytes), kb = qk_desc_low(kv0 + ks * kTileBytes);
         if (elect_one()) {
           if (j > 0) {
             if (j <= ni) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
+              for (int kk = 4; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, true);
               if (j == ni) mma_commit(&bars->o_full[i]);
               mma_commit(&bars->kv_empty[vs]);
             } else {

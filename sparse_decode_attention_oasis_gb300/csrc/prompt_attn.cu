@@ -121,6 +121,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -329,6 +335,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lanes + (uint32_t)i * 128, o_addr = tmem + lanes + 256u + (uint32_t)i * 128;
     const int g = row % G, tok_in = row / G;
+    const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
     unsigned turn = 0, outputs = 0;
     Item it;
     for (int k = 0; take(k, it); ++k) {
@@ -429,13 +436,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tmem_ld32(o_addr + c, o);
         tmem_wait_ld();
         if (live) {
+          uint32_t w[16];
 #pragma unroll
-          for (int q = 0; q < 32; q += 8)
-            *reinterpret_cast<uint4*>(dst + c + q) =
-                make_uint4(pack_bf16x2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv),
-                           pack_bf16x2(__uint_as_float(o[q + 2]) * inv, __uint_as_float(o[q + 3]) * inv),
-                           pack_bf16x2(__uint_as_float(o[q + 4]) * inv, __uint_as_float(o[q + 5]) * inv),
-                           pack_bf16x2(__uint_as_float(o[q + 6]) * inv, __uint_as_float(o[q + 7]) * inv));
+          for (int q = 0; q < 16; ++q) w[q] = pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
+          if (sectors) {  // whole 32-byte sectors to an instruction
+            store32(dst + c, w);
+            store32(dst + c + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; q += 4)
+              *reinterpret_cast<uint4*>(dst + c + 2 * q) = make_uint4(w[q], w[q + 1], w[q + 2], w[q + 3]);
+          }
         }
       }
       tc_fence_before();

@@ -21,8 +21,9 @@
 //                     the output row at the end;
 //   warps 8, 11       one lane each issues the MMAs of row tile 0 and 1: S_i = Q_i K_j^T, then O_i += P_i V_j
 //                     with P_i from TMEM.  While one tile's softmax runs, the tensor cores work for the
-//                     other.  One issuing warp for both tiles was the bottleneck: about 70 cycles an MMA
-//                     of 64, and the waits between them;
+//                     other.  The issuing lane's instructions are on the critical path: with one warp for
+//                     both tiles and general loops a pair of tiles took 3,200 cycles, so it now is a warp for
+//                     each tile, one lane from end to end, and loops without a condition to spare;
 //   warp 9            TMA producer: Q tiles, and K and V tiles of 128 tokens in a ring of 5;
 //   warp 10           scheduler: finds this block's work items and hands them to the others.
 // TMEM: two S/P and two O tiles of 128 columns, all 512.  Shared memory: 64 KB of Q and a ring
@@ -345,7 +346,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       float ref = 0.f;
       uint64_t sum_a = 0, sum_b = 0;
       for (int j = 0; j < n; ++j, ++turn) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[i], turn & 1, abort_flag))) {
+        if (!wait_all(&bars->s_full[i], turn & 1)) {
           timed_out = true;
           break;
         }
@@ -417,7 +418,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
       }
       if (timed_out) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full[i], outputs & 1, abort_flag))) {
+      if (!wait_all(&bars->o_full[i], outputs & 1)) {
         timed_out = true;
         break;
       }
@@ -455,83 +456,85 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
   if (warp == 8 || warp == 11) {
-    // ------------------------------------------------------------ MMA issuer of one row tile
+    // ------------------------------------------------------------ MMA issuer of one row tile: one lane
     const int i = warp == 8 ? 0 : 1;
     const uint32_t id_s = instr_desc(kTile), id_o = instr_desc(kTile) | (1u << 16);
     const uint32_t q_low = qk_desc_low(smem_u32(smem) + (uint32_t)i * kTileBytes), kv0 = smem_u32(ring);
     const uint32_t s_addr = tmem + (uint32_t)i * 128, o_addr = tmem + 256u + (uint32_t)i * 128;
-    unsigned ks = 0, k_phase = 0;   // ring place of K_j and its phase; V_j follows in the next place
-    unsigned vs = 0, v_phase = 0;   // of V_(j-1)
-    unsigned items = 0, turns = 0;  // Q tiles, S tiles so far
-    Item it;
-    for (int k = 0; take(k, it) && !timed_out; ++k) {
-      const int ni = kv_tiles(it, i, per), n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
-      // the whole warp walks and waits, so that the operands stay warp-uniform; one lane issues
-      for (int j = 0; j <= n; ++j) {
-        // also for tiles that this row tile does not read: their places are given back in step with the ring
-        if (j == 0 && ni > 0) timed_out |= !wait_all(&bars->q_full[i], items++ & 1);
-        if (j < n) timed_out |= !wait_all(&bars->kv_full[ks], k_phase);
-        if (j > 0) timed_out |= !wait_all(&bars->kv_full[vs], v_phase);
-        const uint32_t vb = v_desc_low(kv0 + vs * kTileBytes), kb = qk_desc_low(kv0 + ks * kTileBytes);
-        if (j > 0 && j <= ni) {
-          timed_out |= !wait_all(&bars->p_full[i][0], (turns - 1) & 1);
-          if (timed_out) break;
-          tc_fence_after();
-          if (elect_one()) {
+    if (elect_one()) {
+      unsigned at = 0, phase = 0;     // ring place of the next K or V tile (K_0 V_0 K_1 V_1 ..), and its phase
+      unsigned items = 0, turns = 0;  // Q tiles, S tiles so far
+      auto advance = [&] {
+        if (++at == kRing) {
+          at = 0;
+          phase ^= 1;
+        }
+      };
+      auto ready = [&](uint64_t* bar, uint32_t parity) {
+        timed_out |= !mbar_wait(bar, parity, abort_flag);
+        return !timed_out;
+      };
+      auto scores = [&](uint32_t place) {  // S = Q K^T
+        const uint32_t kb = qk_desc_low(kv0 + place * kTileBytes);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
+          mma_ss(s_addr, q_low + off, kb + off, id_s, kk > 0);
+        }
+        mma_commit(&bars->s_full[i]);
+      };
+      for (int k = 0;; ++k) {
+        const int st = k % kItems;
+        if (!ready(&bars->item_full[st], (k / kItems) & 1)) break;
+        const Item it = bars->items[st];
+        mbar_arrive(&bars->item_empty[st]);
+        if (it.row0 < 0) break;
+        const int ni = kv_tiles(it, i, per), n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
+        if (ni > 0) {
+          if (!ready(&bars->q_full[i], items++ & 1) || !ready(&bars->kv_full[at], phase)) break;
+          tc_fence_after();
+          scores(at);
+          if (ni == 1) mma_commit(&bars->q_empty[i]);
+          mma_commit(&bars->kv_empty[at]);
+          advance();
+        }
+        for (int j = 1; j <= ni; ++j) {  // P_(j-1) V_(j-1), then S_j
+          const uint32_t v_at = at, v_phase = phase;
+          advance();
+          const uint32_t vb = v_desc_low(kv0 + v_at * kTileBytes), p_phase = turns & 1;
+          ++turns;
+          if (!ready(&bars->kv_full[v_at], v_phase) || (j < ni && !ready(&bars->kv_full[at], phase)) ||
+              !ready(&bars->p_full[i][0], p_phase))
+            break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
+          if (!ready(&bars->p_full[i][1], p_phase)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, true);
+          if (j < ni) {
+            scores(at);
+            if (j == ni - 1) mma_commit(&bars->q_empty[i]);
+            mma_commit(&bars->kv_empty[at]);
+            advance();
+          } else {
+            mma_commit(&bars->o_full[i]);
           }
-          __syncwarp();
-          timed_out |= !wait_all(&bars->p_full[i][1], (turns - 1) & 1);
+          mma_commit(&bars->kv_empty[v_at]);
+        }
+        // tiles that this row tile does not read: their places are given back in step with the ring
+        for (int t = 2 * ni; t < 2 * n && !timed_out; ++t) {
+          if (ready(&bars->kv_full[at], phase)) mbar_arrive(&bars->kv_empty[at]);
+          advance();
         }
         if (timed_out) break;
-        tc_fence_after();
-        if (elect_one()) {
-          if (j > 0) {
-            if (j <= ni) {
-#pragma unroll
-              for (int kk = 4; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, true);
-              if (j == ni) mma_commit(&bars->o_full[i]);
-              mma_commit(&bars->kv_empty[vs]);
-            } else {
-              mbar_arrive(&bars->kv_empty[vs]);  // a tile that this row tile does not read
-            }
-          }
-          if (j < ni) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = ((uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u) >> 4;
-              mma_ss(s_addr, q_low + off, kb + off, id_s, kk > 0);
-            }
-            mma_commit(&bars->s_full[i]);
-            if (j == ni - 1) mma_commit(&bars->q_empty[i]);
-            mma_commit(&bars->kv_empty[ks]);
-          } else if (j < n) {
-            mbar_arrive(&bars->kv_empty[ks]);
-          }
-        }
-        __syncwarp();
-        if (j < ni) ++turns;
-        if (j < n) {  // K_j, then V_j, then K_(j+1)
-          vs = ks;
-          v_phase = k_phase;
-          if (++vs == kRing) {
-            vs = 0;
-            v_phase ^= 1;
-          }
-          ks = vs;
-          k_phase = v_phase;
-          if (++ks == kRing) {
-            ks = 0;
-            k_phase ^= 1;
-          }
-        }
       }
+      // nothing of this tile is in flight on the tensor cores when it leaves
+      mma_commit(&bars->done[i]);
+      mbar_drain(&bars->done[i], 0);
     }
-    // nothing of this warp is in flight on the tensor cores when it leaves
-    if (elect_one()) mma_commit(&bars->done[i]);
-    __syncwarp();
-    mbar_drain(&bars->done[i], 0);
+    timed_out = __any_sync(0xffffffffu, timed_out);
   } else if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
     unsigned slot = 0, q_uses[2] = {0, 0}, tails = 0;

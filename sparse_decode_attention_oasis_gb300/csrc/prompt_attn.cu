@@ -174,6 +174,7 @@ struct Schedule {
   int lane;
   bool sorted;
   int n[kKept];                     // items of sequence lane + 32 i
+  int first[kKept], end[kKept];     // its rows
   int most;                         // the most items of a sequence
   int window;                       // unsorted: first sequence of the window, items before it
   long long before;
@@ -203,6 +204,8 @@ struct Schedule {
       for (int i = 0; i < kKept; ++i) {
         const int b = lane + 32 * i;
         n[i] = b < B ? items_of(b, true) : 0;
+        first[i] = b < B ? row_start[b] : 0;
+        end[i] = b < B ? row_start[b + 1] : 0;
         most = max(most, n[i]);
       }
       most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
@@ -214,8 +217,8 @@ struct Schedule {
     for (int i = 0; i < kKept; ++i) c += max(n[i] - level, 0);
     return __reduce_add_sync(0xffffffffu, c);
   }
-  // Sequence and place of item idx (calls with rising idx); false: there are no more.
-  __device__ bool find(long long idx, int& b, int& place) {
+  // Rows a .. z - 1 of the sequence of item idx, and its place there (calls with rising idx); false: there are no more.
+  __device__ bool find(long long idx, int& a, int& z, int& place) {
     if (sorted) {
       if (idx >= at_or_above(0)) return false;
       int lo = 0, hi = most - 1;  // the highest level with more than idx items at or above it
@@ -223,17 +226,19 @@ struct Schedule {
         const int m = (lo + hi + 1) >> 1;
         if (at_or_above(m) > idx) lo = m; else hi = m - 1;
       }
-      int rank = (int)idx - at_or_above(lo + 1);
+      int rank = (int)idx - at_or_above(lo + 1);  // among the sequences that have this level
       place = lo;
-      b = -1;
 #pragma unroll
       for (int i = 0; i < kKept; ++i) {
         const unsigned has = __ballot_sync(0xffffffffu, n[i] > lo);
         const int c = __popc(has);
-        if (b < 0) {
-          if (rank < c) b = 32 * i + __fns(has, 0, rank + 1);
-          rank -= c;
+        if (rank >= 0 && rank < c) {
+          const bool mine = n[i] > lo && __popc(has & ((1u << lane) - 1)) == rank;
+          const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+          a = __shfl_sync(0xffffffffu, first[i], src);
+          z = __shfl_sync(0xffffffffu, end[i], src);
         }
+        rank -= c;
       }
       return true;
     }
@@ -251,7 +256,8 @@ struct Schedule {
         const int local = (int)(idx - before);
         const unsigned has = __ballot_sync(0xffffffffu, x > local);
         const int w = __ffs(has) - 1;
-        b = window + w;
+        a = row_start[window + w];
+        z = row_start[window + w + 1];
         place = local - __shfl_sync(0xffffffffu, x - c, w);
         return true;
       }
@@ -538,6 +544,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   } else if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
     unsigned slot = 0, q_uses[2] = {0, 0}, tails = 0;
+    if (lane < 3) {
+      const CUtensorMap* map = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    }
     const uint32_t q_bytes = 2u * 128u * (uint32_t)(per * G);
     Item it;
     for (int k = 0; take(k, it) && !timed_out; ++k) {
@@ -601,12 +611,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     for (int k = 0;; ++k) {
       // rounds of gridDim.x items, every second one in the other direction
       const long long at = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      int b = 0, place = 0;
+      int a = 0, z = 0, place = 0;
       Item it{-1, 0, 0, 0};
-      if (sch.find(at / s.Hkv, b, place)) {
-        const int a = row_start[b];
-        it = Item{a, row_start[b + 1] - a, place * 2 * per, (int)(at % s.Hkv)};
-      }
+      if (sch.find(at / s.Hkv, a, z, place)) it = Item{a, z - a, place * 2 * per, (int)(at % s.Hkv)};
       const int st = k % kItems;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[st], ((k / kItems) & 1) ^ 1, abort_flag))) {
         timed_out = true;

@@ -56,26 +56,13 @@ class Plan(NamedTuple):
     slot_map: torch.Tensor   # int32 [n_rows]: page * 16 + position, -1 for rows of no request
 
 
-class _On:
-    """`with _On(device) as stream`: the device is the current one inside; the raw handle of its
-    current stream.  Lighter than torch.cuda.device + current_stream (3 us of a 10 us call)."""
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("index", "back")
 
-    def __init__(self, device: torch.device):
-        if device.type != "cuda":
-            raise ValueError("CUDA tensors are needed (there is no CPU path)")
-        self.index = device.index
-
-    def __enter__(self) -> int:
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
+def _cuda(device: torch.device) -> int:
+    if device.type != "cuda":
+        raise ValueError("CUDA tensors are needed (there is no CPU path)")
+    return device.index
 
 
 def _rows(name: str, t: torch.Tensor, heads: int, n: int, device) -> int:
@@ -108,22 +95,23 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: to
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [rows, heads, 128]")
     n, hq, hkv, device = q.shape[0], q.shape[1], k.shape[1], q.device
-    with _On(device) as stream:
-        qs, ks, vs = _rows("q", q, hq, n, device), _rows("k", k, hkv, n, device), _rows("v", v, hkv, n, device)
-        if row_start.dim() != 1 or row_start.shape[0] < 2:
-            raise ValueError("row_start must be int32 [sequences + 1]")
-        _ints("row_start", row_start, row_start.shape, device)
-        if err is not None:
-            _ints("err", err, (1,), device)
-        if out is None:
-            out = torch.zeros((n, hq, D), dtype=_BF16, device=device)
-        shape = B.PagedShape(row_start.shape[0] - 1, hq, hkv, D, BS, 1, 1)
-        st = B.load().oasis_prompt_attn(
-            ctypes.byref(shape), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, row_start.data_ptr(), n,
-            _SCALE if scale is None else scale, out.data_ptr(), _rows("out", out, hq, n, device),
-            None if err is None else err.data_ptr(), stream)
-        if st:
-            B._check("oasis_prompt_attn", st)
+    index = _cuda(device)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return prompt_attn(q, k, v, row_start, scale, out, err)
+    qs, ks, vs = _rows("q", q, hq, n, device), _rows("k", k, hkv, n, device), _rows("v", v, hkv, n, device)
+    sequences = row_start.numel() - 1
+    if sequences < 1:
+        raise ValueError("row_start must be int32 [sequences + 1]")
+    _ints("row_start", row_start, (sequences + 1,), device)
+    if out is None:
+        out = torch.zeros((n, hq, D), dtype=_BF16, device=device)
+    st = (B._lib or B.load()).oasis_prompt_attn(
+        ctypes.byref(B.PagedShape(sequences, hq, hkv, D, BS, 1, 1)), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        row_start.data_ptr(), n, _SCALE if scale is None else scale, out.data_ptr(), _rows("out", out, hq, n, device),
+        None if err is None else _ints("err", err, (1,), device).data_ptr(), _current_stream(index))
+    if st:
+        B._check("oasis_prompt_attn", st)
     return out
 
 
@@ -145,7 +133,9 @@ class PagedKV:
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         self.device = self.kv.device
+        self._index = _cuda(self.device)
         self._shape = ctypes.byref(self.shape)
+        self._kv_bytes, self._scale_bytes = self.kv.stride(0), 4 * self.scale.stride(0)  # of a layer
         self._scratch = {}  # decode's, by stream
 
     def adopt(self, **tensors: torch.Tensor) -> None:
@@ -166,83 +156,97 @@ class PagedKV:
         """Pages for requests that grow to new_len tokens and slots for their new rows (at most
         n_rows).  Only new table entries are written: lens and n_free change with commit."""
         b = self.batch
-        _ints("new_len", new_len, (b,), self.device)
-        n_rows = int(n_rows)
+        device = self.device
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.extend(new_len, n_rows)
+        _ints("new_len", new_len, (b,), device)
         if n_rows < 0:
             raise ValueError("n_rows must be >= 0")
-        with _On(self.device) as stream:
-            # four allocations: views of one cost more on the host than the launch
-            plan = Plan(*[torch.empty(n, dtype=_INT32, device=self.device) for n in (b, 1, b + 1, n_rows)])
-            st = B.load().oasis_extend_tables(
-                self._shape, self.lens.data_ptr(), new_len.data_ptr(), self.free.data_ptr(), self.n_free.data_ptr(),
-                self.table.data_ptr(), plan.lens.data_ptr(), plan.n_free.data_ptr(), plan.row_start.data_ptr(),
-                plan.slot_map.data_ptr(), n_rows, self.err.data_ptr(), stream)
-            if st:
-                B._check("oasis_extend_tables", st)
-        return plan
+        # four allocations: views of one cost more on the host than the launch
+        lens = torch.empty(b, dtype=_INT32, device=device)
+        n_free = torch.empty(1, dtype=_INT32, device=device)
+        row_start = torch.empty(b + 1, dtype=_INT32, device=device)
+        slot_map = torch.empty(n_rows, dtype=_INT32, device=device)
+        st = (B._lib or B.load()).oasis_extend_tables(
+            self._shape, self.lens.data_ptr(), new_len.data_ptr(), self.free.data_ptr(), self.n_free.data_ptr(),
+            self.table.data_ptr(), lens.data_ptr(), n_free.data_ptr(), row_start.data_ptr(), slot_map.data_ptr(), n_rows,
+            self.err.data_ptr(), _current_stream(self._index))
+        if st:
+            B._check("oasis_extend_tables", st)
+        return Plan(lens, n_free, row_start, slot_map)
 
     def commit(self, plan: Plan) -> None:
         """The plan's lengths and free count become the cache's."""
-        with _On(self.device):
-            self.lens.copy_(plan.lens)
-            self.n_free.copy_(plan.n_free)
+        self.lens.copy_(plan.lens)
+        self.n_free.copy_(plan.n_free)
 
     def release(self, keep_len: torch.Tensor) -> None:
         """Requests keep their first keep_len tokens (0: the request is done); the pages of the
         others are free again."""
         _ints("keep_len", keep_len, (self.batch,), self.device)
-        with _On(self.device) as stream:
+        with torch.cuda.device(self._index):
             left = torch.empty_like(self.n_free)
-            B.oasis_release_tables(self.shape, self.lens, keep_len, self.table, self.free, self.n_free, left, self.err,
-                                   stream)
+            B.oasis_release_tables(self.shape, self.lens, keep_len, self.table, self.free, self.n_free, left, self.err)
             self.n_free.copy_(left)
             kept = (keep_len >= 0) & (keep_len <= self.lens)  # the others released nothing
             self.lens.copy_(torch.where(kept, keep_len, self.lens))
 
     def store(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, layer: int = 0) -> None:
         """Rows k, v [rows, Hkv, 128] (bf16) into the layer's pages at slot_map's slots."""
-        n, h = slot_map.shape[0], self.n_kv_heads
-        ks, vs = _rows("k", k, h, n, self.device), _rows("v", v, h, n, self.device)
-        _ints("slot_map", slot_map, (n,), self.device)
-        with _On(self.device) as stream:
-            st = B.load().oasis_store_kv_q8(
-                self._shape, k.data_ptr(), ks, v.data_ptr(), vs, slot_map.data_ptr(), n, self._layer(self.kv, layer),
-                self._layer(self.scale, layer), self.err.data_ptr(), stream)
-            if st:
-                B._check("oasis_store_kv_q8", st)
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.store(k, v, slot_map, layer)
+        n, h, device = slot_map.numel(), self.n_kv_heads, self.device
+        ks, vs = _rows("k", k, h, n, device), _rows("v", v, h, n, device)
+        _ints("slot_map", slot_map, (n,), device)
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of {self.layers}")
+        st = (B._lib or B.load()).oasis_store_kv_q8(
+            self._shape, k.data_ptr(), ks, v.data_ptr(), vs, slot_map.data_ptr(), n,
+            self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
+            self.err.data_ptr(), _current_stream(self._index))
+        if st:
+            B._check("oasis_store_kv_q8", st)
 
     def decode(self, q: torch.Tensor, ctx_len: Optional[torch.Tensor] = None, layer: int = 0,
                sel: Optional[torch.Tensor] = None, nsel: Optional[torch.Tensor] = None,
                scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Attention of q [batch, Hq, 128] (bf16) over the first ctx_len tokens of every request
         (lens by default), or over the blocks that sel [batch, Hkv, most], nsel [batch, Hkv] list."""
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.decode(q, ctx_len, layer, sel, nsel, scale, out)
         b, hq, device = self.batch, self.n_q_heads, self.device
         stride = _rows("q", q, hq, b, device)
         ctx_len = _ints("ctx_len", self.lens if ctx_len is None else ctx_len, (b,), device)
-        most = 0
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of {self.layers}")
+        most, sel_at, nsel_at = 0, None, None
         if sel is not None or nsel is not None:
             if sel is None or nsel is None or sel.dim() != 3:
                 raise ValueError("sel [batch, Hkv, most] and nsel [batch, Hkv] must be given together")
             most = sel.shape[2]
-            _ints("sel", sel, (b, self.n_kv_heads, most), device)
-            _ints("nsel", nsel, (b, self.n_kv_heads), device)
-        with _On(device) as stream:
-            if out is None:
-                out = torch.empty((b, hq, D), dtype=_BF16, device=device)
-            elif out.dtype is not _BF16 or out.shape != (b, hq, D) or out.device != device or not out.is_contiguous():
-                raise ValueError(f"out must be contiguous bfloat16 [{b}, {hq}, {D}] on {device}")
-            ws = None if torch._C._cuda_isCurrentStreamCapturing() else self._scratch.get(stream)
-            if ws is None:
-                ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-                if not torch._C._cuda_isCurrentStreamCapturing():
-                    self._scratch[stream] = ws
-            st = B.load().oasis_paged_decode_attn_q8(
-                self._shape, q.data_ptr(), stride, self._layer(self.kv, layer), self._layer(self.scale, layer),
-                self.table.data_ptr(), ctx_len.data_ptr(), None if sel is None else sel.data_ptr(),
-                None if sel is None else nsel.data_ptr(), most, _SCALE if scale is None else scale, ws.data_ptr(),
-                self.ws_bytes, out.data_ptr(), self.err.data_ptr(), stream)
-            if st:
-                B._check("oasis_paged_decode_attn_q8", st)
+            sel_at = _ints("sel", sel, (b, self.n_kv_heads, most), device).data_ptr()
+            nsel_at = _ints("nsel", nsel, (b, self.n_kv_heads), device).data_ptr()
+        if out is None:
+            out = torch.empty((b, hq, D), dtype=_BF16, device=device)
+        elif out.dtype is not _BF16 or out.shape != (b, hq, D) or out.device != device or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous bfloat16 [{b}, {hq}, {D}] on {device}")
+        stream = _current_stream(self._index)
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        ws = None if capturing else self._scratch.get(stream)
+        if ws is None:
+            ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+            if not capturing:
+                self._scratch[stream] = ws
+        st = (B._lib or B.load()).oasis_paged_decode_attn_q8(
+            self._shape, q.data_ptr(), stride, self.kv.data_ptr() + layer * self._kv_bytes,
+            self.scale.data_ptr() + layer * self._scale_bytes, self.table.data_ptr(), ctx_len.data_ptr(), sel_at, nsel_at,
+            most, _SCALE if scale is None else scale, ws.data_ptr(), self.ws_bytes, out.data_ptr(), self.err.data_ptr(),
+            stream)
+        if st:
+            B._check("oasis_paged_decode_attn_q8", st)
         return out
 
     def check(self) -> None:
@@ -253,8 +257,3 @@ class PagedKV:
             names = [n for n in ("BAD_BLOCK", "BAD_SLOT", "NO_SLOT", "BAD_COUNT", "TIMEOUT")
                      if bits & getattr(B, "EW_" + n)]
             raise B.OasisError("paged cache", 1, "device error word: " + ", ".join(names))
-
-    def _layer(self, t: torch.Tensor, layer: int) -> int:
-        if not 0 <= layer < self.layers:
-            raise ValueError(f"layer {layer} of {self.layers}")
-        return t.data_ptr() + layer * t.stride(0) * t.element_size()

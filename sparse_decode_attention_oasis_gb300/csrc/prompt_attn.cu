@@ -173,11 +173,12 @@ struct Schedule {
   int B, n_rows, pair;              // pair: tokens of an item
   int lane;
   bool sorted;
+  int kept;                         // registers of a lane in use
   int n[kKept];                     // items of sequence lane + 32 i
   int first[kKept], end[kKept];     // its rows
   int most;                         // the most items of a sequence
   int window;                       // unsorted: first sequence of the window, items before it
-  long long before;
+  int before;
   unsigned bits;
 
   __device__ int items_of(int b, bool flag) {
@@ -196,12 +197,14 @@ struct Schedule {
     lane = ln;
     bits = 0;
     sorted = B <= 32 * kKept;
+    kept = (B + 31) / 32;
     window = 0;
     before = 0;
     most = 0;
     if (sorted) {
 #pragma unroll
       for (int i = 0; i < kKept; ++i) {
+        if (i >= kept) break;
         const int b = lane + 32 * i;
         n[i] = b < B ? items_of(b, true) : 0;
         first[i] = b < B ? row_start[b] : 0;
@@ -214,11 +217,12 @@ struct Schedule {
   __device__ int at_or_above(int level) const {  // items whose place in their sequence is >= level
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < kKept; ++i) c += max(n[i] - level, 0);
+    for (int i = 0; i < kKept; ++i)
+      if (i < kept) c += max(n[i] - level, 0);
     return __reduce_add_sync(0xffffffffu, c);
   }
   // Rows a .. z - 1 of the sequence of item idx, and its place there (calls with rising idx); false: there are no more.
-  __device__ bool find(long long idx, int& a, int& z, int& place) {
+  __device__ bool find(int idx, int& a, int& z, int& place) {
     if (sorted) {
       if (idx >= at_or_above(0)) return false;
       int lo = 0, hi = most - 1;  // the highest level with more than idx items at or above it
@@ -226,10 +230,11 @@ struct Schedule {
         const int m = (lo + hi + 1) >> 1;
         if (at_or_above(m) > idx) lo = m; else hi = m - 1;
       }
-      int rank = (int)idx - at_or_above(lo + 1);  // among the sequences that have this level
+      int rank = idx - at_or_above(lo + 1);  // among the sequences that have this level
       place = lo;
 #pragma unroll
       for (int i = 0; i < kKept; ++i) {
+        if (i >= kept) break;
         const unsigned has = __ballot_sync(0xffffffffu, n[i] > lo);
         const int c = __popc(has);
         if (rank >= 0 && rank < c) {
@@ -253,7 +258,7 @@ struct Schedule {
       }
       const int all = __shfl_sync(0xffffffffu, x, 31);
       if (idx < before + all) {
-        const int local = (int)(idx - before);
+        const int local = idx - before;
         const unsigned has = __ballot_sync(0xffffffffu, x > local);
         const int w = __ffs(has) - 1;
         a = row_start[window + w];
@@ -610,10 +615,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     sch.init(row_start, s.B, n_rows, 2 * per, lane);
     for (int k = 0;; ++k) {
       // rounds of gridDim.x items, every second one in the other direction
-      const long long at = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      // (32 bits: the rows of K alone limit items to a 32nd of what the GPU's memory holds)
+      const unsigned at = (unsigned)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       int a = 0, z = 0, place = 0;
       Item it{-1, 0, 0, 0};
-      if (sch.find(at / s.Hkv, a, z, place)) it = Item{a, z - a, place * 2 * per, (int)(at % s.Hkv)};
+      if (sch.find((int)(at / (unsigned)s.Hkv), a, z, place)) it = Item{a, z - a, place * 2 * per, (int)(at % (unsigned)s.Hkv)};
       const int st = k % kItems;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[st], ((k / kItems) & 1) ^ 1, abort_flag))) {
         timed_out = true;

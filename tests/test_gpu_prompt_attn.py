@@ -75,6 +75,15 @@ def test_long(G, hkv):
     _check([n, 1030], hkv, G, seed=n + G, pad=1, rows=rows)
 
 
+@pytest.mark.parametrize("count", [320, 321, 700])
+def test_many_sequences(count):
+    """Both schedules: up to 320 sequences sorted, more in their order; empty ones among them."""
+    rng = np.random.default_rng(count)
+    lens = [int(n) for n in rng.integers(0, 9, count)]
+    lens[count // 2] = 600
+    _check(lens, 1, 4, seed=count, pad=2)
+
+
 def test_rows_before_and_behind_are_left():
     _check([37, 5], 2, 4, seed=1, pad=200, first=11)
 

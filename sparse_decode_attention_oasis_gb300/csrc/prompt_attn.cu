@@ -46,7 +46,8 @@ constexpr int kRing = 5;
 constexpr int kItems = 4;                    // items that the scheduler may be ahead
 constexpr int kThreads = 384;
 // 168 registers a thread at launch (64,512 in all): 8 warps of 208 and 4 of 88 use them up
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(12 * kLaunchRegs >= 8 * kSoftmaxRegs + 4 * kOtherRegs, "register split");
 constexpr int kConsumers = 11;               // warps that read an item: softmax, MMA, producer
 constexpr float kSlack = 8.0f;
 
@@ -69,6 +70,7 @@ struct Bars {
 };
 
 constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a thread block");
 
 // Shared-memory operand descriptors, low word: address and leading offset, high word: the rest.
 // Q, K: K-major 128-byte rows, 8-row groups 1,024 B apart.  V: rows are tokens (the contraction),
@@ -674,6 +676,16 @@ cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_
   static int attr_cache[kMaxDevicesCached] = {};
   cudaError_t e = ensure_dyn_smem((const void*)prompt_attn_kernel, kSmemBytes, attr_cache);
   if (e != cudaSuccess) return e;
+  // the roles' register split draws on what the kernel is launched with: a build with fewer would wait for ever
+  static int launch_regs[kMaxDevicesCached] = {};
+  int& regs = launch_regs[current_device()];
+  if (!regs) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, prompt_attn_kernel);
+    if (e != cudaSuccess) return e;
+    regs = fa.numRegs;
+  }
+  if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   prompt_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(mq, mk, mv, s, row_start, n_rows,
                                                              scale * 1.4426950408889634f, out, out_stride, err);
   return cudaGetLastError();

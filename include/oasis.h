@@ -674,7 +674,7 @@ OASIS_API oasis_status oasis_trace_set(void* dev_buf, int32_t capacity);
  * Shape (oasis_paged_shape):
  *   B        requests (rows of the table)      (1 .. 65535)
  *   Hq       query heads, Hq = G * Hkv, G in 1 .. 8
- *   Hkv      KV heads                          B * Hkv <= 2^20
+ *   Hkv      KV heads                          (1 .. 1024), B * Hkv <= 2^20
  *   d, bs    must be 128 and 16
  *   nb_max   blocks per request                (1 .. 2^24)
  *   n_pages  pages of one layer's pool         (1 .. 2^27 - 1)
@@ -803,10 +803,12 @@ OASIS_API oasis_status oasis_paged_decode_attn_q8(const oasis_paged_shape* shape
  *   row_start  device int32 [B+1], not decreasing, inside [0, n_rows] (the row_start
  *              of oasis_extend_tables when every old_len is 0); a sequence that
  *              breaks this is skipped with OASIS_EW_BAD_COUNT
- *   n_rows     0 .. 2^28
+ *   n_rows     0 .. 2^26
  *   scale      softmax scale, > 0 and finite
- *   out        device bf16, n_rows rows of [Hq][d], stride out_stride
- *   err_word   device uint32 [1] or NULL
+ *   out        device bf16, n_rows rows of [Hq][d], stride out_stride; must not overlap
+ *              q, k or v
+ *   err_word   device uint32 [1] or NULL; OASIS_EW_TIMEOUT: a bounded wait inside the
+ *              kernel gave up, and the output is incomplete
  * Only B, Hq, Hkv and d of the shape are used; the others are checked as for
  * every call.
  */

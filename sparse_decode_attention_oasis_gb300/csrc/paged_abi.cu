@@ -191,7 +191,7 @@ oasis_status oasis_prompt_attn(const oasis_paged_shape* shape, const void* q, si
   static const char* fn = "oasis_prompt_attn";
   Call c;
   const PagedShape s = check_shape(shape, &c);
-  c.refuse(n_rows < 0 || n_rows > (1 << 28), "n_rows must be in [0, 2^28]");
+  c.refuse(n_rows < 0 || n_rows > (1 << 26), "n_rows must be in [0, 2^26]");
   c.refuse(!ints(row_start), "row_start must be 4-byte aligned and non-NULL");
   if (n_rows > 0) {
     c.refuse(!rows_ok(q, q_stride, s.Hq * oasis::kD) || !rows_ok(out, out_stride, s.Hq * oasis::kD),

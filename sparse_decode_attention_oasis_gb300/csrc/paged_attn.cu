@@ -18,16 +18,27 @@
 // e4m3 converts to fp16 exactly; q is scaled by a power of two for each row so that
 // its largest value lies in [2^14, 2^15), then converts to fp16 without rounding
 // (bf16 has 8 significant bits, fp16 11; values 2^29 below the row's largest lose
-// bits, 2^-40 of the score).  Roundings: w to fp16 (2^-12 each) for the product
-// with V, the output to bf16 (2^-9 of its value, which dominates); s, w, the sums and
-// the accumulators are fp32.
+// bits, 2^-40 of the score).  Roundings: w to fp16 (2^-11 of its value at most) for the product
+// with V, the output to bf16 (2^-8, which dominates); s, w, the sums and the
+// accumulators are fp32.
 //
 // Split: the pages of all (request, KV head) pairs form one sequence, cut into equal
 // ranges for the thread blocks and again for their warps, whatever the lengths are.
 // A warp writes a pair that lies wholly inside its range; pieces are joined in shared
 // memory, and pieces of pairs that cross thread blocks by a second kernel from the
 // workspace (two pieces at most for each block, so its size does not depend on the
-// context).  Bound: HBM, 4 KiB + 8 B for a page and head.
+// context).
+//
+// Bound: HBM, 4 KiB + 8 B for a page and head.  32 requests of 16K tokens, 32/8 heads (1.07
+// GB): 170 us, 6.3 TB/s, 0.93 of the measured copy rate; ncu: DRAM bytes equal the
+// algorithmic ones, 32% of the issue slots used.  The time is 9 to 12 us (launch, tables and
+// first pages 4, the blocks' uneven ends 3, the two joins 4) and the bytes at the copy rate,
+// so 128 pages for each of 256 pairs (134 MB) take 31 us and one pair of short
+// requests 8.  Measured and not kept: pages in a ring of three in shared memory by bulk
+// copies (186 against 174 us: the deeper queues end more unevenly), L2 prefetch 2 to 8
+// pages ahead (177 to 197), queries loaded before the tables but converted after (205:
+// the live registers cost the loop), 4 or 16 warps to a block (no change), one join
+// block for all query rows of a pair (1 us more).
 #include "paged.cuh"
 
 namespace oasis {
@@ -84,7 +95,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 
 // Pages of pair e = b * Hkv + h.
 __device__ __forceinline__ int pair_pages(const PagedShape& s, const Args& a, int e, unsigned* bits) {
-  if (a.sel == nullptr) return clamp_nb(a.ctx_len[e / s.Hkv], s.nb_max);
+  if (a.sel == nullptr) return (int)min(((long long)max(a.ctx_len[e / s.Hkv], 0) + kBS - 1) / kBS, (long long)s.nb_max);
   const int n = a.nsel[e];
   if (n < 0 || n > a.sel_max) {
     *bits |= OASIS_EW_BAD_COUNT;

@@ -10,7 +10,7 @@
 // Rows: the G query heads of a KV head and consecutive tokens are packed into the
 // rows of a tile (row = token * G + head), so that every K/V tile is read once for
 // the whole group and a tile of short sequences is not mostly empty.
-// Roundings: weights to bf16 for the product with V (2^-9 each at most; the sums are of the
+// Roundings: weights to bf16 for the product with V (2^-8 of each at most; the sums are of the
 // unrounded fp32 weights), the output to bf16; scores, maxima, sums and accumulators
 // are fp32.  fp16 weights would keep 3 bits more, but both operands of an MMA have one
 // type, and bf16 values do not fit fp16's range.
@@ -29,6 +29,18 @@
 // TMEM: two S/P and two O tiles of 128 columns, all 512.  Shared memory: 64 KB of Q and a ring
 // of 160 KB.  V rows behind a sequence's last token (another sequence's, or padding that
 // may hold NaN) are zeroed in shared memory before the product: zero times NaN is not zero.
+//
+// Bound: the tensor cores, 4 x 128 x 128 x 128 multiply-adds for a pair of tiles, 2,048 cycles; a
+// pair takes 2,300 to 2,600, the chain S -> softmax (1,250 cycles) -> product of one tile being longer than
+// twice the other's MMAs.  One prompt of 16,384 tokens, 32/8 heads: 1.20 ms alone (1.83 PFLOP/s, 0.94
+// of the measured matrix product), 1.35 ms under the power cap of back-to-back calls; ncu at 8,192 tokens:
+// tensor pipe 76% of elapsed cycles, issue slots 45%.  Twelve packed prompts (11,430 tokens): 169 us; an item of
+// about ten tiles pays some 4,000 cycles for its output and the next one's start.  Measured and not
+// kept: two softmax warps to 32 rows (2,300 against 1,500 us: the issuing lane starves), output by warps of its own
+// (1,250 against 1,200: fewer registers for the softmax), 200 or 216 registers for the softmax (3% more),
+// scores and weights of a last tile cut to the chunks that hold keys, as branches (1,650) or as a second
+// body (packed 210 against 175: the instructions are fetched anew), outputs transposed
+// over four lanes (packed 181 against 175).
 // Every wait is bounded: on expiry the block raises OASIS_EW_TIMEOUT, waits (bounded)
 // for its own copies and MMAs, frees TMEM and returns.
 #include "paged.cuh"

@@ -164,7 +164,8 @@ def test_lengths_beyond_the_table_are_clamped():
     rng = np.random.default_rng(14)
     kv, scale, table, q, q64 = _inputs(rng, [96, 96], 1, 1)
     c = cache_of(kv, scale, table, 1)
-    _check(c, q, q64, kv, scale, table, [10 ** 9, -1])
+    for beyond in (97, 10 ** 9, 2 ** 31 - 1):
+        _check(c, q, q64, kv, scale, table, [beyond, -1])
 
 
 def test_strided_queries_given_scale_and_output():
@@ -223,6 +224,29 @@ def test_a_long_cache_past_32_bit_offsets():
     out = c.decode(q, ints([42])).double().cpu().numpy()
     want = ref.decode(q64, kv2, scale2, np.array([[0, 1, 2, -1]]), [42], SCALE)
     check_attention(out, want[0], want[1], want[2], F16_HALF_STEP, want[3])
+
+
+def test_captured_and_replayed_with_other_lengths():
+    from paged_helpers import cache_of, ints
+
+    rng = np.random.default_rng(19)
+    kv, scale, table, q, q64 = _inputs(rng, [3000, 3000, 3000], 2, 8)
+    kv[kv & 0x7f == 0x7f] = 0
+    c = cache_of(kv, scale, table, 8)
+    ctx = ints([3000, 1, 0])
+    c.decode(q, ctx)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.decode(q, ctx)
+    from paged_helpers import F16_HALF_STEP, check_attention
+
+    for n in ([3000, 1, 0], [0, 0, 0], [17, 2999, 1600], [1, 1, 1]):
+        ctx.copy_(ints(n))
+        g.replay()
+        torch.cuda.synchronize()
+        want = ref.decode(q64, kv, scale, table, n, SCALE)
+        check_attention(out.double().cpu().numpy(), want[0], want[1], want[2], F16_HALF_STEP, want[3])
 
 
 def test_two_captured_graphs_and_two_streams():

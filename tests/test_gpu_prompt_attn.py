@@ -169,6 +169,28 @@ def test_refusals():
             prompt_attn(**{"q": q, "k": k, "v": k, "row_start": s, **bad})
 
 
+def test_two_streams_at_once():
+    from paged_helpers import bf16, ints
+
+    from sparse_decode_attention_oasis_gb300.paged import prompt_attn
+
+    rng = np.random.default_rng(9)
+    cases = []
+    for n, cut in ((3000, 1100), (2500, 7)):
+        q, _ = bf16(rng, (n, 8, 128))
+        k, _ = bf16(rng, (n, 2, 128))
+        cases.append((q, k, ints([0, cut, n]), torch.cuda.Stream()))
+    alone = [prompt_attn(q, k, k, s) for q, k, s, _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        outs = []
+        for q, k, s, st in cases:
+            with torch.cuda.stream(st):
+                outs.append(prompt_attn(q, k, k, s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, alone))
+
+
 def test_captured_and_replayed_with_other_lengths():
     from paged_helpers import bf16, ints
 

@@ -65,7 +65,7 @@ NAN, INF = float("nan"), float("inf")
 
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(q=8), dict(qs=4095), dict(qs=4088), dict(qs=1 << 32), dict(k=None), dict(ks=1020), dict(ks=1016),
-    dict(v=24), dict(vs=0), dict(start=None), dict(start=18), dict(n=-1), dict(n=(1 << 28) + 1), dict(scale=0.0),
+    dict(v=24), dict(vs=0), dict(start=None), dict(start=18), dict(n=-1), dict(n=(1 << 26) + 1), dict(scale=0.0),
     dict(scale=-1.0), dict(scale=NAN), dict(scale=INF), dict(out=None), dict(out=8), dict(os=4088), dict(err=2)])
 def test_prompt_refusals(lib, kw):
     assert _prompt(lib, _shape(), **kw) == 1

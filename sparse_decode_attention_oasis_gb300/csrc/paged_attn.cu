@@ -224,19 +224,20 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
       const int nb = (ctx + kBS - 1) / kBS;
       const int first = (int)(p - e_lo), last = (int)min((long long)count, w_hi - e_lo);  // pages of the pair
 
+      // ---- the query row lane / 4, dimensions as for the keys
       uint32_t qf[16];
       float fac[2];
       {
         uint4 w[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
-      if ((lane >> 2) < G) {
-        const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * 16;
-        w[0] = ldg_nc(src);
-        w[1] = ldg_nc(src + 8);
-        w[2] = ldg_nc(src + 64);
-        w[3] = ldg_nc(src + 72);
-      }
+        for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
+        if ((lane >> 2) < G) {
+          const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * 16;
+          w[0] = ldg_nc(src);
+          w[1] = ldg_nc(src + 8);
+          w[2] = ldg_nc(src + 64);
+          w[3] = ldg_nc(src + 72);
+        }
         uint32_t m = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)

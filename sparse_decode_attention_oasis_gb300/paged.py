@@ -125,7 +125,8 @@ class PagedKV:
         if layers < 1:
             raise ValueError("layers must be >= 1")
         self.batch, self.n_q_heads, self.n_kv_heads, self.layers = batch, n_q_heads, n_kv_heads, layers
-        self.kv = torch.zeros((layers, n_pages, n_kv_heads, 2, BS, D), dtype=torch.uint8, device=device)
+        # not initialised: positions that were never stored are never read
+        self.kv = torch.empty((layers, n_pages, n_kv_heads, 2, BS, D), dtype=torch.uint8, device=device)
         self.scale = torch.ones((layers, n_pages, n_kv_heads, 2), dtype=torch.float32, device=device)
         self.table = torch.full((batch, nb_max), -1, dtype=torch.int32, device=device)
         self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 is taken first
@@ -164,8 +165,7 @@ class PagedKV:
         if n_rows < 0:
             raise ValueError("n_rows must be >= 0")
         # four allocations: views of one cost more on the host than the launch
-        lens = torch.empty(b, dtype=_INT32, device=device)
-        n_free = torch.empty(1, dtype=_INT32, device=device)
+        lens, n_free = torch.empty_like(self.lens), torch.empty_like(self.n_free)
         row_start = torch.empty(b + 1, dtype=_INT32, device=device)
         slot_map = torch.empty(n_rows, dtype=_INT32, device=device)
         st = (B._lib or B.load()).oasis_extend_tables(

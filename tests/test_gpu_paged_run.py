@@ -28,6 +28,7 @@ def test_prompts_then_decode_steps():
     rng = np.random.default_rng(0)
     hkv, G, layers, n_pages = 2, 4, 2, 40
     c = PagedKV(n_pages=n_pages, batch=3, nb_max=16, n_q_heads=hkv * G, n_kv_heads=hkv, layers=layers)
+    c.kv.zero_()
     lens = np.array([70, 1, 33])
     table, free, n_free = c.table.cpu().numpy(), c.free.cpu().numpy(), n_pages
     pages = [[np.zeros((n_pages, hkv, 2, 16, 128), np.uint8), np.ones((n_pages, hkv, 2))] for _ in range(layers)]

@@ -168,6 +168,7 @@ def test_layers_are_apart():
     from sparse_decode_attention_oasis_gb300.paged import PagedKV
 
     c = PagedKV(n_pages=3, batch=1, nb_max=2, n_q_heads=2, n_kv_heads=2, layers=3)
+    c.kv.zero_()
     k = torch.ones((2, 2, 128), dtype=torch.bfloat16, device="cuda")
     c.store(k, k, ints([16, 17]), layer=1)
     assert c.kv[0].any() == 0 and c.kv[2].any() == 0 and c.kv[1, 1].any()

@@ -34,6 +34,7 @@ kernels the host's share of a call is what counts.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple, Optional
 
@@ -86,6 +87,11 @@ def _ints(name: str, t: torch.Tensor, shape, device) -> torch.Tensor:
     return t
 
 
+@functools.lru_cache(maxsize=256)
+def _prompt_shape(sequences: int, hq: int, hkv: int):
+    return ctypes.byref(B.PagedShape(sequences, hq, hkv, D, BS, 1, 1))
+
+
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                 err: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -107,8 +113,8 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: to
     if out is None:
         out = torch.zeros((n, hq, D), dtype=_BF16, device=device)
     st = (B._lib or B.load()).oasis_prompt_attn(
-        ctypes.byref(B.PagedShape(sequences, hq, hkv, D, BS, 1, 1)), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        row_start.data_ptr(), n, _SCALE if scale is None else scale, out.data_ptr(), _rows("out", out, hq, n, device),
+        _prompt_shape(sequences, hq, hkv), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, row_start.data_ptr(), n,
+        _SCALE if scale is None else scale, out.data_ptr(), _rows("out", out, hq, n, device),
         None if err is None else _ints("err", err, (1,), device).data_ptr(), _current_stream(index))
     if st:
         B._check("oasis_prompt_attn", st)

@@ -79,6 +79,7 @@ struct Bars {
   Item items[kItems];
   uint32_t tmem_base;
   int abort_flag;
+  int token;  // 1: a row tile's products are being issued
 };
 
 constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars);
@@ -321,6 +322,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     mbar_init(&bars->done[0], 1);
     mbar_init(&bars->done[1], 1);
     bars->abort_flag = 0;
+    bars->token = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -499,6 +501,22 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         timed_out |= !mbar_wait(bar, parity, abort_flag);
         return !timed_out;
       };
+      // One tile's products at a time: what is issued from both at once is executed in turns and ends late for both,
+      // which then stay in step, softmax beside softmax and products beside products (some
+      // blocks took 25% longer).
+      auto take_token = [&] {
+        if (atomicExch(&bars->token, 1) == 0) return true;
+        const unsigned long long t0 = global_ns();
+        unsigned n = 0;
+        while (atomicExch(&bars->token, 1) != 0) {
+          if ((++n & 63u) == 0 && (*abort_flag || global_ns() - t0 > kWaitNs)) {
+            timed_out = true;
+            return false;
+          }
+        }
+        return true;
+      };
+      auto give_token = [&] { *reinterpret_cast<volatile int*>(&bars->token) = 0; };
       auto scores = [&](uint32_t place) {  // S = Q K^T
         const uint32_t kb = qk_desc_low(kv0 + place * kTileBytes);
 #pragma unroll
@@ -532,19 +550,22 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
               !ready(&bars->p_full[i][0], p_phase))
             break;
           tc_fence_after();
+          if (!take_token()) break;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, kk > 0 || j > 1);
-          if (!ready(&bars->p_full[i][1], p_phase)) break;
+          if (!ready(&bars->p_full[i][1], p_phase)) { give_token(); break; }
           tc_fence_after();
 #pragma unroll
           for (int kk = 4; kk < 8; ++kk) mma_ts(o_addr, s_addr + kk * 8, vb + kk * (2048 >> 4), id_o, true);
           if (j < ni) {
             scores(at);
+            give_token();
             if (j == ni - 1) mma_commit(&bars->q_empty[i]);
             mma_commit(&bars->kv_empty[at]);
             advance();
           } else {
             mma_commit(&bars->o_full[i]);
+            give_token();
           }
           mma_commit(&bars->kv_empty[v_at]);
         }

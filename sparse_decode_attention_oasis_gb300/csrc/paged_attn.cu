@@ -156,8 +156,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = s.Hq / s.Hkv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");  // the join's launch overlaps this kernel
+  wait_for_predecessor();
   const int pairs = s.B * s.Hkv;
   const int per = (pairs + kThreads - 1) / kThreads;
   unsigned bits = 0;
@@ -473,8 +472,7 @@ paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const in
   __shared__ float rows[kJoinWarps][kRowFloats];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = s.Hq / s.Hkv, r = blockIdx.y, first = blockIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  wait_for_predecessor();  // the pieces are written
   const int2 t = tails[first];
   if (t.x < 0) return;
   const int n = t.y - first + 1;
@@ -540,22 +538,10 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   static int attr_cache[kMaxDevicesCached] = {};
   cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel, smem, attr_cache);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_decode_attn_kernel, s, a);
+  e = launch_chained(paged_decode_attn_kernel, dim3(grid), dim3(kThreads), smem, stream, s, a);
   if (e != cudaSuccess || grid == 1) return e;
-  cfg.dynamicSmemBytes = 0;
-  cfg.gridDim = dim3(grid, s.G());
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel, s, (const float*)parts, (const int2*)a.tails, out);
+  return launch_chained(paged_decode_join_kernel, dim3(grid, s.G()), dim3(kJoinWarps * 32), 0, stream, s, parts, a.tails,
+                        out);
 }
 
 }  // namespace oasis

@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 store_kv_q8_kernel(PagedShape s, const uint16_t* __restrict__ k, size_t k_stride, const uint16_t* __restrict__ v,
                    size_t v_stride, const int* __restrict__ slot_map, int n_rows, int rows_per_warp,
                    uint8_t* __restrict__ pages, float* __restrict__ scales, unsigned* __restrict__ err) {
+  wait_for_predecessor();
   const int lane = threadIdx.x & 31;
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
   const uint16_t* src = which ? v : k;
@@ -148,9 +149,8 @@ cudaError_t launch_store_kv_q8(const PagedShape& s, const uint16_t* k, size_t k_
   const int per = (long long)n_rows * s.Hkv * 2 <= resident ? 1 : kBS;
   const long long groups = ((long long)n_rows + kWarps * per - 1) / (kWarps * per);
   dim3 grid((unsigned)groups, (unsigned)(2 * s.Hkv));
-  store_kv_q8_kernel<<<grid, kWarps * 32, 0, stream>>>(s, k, k_stride, v, v_stride, slot_map, n_rows, per, pages,
-                                                       scales, err);
-  return cudaGetLastError();
+  return launch_chained(store_kv_q8_kernel, grid, dim3(kWarps * 32), 0, stream, s, k, k_stride, v, v_stride, slot_map,
+                        n_rows, per, pages, scales, err);
 }
 
 }  // namespace oasis

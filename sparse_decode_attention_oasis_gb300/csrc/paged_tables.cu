@@ -77,6 +77,7 @@ extend_tables_kernel(PagedShape s, const int* __restrict__ old_len, const int* _
   __shared__ RowSpan spans[kSpans + 1];
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ int taken_max[kThreads / 32];
+  wait_for_predecessor();
   const int tid = threadIdx.x;
   const bool first_cta = blockIdx.x == 0;
   const long long lo = (long long)blockIdx.x * kRowsPerCta;
@@ -222,6 +223,7 @@ release_tables_kernel(PagedShape s, const int* __restrict__ len, const int* __re
                       const int* __restrict__ n_free_in, int* __restrict__ n_free_out, unsigned* __restrict__ err) {
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ long long chunk0[kThreads];
+  wait_for_predecessor();
   const int tid = threadIdx.x;
   const int nf_raw = *n_free_in;
   const int n_free = nf_raw < 0 ? 0 : (nf_raw > s.n_pages ? s.n_pages : nf_raw);
@@ -267,9 +269,8 @@ cudaError_t launch_extend_tables(const PagedShape& s, const int* old_len, const 
                                  const int* n_free, int* table, int* len_out, int* n_free_out, int* row_start,
                                  int* slot_map, int n_rows, unsigned* err, cudaStream_t stream) {
   const int grid = n_rows > kRowsPerCta ? (n_rows + kRowsPerCta - 1) / kRowsPerCta : 1;
-  extend_tables_kernel<<<grid, kThreads, 0, stream>>>(s, old_len, new_len, free_pages, n_free, table, len_out,
-                                                      n_free_out, row_start, slot_map, n_rows, err);
-  return cudaGetLastError();
+  return launch_chained(extend_tables_kernel, dim3(grid), dim3(kThreads), 0, stream, s, old_len, new_len, free_pages,
+                        n_free, table, len_out, n_free_out, row_start, slot_map, n_rows, err);
 }
 
 cudaError_t launch_release_tables(const PagedShape& s, const int* len, const int* keep_len, const int* table,
@@ -277,8 +278,8 @@ cudaError_t launch_release_tables(const PagedShape& s, const int* len, const int
                                   cudaStream_t stream) {
   const int most = 2 * sm_count();
   const int grid = s.B < most ? s.B : most;
-  release_tables_kernel<<<grid, kThreads, 0, stream>>>(s, len, keep_len, table, free_pages, n_free, n_free_out, err);
-  return cudaGetLastError();
+  return launch_chained(release_tables_kernel, dim3(grid), dim3(kThreads), 0, stream, s, len, keep_len, table, free_pages,
+                        n_free, n_free_out, err);
 }
 
 }  // namespace oasis

@@ -334,6 +334,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  wait_for_predecessor();
   bool timed_out = false;
 
   // Item k of this block, for the warps that consume items: false at the end or on a time-out.
@@ -719,9 +720,8 @@ cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_
     regs = fa.numRegs;
   }
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  prompt_attn_kernel<<<grid, kThreads, kSmemBytes, stream>>>(mq, mk, mv, s, row_start, n_rows,
-                                                             scale * 1.4426950408889634f, out, out_stride, err);
-  return cudaGetLastError();
+  return launch_chained(prompt_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, mq, mk, mv, s, row_start, n_rows,
+                        scale * 1.4426950408889634f, out, out_stride, err);
 }
 
 }  // namespace oasis

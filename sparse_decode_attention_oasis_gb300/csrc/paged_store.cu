@@ -11,8 +11,8 @@
 // One warp per (run of rows in one page, head, K or V): 16 lanes cover a row's 256
 // bytes in 16-byte loads, two rows to an instruction, held in registers from the
 // maximum to the conversion, so that every row is read once.  Bound: HBM.  15,170 tokens of
-// 8 heads (93 MB): 17.5 us, 5.3 TB/s, 0.79 of the measured copy rate, of which 2 us are launch
-// and first loads; 32 tokens of a decode step: 3 us.
+// 8 heads (93 MB): 17.1 us, 5.5 TB/s, 0.81 of the measured copy rate, of which 2 us are launch
+// and first loads; 32 tokens of a decode step: 2.4 us.
 #include "paged.cuh"
 
 namespace oasis {

@@ -10,8 +10,8 @@
 // One launch: every thread block forms the prefixes for itself (2 x 4 bytes per
 // request from L2, one scan over 256 threads that each own ceil(B/256) requests)
 // and then writes its own 4,096 rows of the slot map, so no block waits for
-// another.  Bound: the launch, three scans and two dependent rounds of loads: 4.2 us for 256
-// requests of one new token, 9.0 us for 64 prompts of 1.9 million (7.7 MB, 1.5 us at the
+// another.  Bound: the launch, three scans and two dependent rounds of loads: 3.9 us for 256
+// requests of one new token, 9.9 us for 64 prompts of 1.9 million (7.7 MB, 1.5 us at the
 // copy rate: the scans' instructions, which every block repeats).
 #include "paged.cuh"
 

@@ -32,15 +32,17 @@
 //
 // Bound: the tensor cores, 4 x 128 x 128 x 128 multiply-adds for a pair of tiles, 2,048 cycles; a
 // pair takes 2,300 to 2,600, the chain S -> softmax (1,250 cycles) -> product of one tile being longer than
-// twice the other's MMAs.  One prompt of 16,384 tokens, 32/8 heads: 1.20 ms alone (1.83 PFLOP/s, 0.94
-// of the measured matrix product), 1.35 ms under the power cap of back-to-back calls; ncu at 8,192 tokens:
-// tensor pipe 76% of elapsed cycles, issue slots 45%.  Twelve packed prompts (11,430 tokens): 169 us; an item of
-// about ten tiles pays some 4,000 cycles for its output and the next one's start.  Measured and not
-// kept: two softmax warps to 32 rows (2,300 against 1,500 us: the issuing lane starves), output by warps of its own
-// (1,250 against 1,200: fewer registers for the softmax), 200 or 216 registers for the softmax (3% more),
-// scores and weights of a last tile cut to the chunks that hold keys, as branches (1,650) or as a second
-// body (packed 210 against 175: the instructions are fetched anew), outputs transposed
-// over four lanes (packed 181 against 175).
+// twice the other's MMAs; and the power cap: in long calls the SM clock settles at 1.7 to 1.85 GHz.  One
+// prompt of 16,384 tokens, 32/8 heads: 1.20 ms (1.83 PFLOP/s, 0.94 of the measured matrix product),
+// 1.34 ms in calls that follow each other for seconds; ncu at 8,192 tokens: tensor pipe 77% of
+// elapsed cycles, issue slots 45%.  Twelve packed prompts (11,430 tokens): 163 us; an item pays
+// some 4,000 cycles at its ends beside its tiles.  Measured and not kept: two softmax warps to 32 rows
+// (2,300 against 1,500 us then: the issuing lane starves), output by warps of its own (1,250 against
+// 1,200: fewer registers for the softmax), 200 or 216 registers for the softmax (3% more), scores
+// and weights of a last tile cut to the chunks that hold keys, as branches (1,650) or as a second body
+// (packed 210 against 175), only its products cut (within 2% either way), outputs transposed over four lanes
+// (packed 181 against 175), the output through a ring place and a tensor store (16 prompts of 512 tokens 51
+// against 53, the others the same, for 80 lines of accounting).
 // Every wait is bounded: on expiry the block raises OASIS_EW_TIMEOUT, waits (bounded)
 // for its own copies and MMAs, frees TMEM and returns.
 #include "paged.cuh"

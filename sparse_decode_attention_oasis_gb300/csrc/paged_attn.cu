@@ -27,14 +27,15 @@
 // A warp writes a pair that lies wholly inside its range; pieces are joined in shared
 // memory, and pieces of pairs that cross thread blocks by a second kernel from the
 // workspace (two pieces at most for each block, so its size does not depend on the
-// context).
+// context).  Where a pair can have few pages only, a cluster of 1 to 8 blocks takes a pair and
+// joins its pieces through distributed shared memory, in one launch.
 //
 // Bound: HBM, 4 KiB + 8 B for a page and head.  32 requests of 16K tokens, 32/8 heads (1.07
 // GB): 170 us, 6.3 TB/s, 0.93 of the measured copy rate; ncu: DRAM bytes equal the
 // algorithmic ones, 32% of the issue slots used.  The time is 9 to 12 us (launch, tables and
 // first pages 4, the blocks' uneven ends 3, the two joins 4) and the bytes at the copy rate,
-// so 128 pages for each of 256 pairs (134 MB) take 31 us and one pair of short
-// requests 8.  Measured and not kept: pages in a ring of three in shared memory by bulk
+// so 128 pages for each of 256 pairs (134 MB) took 31 us; by clusters they take 28, and one
+// request of 700 tokens 6.8 against 8.4.  Measured and not kept: pages in a ring of three in shared memory by bulk
 // copies (186 against 174 us: the deeper queues end more unevenly), L2 prefetch 2 to 8
 // pages ahead (177 to 197), queries loaded before the tables but converted after (205:
 // the live registers cost the loop), 4 or 16 warps to a block (no change), one join
@@ -63,6 +64,7 @@ struct Args {
   const int* sel;
   const int* nsel;
   int sel_max;
+  int team;  // blocks of a cluster
   float scale_log2;
   float* parts;  // [grid][2][G][kRowFloats]
   int2* tails;   // [grid]: the pair whose first piece is a block's tail (-1: none), its last block
@@ -150,65 +152,99 @@ struct Shared {
   int slot_pair[2 * kWarps];
 };
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 load_remote(const float* mine, unsigned rank) {  // the same place in block `rank`'s shared memory
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+// kClustered: a cluster of `team` blocks for each pair, else all pages in equal ranges.
+template <bool kClustered>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_decode_attn_kernel(PagedShape s, Args a) {
-  extern __shared__ __align__(16) float slot_rows[];  // [2 * kWarps][G][kD]
+  extern __shared__ __align__(16) float slot_rows[];  // [2 * kWarps][G][kD], then (kClustered) [G][kRowFloats]
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = s.Hq / s.Hkv;
   wait_for_predecessor();
   const int pairs = s.B * s.Hkv;
   const int per = (pairs + kThreads - 1) / kThreads;
+  const int team = a.team, rank = blockIdx.x % team;  // kClustered: blocks to a pair, this one's place
   unsigned bits = 0;
+  int blocks = 1;
+  long long total = 0, c_lo, c_hi;  // pages of all pairs (of this one), this block's range
 
-  // prefix of the pairs' pages; pairs without pages get their zero rows here
-  long long n = 0;
-  for (int e = min(tid * per, pairs); e < min((tid + 1) * per, pairs); ++e) {
-    const int c = pair_pages(s, a, e, &bits);
-    n += c;
-    if (c == 0 && e % (int)gridDim.x == (int)blockIdx.x)
-      for (int i = 0; i < G * kD / 8; ++i)
-        reinterpret_cast<uint4*>(a.out + (long long)e * G * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (kClustered) {
+    const int e = blockIdx.x / team;
+    total = pair_pages(s, a, e, &bits);
+    if (total == 0) {
+      set_err(a.err, bits);
+      if (rank == 0)
+        for (int i = tid; i < G * kD / 8; i += kThreads)
+          reinterpret_cast<uint4*>(a.out + (long long)e * G * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+      return;  // the whole cluster
+    }
+    c_lo = rank * total / team;
+    c_hi = (rank + 1) * total / team;
+    if (lane < 2) sh.slot_pair[warp * 2 + lane] = -1;
+    __syncwarp();
+  } else {
+    // prefix of the pairs' pages; pairs without pages get their zero rows here
+    long long n = 0;
+    for (int e = min(tid * per, pairs); e < min((tid + 1) * per, pairs); ++e) {
+      const int c = pair_pages(s, a, e, &bits);
+      n += c;
+      if (c == 0 && e % (int)gridDim.x == (int)blockIdx.x)
+        for (int i = 0; i < G * kD / 8; ++i)
+          reinterpret_cast<uint4*>(a.out + (long long)e * G * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    long long x = n;
+  #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh.warp_sums[warp] = x;
+    if (lane < 2) sh.slot_pair[warp * 2 + lane] = -1;
+    __syncthreads();
+    long long off = 0;
+  #pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      off += w < warp ? sh.warp_sums[w] : 0;
+      total += sh.warp_sums[w];
+    }
+    sh.chunk_start[tid] = off + x - n;
+    if (tid == 0) sh.chunk_start[kThreads] = total;
+    __syncthreads();
+    const long long wanted = (total + kMinPages - 1) / kMinPages;
+    blocks = wanted < (long long)gridDim.x ? (int)wanted : (int)gridDim.x;
+    if ((int)blockIdx.x >= blocks) {
+      if (tid == 0) a.tails[blockIdx.x] = make_int2(-1, 0);
+      if (blockIdx.x == 0) set_err(a.err, bits);
+      return;
+    }
+    c_lo = blockIdx.x * total / blocks;
+    c_hi = (blockIdx.x + 1) * total / blocks;
   }
-  long long x = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sh.warp_sums[warp] = x;
-  if (lane < 2) sh.slot_pair[warp * 2 + lane] = -1;
-  __syncthreads();
-  long long total = 0, off = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    off += w < warp ? sh.warp_sums[w] : 0;
-    total += sh.warp_sums[w];
-  }
-  sh.chunk_start[tid] = off + x - n;
-  if (tid == 0) sh.chunk_start[kThreads] = total;
-  __syncthreads();
-  const long long wanted = (total + kMinPages - 1) / kMinPages;
-  const int blocks = wanted < (long long)gridDim.x ? (int)wanted : (int)gridDim.x;
-  if ((int)blockIdx.x >= blocks) {
-    if (tid == 0) a.tails[blockIdx.x] = make_int2(-1, 0);
-    if (blockIdx.x == 0) set_err(a.err, bits);
-    return;
-  }
-  const long long c_lo = blockIdx.x * total / blocks, c_hi = (blockIdx.x + 1) * total / blocks;
   const long long w_lo = c_lo + warp * (c_hi - c_lo) / kWarps, w_hi = c_lo + (warp + 1) * (c_hi - c_lo) / kWarps;
 
   if (w_lo < w_hi) {
     // the pair that holds page w_lo: the last chunk of pairs that starts at or before it, then a walk
-    int i = 0, j = kThreads - 1;
+    int i = 0, j = kClustered ? 0 : kThreads - 1;
     while (i < j) {
       const int m = (i + j + 1) >> 1;
       if (sh.chunk_start[m] <= w_lo) i = m; else j = m - 1;
     }
-    int e = i * per;
-    long long e_lo = sh.chunk_start[i];
+    int e = kClustered ? blockIdx.x / team : i * per;
+    long long e_lo = kClustered ? 0 : sh.chunk_start[i];
     // with one pair to a chunk the prefix holds its pages
     auto pages_of = [&](int pair) {
+      if (kClustered) return (int)total;
       return per == 1 ? (int)(sh.chunk_start[pair + 1] - sh.chunk_start[pair]) : pair_pages(s, a, pair, &bits);
     };
     int count = pages_of(e);
@@ -379,7 +415,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         st.sum[0] += __shfl_xor_sync(0xffffffffu, st.sum[0], o);
         st.sum[1] += __shfl_xor_sync(0xffffffffu, st.sum[1], o);
       }
-      const bool whole = first == 0 && last == count;
+      const bool whole = first == 0 && last == count && !(kClustered && team > 1);
       const int which = first == 0 ? 1 : 0, slot = warp * 2 + which;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -424,14 +460,15 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
   const unsigned leads = __ballot_sync(0xffffffffu, my_pair >= 0 && __ffs(same) - 1 == lane);
   const int units = __popc(leads) * G;
   int2 tail = make_int2(-1, 0);
-  if (leads) {  // only the last pair can go on in the next block
+  if (!kClustered && leads) {  // only the last pair can go on in the next block
     const int lead = 31 - __clz(leads);
     const long long e_hi = sh.slot_hi[lead];
     // its last piece is in the last block whose range starts before e_hi
     if (sh.slot_lo[lead] >= c_lo && e_hi > c_hi)
       tail = make_int2(sh.slot_pair[lead], (int)((e_hi * blocks + total - 1) / total - 1));
   }
-  if (tid == 0) a.tails[blockIdx.x] = tail;
+  if (!kClustered && tid == 0) a.tails[blockIdx.x] = tail;
+  float* piece = slot_rows + (size_t)2 * kWarps * G * kD;  // kClustered: this block's rows
   for (int u = warp; u < units; u += kWarps) {
     const int lead = __fns(leads, 0, u / G + 1), r = u % G;
     const unsigned mask = __shfl_sync(0xffffffffu, same, lead);
@@ -451,16 +488,43 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     }
     const int e = sh.slot_pair[lead];
     const bool starts = sh.slot_lo[lead] >= c_lo;
-    if (starts && sh.slot_hi[lead] <= c_hi) {
+    if (starts && sh.slot_hi[lead] <= c_hi && !(kClustered && team > 1)) {
       const float inv = sum > 0.f ? 1.0f / sum : 0.f;
       reinterpret_cast<uint2*>(a.out + ((long long)e * G + r) * kD)[lane] =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     } else {
-      float* row = a.parts + (((long long)blockIdx.x * 2 + (starts ? 1 : 0)) * G + r) * kRowFloats;
+      float* row = kClustered ? piece + r * kRowFloats
+                              : a.parts + (((long long)blockIdx.x * 2 + (starts ? 1 : 0)) * G + r) * kRowFloats;
       *reinterpret_cast<float2*>(row + lane * 4) = make_float2(o.x, o.y);
       *reinterpret_cast<float2*>(row + lane * 4 + 2) = make_float2(o.z, o.w);
       if (lane == 0) *reinterpret_cast<float2*>(row + kD) = make_float2(top, sum);
     }
+  }
+  if constexpr (kClustered) {
+    if (team == 1) return;
+    if (leads == 0)  // no page of the pair for this block
+      for (int r = tid; r < G; r += kThreads) *reinterpret_cast<float2*>(piece + r * kRowFloats + kD) = make_float2(neg_inf(), 0.f);
+    cluster_sync();
+    // row r is joined by warp r / team of block r % team
+    const int r = warp * team + rank;
+    if (r < G) {
+      const float* row = piece + r * kRowFloats;
+      const float2 ts = lane < team ? load_remote(row + kD, lane) : make_float2(neg_inf(), 0.f);
+      const float top = warp_max(ts.x);
+      const float f = ts.x == neg_inf() ? 0.f : exp2f(ts.x - top);
+      const float sum = warp_sum(f * ts.y);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < team; ++c) {
+        const float fc = __shfl_sync(0xffffffffu, f, c);
+        if (fc == 0.f) continue;  // nothing there, or as good as nothing
+        const float2 u = load_remote(row + lane * 4, c), v = load_remote(row + lane * 4 + 2, c);
+        o = make_float4(fmaf(fc, u.x, o.x), fmaf(fc, u.y, o.y), fmaf(fc, v.x, o.z), fmaf(fc, v.y, o.w));
+      }
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+      reinterpret_cast<uint2*>(a.out + ((long long)(blockIdx.x / team) * G + r) * kD)[lane] =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+    cluster_sync();  // no block's shared memory goes while another reads it
   }
 }
 
@@ -532,15 +596,32 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   const long long blocks = (pages_max + kMinPages - 1) / kMinPages;
   const int grid = blocks < most ? (int)blocks : most;
   float* parts = static_cast<float*>(ws);
-  Args a{q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, scale * 1.4426950408889634f, parts,
+  Args a{q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, 1, scale * 1.4426950408889634f, parts,
          reinterpret_cast<int2*>(parts + (size_t)most * 2 * s.G() * kRowFloats), out, err};
   const size_t smem = (size_t)2 * kWarps * s.G() * kD * sizeof(float);
+  const long long pairs = (long long)s.B * s.Hkv;
+  const int pair_max = sel ? sel_max : s.nb_max;
+  // A cluster for each pair needs no prefix over the pairs, no workspace and no second kernel, but leaves blocks
+  // idle that other pairs could use: taken while a pair's most pages keep its blocks busy for a few us.  32/8 heads, one
+  // cluster a pair against equal ranges: 1 x 700 tokens 6.5 against 7.9 us, 1 x 4,096 9.6 against 11.0, 1 x
+  // 8,192 (64 pages for each of 64 blocks) 14.0 against 13.6, 32 x 1,000 16.8 against 19.6, 32 x 2,000
+  // (125 pages for each of 256 blocks) 27.5 against 29.8.
+  while (a.team < 8 && pairs * a.team * 2 <= most && pair_max > kMinPages * a.team) a.team *= 2;
+  const int team_pages = pairs * a.team * 3 >= most * 2LL ? 128 : 56;  // two thirds of the GPU's places filled, or fewer
+  if (pairs * a.team <= most && pair_max <= team_pages * a.team) {
+    const size_t with_piece = smem + (size_t)s.G() * kRowFloats * sizeof(float);
+    static int attr_cache[kMaxDevicesCached] = {};
+    cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<true>, with_piece, attr_cache);
+    if (e != cudaSuccess) return e;
+    return launch_chained(paged_decode_attn_kernel<true>, dim3((unsigned)(pairs * a.team)), dim3(kThreads), with_piece, stream,
+                          a.team, s, a);
+  }
   static int attr_cache[kMaxDevicesCached] = {};
-  cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel, smem, attr_cache);
+  cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<false>, smem, attr_cache);
   if (e != cudaSuccess) return e;
-  e = launch_chained(paged_decode_attn_kernel, dim3(grid), dim3(kThreads), smem, stream, s, a);
+  e = launch_chained(paged_decode_attn_kernel<false>, dim3(grid), dim3(kThreads), smem, stream, 1, s, a);
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_chained(paged_decode_join_kernel, dim3(grid, s.G()), dim3(kJoinWarps * 32), 0, stream, s, parts, a.tails,
+  return launch_chained(paged_decode_join_kernel, dim3(grid, s.G()), dim3(kJoinWarps * 32), 0, stream, 1, s, parts, a.tails,
                         out);
 }
 

@@ -149,7 +149,7 @@ cudaError_t launch_store_kv_q8(const PagedShape& s, const uint16_t* k, size_t k_
   const int per = (long long)n_rows * s.Hkv * 2 <= resident ? 1 : kBS;
   const long long groups = ((long long)n_rows + kWarps * per - 1) / (kWarps * per);
   dim3 grid((unsigned)groups, (unsigned)(2 * s.Hkv));
-  return launch_chained(store_kv_q8_kernel, grid, dim3(kWarps * 32), 0, stream, s, k, k_stride, v, v_stride, slot_map,
+  return launch_chained(store_kv_q8_kernel, grid, dim3(kWarps * 32), 0, stream, 1, s, k, k_stride, v, v_stride, slot_map,
                         n_rows, per, pages, scales, err);
 }
 

@@ -269,7 +269,7 @@ cudaError_t launch_extend_tables(const PagedShape& s, const int* old_len, const 
                                  const int* n_free, int* table, int* len_out, int* n_free_out, int* row_start,
                                  int* slot_map, int n_rows, unsigned* err, cudaStream_t stream) {
   const int grid = n_rows > kRowsPerCta ? (n_rows + kRowsPerCta - 1) / kRowsPerCta : 1;
-  return launch_chained(extend_tables_kernel, dim3(grid), dim3(kThreads), 0, stream, s, old_len, new_len, free_pages,
+  return launch_chained(extend_tables_kernel, dim3(grid), dim3(kThreads), 0, stream, 1, s, old_len, new_len, free_pages,
                         n_free, table, len_out, n_free_out, row_start, slot_map, n_rows, err);
 }
 
@@ -278,7 +278,7 @@ cudaError_t launch_release_tables(const PagedShape& s, const int* len, const int
                                   cudaStream_t stream) {
   const int most = 2 * sm_count();
   const int grid = s.B < most ? s.B : most;
-  return launch_chained(release_tables_kernel, dim3(grid), dim3(kThreads), 0, stream, s, len, keep_len, table, free_pages,
+  return launch_chained(release_tables_kernel, dim3(grid), dim3(kThreads), 0, stream, 1, s, len, keep_len, table, free_pages,
                         n_free, n_free_out, err);
 }
 

@@ -722,7 +722,7 @@ cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_
     regs = fa.numRegs;
   }
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_chained(prompt_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, mq, mk, mv, s, row_start, n_rows,
+  return launch_chained(prompt_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, 1, mq, mk, mv, s, row_start, n_rows,
                         scale * 1.4426950408889634f, out, out_stride, err);
 }
 

@@ -18,10 +18,13 @@ def built():
     build.build()
 
 
-def _inputs(rng, ctx, hkv, hq, q_size=1.0, low=-9, high=-5):
+WIDE = 4000  # columns of a table (entries of a selection) beyond which a pair is not left to one cluster
+
+
+def _inputs(rng, ctx, hkv, hq, q_size=1.0, low=-9, high=-5, wide=False):
     from paged_helpers import bf16, random_pages, shuffled_table
 
-    nb_max = max(1, max(-(-n // 16) for n in ctx))
+    nb_max = WIDE if wide else max(1, max(-(-n // 16) for n in ctx))
     n_pages = sum(-(-max(n, 0) // 16) for n in ctx) + 3
     kv, scale = random_pages(rng, n_pages, hkv, low, high)
     table = shuffled_table(rng, ctx, nb_max, n_pages)
@@ -45,26 +48,28 @@ def _check(c, q, q64, kv, page_scale, table, ctx, sel=None, nsel=None, **kw):
     return out
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
-def test_group_sizes(G):
+def test_group_sizes(G, wide):
     from paged_helpers import cache_of
 
     rng = np.random.default_rng(G)
     ctx = [1, 16, 17, 300, 0, 95]
-    kv, scale, table, q, q64 = _inputs(rng, ctx, 3, 3 * G)
+    kv, scale, table, q, q64 = _inputs(rng, ctx, 3, 3 * G, wide=wide)
     c = cache_of(kv, scale, table, 3 * G)
     out = _check(c, q, q64, kv, scale, table, ctx)
     assert (out[4] == 0).all()
     c.check()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ctx", [[1], [15], [0], [0, 0, 5], [31, 32, 33], [4096], [20000, 3], [700] * 9,
                                  list(range(0, 130)), [257, 16, 0, 8000, 1, 2, 0, 0, 500]])
-def test_lengths(ctx):
+def test_lengths(ctx, wide):
     from paged_helpers import cache_of
 
     rng = np.random.default_rng(sum(ctx))
-    kv, scale, table, q, q64 = _inputs(rng, ctx, 2, 8)
+    kv, scale, table, q, q64 = _inputs(rng, ctx, 2, 8, wide=wide)
     c = cache_of(kv, scale, table, 8)
     _check(c, q, q64, kv, scale, table, ctx)
     c.check()
@@ -82,15 +87,16 @@ def test_many_requests():
     _check(c, q, q64, kv, scale, table, ctx)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("low,high", [(-60, -59), (-40, 30), (60, 100), (100, 110)])
-def test_scales_far_apart(low, high):
+def test_scales_far_apart(low, high, wide):
     """Scales of neighbouring pages many binades apart, values' above all: the page with the large
     ones decides the output, whatever its weight."""
     from paged_helpers import F16_HALF_STEP, cache_of, check_attention, ints
 
     rng = np.random.default_rng(high + 100)
     ctx = [200, 33, 1]
-    kv, scale, table, q, q64 = _inputs(rng, ctx, 2, 4, low=low, high=high)
+    kv, scale, table, q, q64 = _inputs(rng, ctx, 2, 4, low=low, high=high, wide=wide)
     scale[:, :, 0] = 2.0 ** -7  # keys of ordinary size
     c = cache_of(kv, scale, table, 4)
     out = c.decode(q, ints(ctx)).double().cpu().numpy()
@@ -103,21 +109,22 @@ def test_scales_far_apart(low, high):
     check_attention(out, want, mass, size, F16_HALF_STEP, tiny)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("q_size", [0.0, 1e-30, 1e-4, 30.0, 1e4])
-def test_query_sizes(q_size):
+def test_query_sizes(q_size, wide):
     """From equal weights to a softmax that takes one token; rows of different size in one group."""
     from paged_helpers import cache_of
 
     rng = np.random.default_rng(12)
     ctx = [500, 70]
-    kv, scale, table, q, q64 = _inputs(rng, ctx, 2, 8, q_size=1.0)
+    kv, scale, table, q, q64 = _inputs(rng, ctx, 2, 8, q_size=1.0, wide=wide)
     sizes = torch.tensor([q_size, 1.0, q_size, 1e-2, 1.0, q_size, 0.0, 3.0])[:, None]
     q = (q.cpu() * sizes).to(torch.bfloat16)
     c = cache_of(kv, scale, table, 8)
     _check(c, q.cuda(), q.double().numpy(), kv, scale, table, ctx)
 
 
-@pytest.mark.parametrize("most", [1, 5, 40, 200])
+@pytest.mark.parametrize("most", [1, 5, 40, 200, WIDE])
 def test_selected_blocks(most):
     from paged_helpers import cache_of
 
@@ -136,12 +143,13 @@ def test_selected_blocks(most):
     c.check()
 
 
-def test_bad_entries_are_skipped_and_flagged():
+@pytest.mark.parametrize("wide", [False, True])
+def test_bad_entries_are_skipped_and_flagged(wide):
     from paged_helpers import cache_of, ints
 
     rng = np.random.default_rng(13)
     ctx = [100, 50]
-    kv, scale, table, q, q64 = _inputs(rng, ctx, 1, 2)
+    kv, scale, table, q, q64 = _inputs(rng, ctx, 1, 2, wide=wide)
     table[0, 2], table[1, 0] = kv.shape[0], -1
     c = cache_of(kv, scale, table, 2)
     _check(c, q, q64, kv, scale, table, ctx)
@@ -154,7 +162,7 @@ def test_bad_entries_are_skipped_and_flagged():
     c.table.fill_(-1)  # nothing left to attend
     assert (c.decode(q, ints(ctx)) == 0).all()
     c.err.zero_()
-    _check(c, q, q64, kv, scale, np.full_like(table, -1), [-5, 10 ** 9])
+    _check(c, q, q64, kv, scale, np.full_like(table, -1), [-5, 10 ** 9 if not wide else 500])
     assert int(c.err) == 2
 
 
@@ -226,11 +234,12 @@ def test_a_long_cache_past_32_bit_offsets():
     check_attention(out, want[0], want[1], want[2], F16_HALF_STEP, want[3])
 
 
-def test_captured_and_replayed_with_other_lengths():
+@pytest.mark.parametrize("wide", [False, True])
+def test_captured_and_replayed_with_other_lengths(wide):
     from paged_helpers import cache_of, ints
 
     rng = np.random.default_rng(19)
-    kv, scale, table, q, q64 = _inputs(rng, [3000, 3000, 3000], 2, 8)
+    kv, scale, table, q, q64 = _inputs(rng, [3000, 3000, 3000], 2, 8, wide=wide)
     kv[kv & 0x7f == 0x7f] = 0
     c = cache_of(kv, scale, table, 8)
     ctx = ints([3000, 1, 0])
@@ -249,7 +258,8 @@ def test_captured_and_replayed_with_other_lengths():
         check_attention(out.double().cpu().numpy(), want[0], want[1], want[2], F16_HALF_STEP, want[3])
 
 
-def test_two_captured_graphs_and_two_streams():
+@pytest.mark.parametrize("wide", [False, True])
+def test_two_captured_graphs_and_two_streams(wide):
     """Graphs of two batches replayed at the same time on two streams, and an eager call beside them:
     no call's scratch is another's."""
     from paged_helpers import cache_of, ints
@@ -257,7 +267,7 @@ def test_two_captured_graphs_and_two_streams():
     rng = np.random.default_rng(18)
     cases = []
     for ctx in ([5000, 17, 900], [64, 3000, 1]):
-        kv, scale, table, q, q64 = _inputs(rng, ctx, 4, 16)
+        kv, scale, table, q, q64 = _inputs(rng, ctx, 4, 16, wide=wide)
         cases.append((cache_of(kv, scale, table, 16), q, ints(ctx)))
     eager = [c.decode(q, n).clone() for c, q, n in cases]
     torch.cuda.synchronize()

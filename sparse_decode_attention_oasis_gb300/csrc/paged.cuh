@@ -15,6 +15,21 @@ struct PagedShape {
 constexpr int kScaleELow = -60, kScaleEHigh = 119;
 constexpr long long kHeadPageBytes = 2LL * kBS * kD;  // keys and values of one head in one page
 
+// 16-byte loads (coherent: see launch_chained); the second leaves no line in L1.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint4 load16_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
 
 // Two e4m3 (low 16 bits of w) -> two halves, exact.
@@ -38,7 +53,9 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 
 // Kernels of a decode step follow each other closely: each is launched while its predecessor in the
 // stream still runs (programmatic stream serialization), sets itself up, and waits for the
-// predecessor's end before it touches global memory.
+// predecessor's end before it touches global memory.  What the predecessor writes changes while
+// such a kernel lives: so none of its pointers is __restrict__, and no load takes the
+// non-coherent path, either of which would let a load pass the wait.
 __device__ __forceinline__ void wait_for_predecessor() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");

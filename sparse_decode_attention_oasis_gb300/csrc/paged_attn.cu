@@ -129,19 +129,19 @@ struct Rows {  // a lane's 16-byte pieces of a page's keys and values
 // Keys: rows lane / 4 and + 8, dimensions 16 (lane % 4) .. and 64 + 16 (lane % 4) ..
 __device__ __forceinline__ void load_keys(Rows& k, const uint8_t* page, int lane) {
   const uint8_t* p = page + (lane >> 2) * kD + (lane & 3) * 16;
-  k.v[0] = ldg_stream(p);
-  k.v[1] = ldg_stream(p + 64);
-  k.v[2] = ldg_stream(p + 8 * kD);
-  k.v[3] = ldg_stream(p + 8 * kD + 64);
+  k.v[0] = load16_stream(p);
+  k.v[1] = load16_stream(p + 64);
+  k.v[2] = load16_stream(p + 8 * kD);
+  k.v[3] = load16_stream(p + 8 * kD + 64);
 }
 
 // Values: tokens 2 (lane % 4), + 1, + 8, + 9, dimensions 16 (lane / 4) ..
 __device__ __forceinline__ void load_values(Rows& v, const uint8_t* page, int lane) {
   const uint8_t* p = page + kBS * kD + (lane & 3) * 2 * kD + (lane >> 2) * 16;
-  v.v[0] = ldg_stream(p);
-  v.v[1] = ldg_stream(p + kD);
-  v.v[2] = ldg_stream(p + 8 * kD);
-  v.v[3] = ldg_stream(p + 9 * kD);
+  v.v[0] = load16_stream(p);
+  v.v[1] = load16_stream(p + kD);
+  v.v[2] = load16_stream(p + 8 * kD);
+  v.v[3] = load16_stream(p + 9 * kD);
 }
 
 struct Shared {
@@ -268,10 +268,10 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
         if ((lane >> 2) < G) {
           const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * 16;
-          w[0] = ldg_nc(src);
-          w[1] = ldg_nc(src + 8);
-          w[2] = ldg_nc(src + 64);
-          w[3] = ldg_nc(src + 72);
+          w[0] = load16(src);
+          w[1] = load16(src + 8);
+          w[2] = load16(src + 64);
+          w[3] = load16(src + 72);
         }
         uint32_t m = 0;
 #pragma unroll
@@ -531,8 +531,8 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
 // Joins the pieces of a pair that starts in block blockIdx.x and ends in a later one, one query
 // row to a thread block: its warps take every kWarps-th piece, a lane four dimensions.
 __global__ void __launch_bounds__(kJoinWarps * 32)
-paged_decode_join_kernel(PagedShape s, const float* __restrict__ parts, const int2* __restrict__ tails,
-                         uint16_t* __restrict__ out) {
+paged_decode_join_kernel(PagedShape s, const float* parts, const int2* tails,
+                         uint16_t* out) {
   __shared__ float rows[kJoinWarps][kRowFloats];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = s.Hq / s.Hkv, r = blockIdx.y, first = blockIdx.x;

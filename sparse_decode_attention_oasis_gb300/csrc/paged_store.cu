@@ -44,9 +44,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
 
 // grid: x = groups of kWarps * rows_per_warp rows, y = heads * 2 (K, V).
 __global__ void __launch_bounds__(kWarps * 32)
-store_kv_q8_kernel(PagedShape s, const uint16_t* __restrict__ k, size_t k_stride, const uint16_t* __restrict__ v,
-                   size_t v_stride, const int* __restrict__ slot_map, int n_rows, int rows_per_warp,
-                   uint8_t* __restrict__ pages, float* __restrict__ scales, unsigned* __restrict__ err) {
+store_kv_q8_kernel(PagedShape s, const uint16_t* k, size_t k_stride, const uint16_t* v,
+                   size_t v_stride, const int* slot_map, int n_rows, int rows_per_warp,
+                   uint8_t* pages, float* scales, unsigned* err) {
   wait_for_predecessor();
   const int lane = threadIdx.x & 31;
   const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
@@ -91,7 +91,7 @@ store_kv_q8_kernel(PagedShape s, const uint16_t* __restrict__ k, size_t k_stride
 #pragma unroll
     for (int i = 0; i < kBS / 2; ++i) {
       const int t = 2 * i + half;
-      x[i] = t < len ? ldg_stream(base + (size_t)t * stride) : make_uint4(0u, 0u, 0u, 0u);
+      x[i] = t < len ? load16_stream(base + (size_t)t * stride) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < kBS / 2; ++i) {

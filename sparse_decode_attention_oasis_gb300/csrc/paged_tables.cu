@@ -70,10 +70,10 @@ struct RowSpan {  // a request with rows in this thread block's range
 };
 
 __global__ void __launch_bounds__(kThreads)
-extend_tables_kernel(PagedShape s, const int* __restrict__ old_len, const int* __restrict__ new_len,
-                     const int* __restrict__ free_pages, const int* __restrict__ n_free_in,
-                     int* __restrict__ table, int* __restrict__ len_out, int* __restrict__ n_free_out,
-                     int* __restrict__ row_start, int* __restrict__ slot_map, int n_rows, unsigned* __restrict__ err) {
+extend_tables_kernel(PagedShape s, const int* old_len, const int* new_len,
+                     const int* free_pages, const int* n_free_in,
+                     int* table, int* len_out, int* n_free_out,
+                     int* row_start, int* slot_map, int n_rows, unsigned* err) {
   __shared__ RowSpan spans[kSpans + 1];
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ int taken_max[kThreads / 32];
@@ -218,9 +218,9 @@ extend_tables_kernel(PagedShape s, const int* __restrict__ old_len, const int* _
 // Request b's released pages go to places n_free + (prefix over requests) of the
 // free list; the blocks of a request are copied by one thread block.
 __global__ void __launch_bounds__(kThreads)
-release_tables_kernel(PagedShape s, const int* __restrict__ len, const int* __restrict__ keep_len,
-                      const int* __restrict__ table, int* __restrict__ free_pages,
-                      const int* __restrict__ n_free_in, int* __restrict__ n_free_out, unsigned* __restrict__ err) {
+release_tables_kernel(PagedShape s, const int* len, const int* keep_len,
+                      const int* table, int* free_pages,
+                      const int* n_free_in, int* n_free_out, unsigned* err) {
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ long long chunk0[kThreads];
   wait_for_predecessor();

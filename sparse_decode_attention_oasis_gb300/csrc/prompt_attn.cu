@@ -292,9 +292,9 @@ struct Schedule {
 
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, PagedShape s, const int* __restrict__ row_start,
-                   int n_rows, float scale_log2, uint16_t* __restrict__ out, size_t out_stride,
-                   unsigned* __restrict__ err) {
+                   const __grid_constant__ CUtensorMap map_v, PagedShape s, const int* row_start,
+                   int n_rows, float scale_log2, uint16_t* out, size_t out_stride,
+                   unsigned* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * kTileBytes;

@@ -106,3 +106,54 @@ def test_the_sparse_path_selects_for_the_paged_cache():
     check_attention(out, want[0], want[1], want[2], F16_HALF_STEP, want[3])
     dense = c.decode(q).double().cpu().numpy()
     assert np.abs(dense[1] - out[1]).max() <= 2.0 ** -7 * np.abs(out[1]).max()  # all its blocks, in another order or split
+
+
+def test_calls_that_follow_closely_see_what_the_call_before_wrote():
+    """A kernel is launched while its predecessor still drains: a run without a pause gives the bits of
+    a run that waits for the device after every call (outputs, pages and scales).  Values of very
+    different sizes make the stores rescale pages that the step before attended."""
+    from sparse_decode_attention_oasis_gb300.paged import PagedKV, prompt_attn
+
+    batch, hkv, hq, steps = 24, 8, 32, 40
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def rows(n, heads, size=1.0):
+        return (torch.randn((n, heads, 128), device="cuda", generator=g) * size).bfloat16()
+
+    def run(cache, pause):
+        outs = []
+        plan = cache.extend(lens, n)
+        pause()
+        outs.append(prompt_attn(q, k, v, plan.row_start))
+        pause()
+        cache.store(k, v, plan.slot_map)
+        pause()
+        cache.commit(plan)
+        for kk, vv, qq in new:
+            longer = cache.lens + 1
+            pause()
+            plan = cache.extend(longer, batch)
+            pause()
+            cache.store(kk, vv, plan.slot_map)
+            pause()
+            outs.append(cache.decode(qq, plan.lens))
+            pause()
+            cache.commit(plan)
+        cache.check()
+        return outs
+
+    for _ in range(4):
+        lens = torch.randint(1, 300, (batch,), dtype=torch.int32, device="cuda", generator=g)
+        n = int(lens.sum())
+        q, k, v = rows(n, hq), rows(n, hkv), rows(n, hkv)
+        new = [(rows(batch, hkv, 2.0 ** (i % 9 - 4)), rows(batch, hkv, 2.0 ** (i * 5 % 11 - 5)), rows(batch, hq))
+               for i in range(steps)]
+        caches = [PagedKV(n_pages=batch * 22, batch=batch, nb_max=22, n_q_heads=hq, n_kv_heads=hkv) for _ in range(2)]
+        for c in caches:
+            c.kv.zero_()
+        torch.cuda.synchronize()
+        got = run(caches[0], lambda: None)
+        want = run(caches[1], torch.cuda.synchronize)
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), f"call {i}"
+        assert torch.equal(caches[0].kv, caches[1].kv) and torch.equal(caches[0].scale, caches[1].scale)

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/oasis.h"
 
 namespace oasis {
@@ -165,12 +167,17 @@ inline int sm_count() {
 }
 
 // Raise a kernel's dynamic shared-memory limit once per device (and when a larger
-// size is needed); `cache` is that kernel's per-device record.
+// size is needed); `cache` is that kernel's per-device record.  The test and the call
+// that sets the limit are one step: of two threads with different sizes, the smaller
+// could otherwise set its own last, below what the other launches with.
 inline cudaError_t ensure_dyn_smem(const void* fn, size_t bytes, int* cache) {
   const int dev = current_device();
+  if (__atomic_load_n(&cache[dev], __ATOMIC_ACQUIRE) >= (int)bytes) return cudaSuccess;
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
   if (cache[dev] >= (int)bytes) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) cache[dev] = (int)bytes;
+  if (e == cudaSuccess) __atomic_store_n(&cache[dev], (int)bytes, __ATOMIC_RELEASE);
   return e;
 }
 

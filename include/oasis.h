@@ -778,7 +778,8 @@ OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const v
  *   scale     softmax scale, > 0 and finite
  *   workspace device scratch, 16-byte aligned, ws_bytes >=
  *             oasis_paged_attn_workspace_bytes(shape); contents on entry are
- *             ignored; calls that may overlap need different ones
+ *             ignored; calls that may overlap need different ones (calls
+ *             on one stream do not, from whichever host threads they come)
  *   out       device bf16 [B][Hq][d], 16-byte aligned: the activation type that the
  *             output projection reads
  *   err_word  device uint32 [1] or NULL

@@ -619,6 +619,9 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   static int attr_cache[kMaxDevicesCached] = {};
   cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<false>, smem, attr_cache);
   if (e != cudaSuccess) return e;
+  // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
+  static std::mutex both[kMaxDevicesCached];
+  std::lock_guard<std::mutex> lock(both[current_device()]);
   e = launch_chained(paged_decode_attn_kernel<false>, dim3(grid), dim3(kThreads), smem, stream, 1, s, a);
   if (e != cudaSuccess || grid == 1) return e;
   return launch_chained(paged_decode_join_kernel, dim3(grid, s.G()), dim3(kJoinWarps * 32), 0, stream, 1, s, parts, a.tails,

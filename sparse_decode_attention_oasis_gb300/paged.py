@@ -25,7 +25,8 @@ A prompt's pass, layer by layer, and a decode step::
 
 Calls run on the current stream of the tensors' device and can be captured into a CUDA
 graph; nothing is kept between calls but the tensors above and decode's scratch, one for
-each stream (calls on one stream follow each other).  A captured call takes scratch of its
+each stream (calls on one stream follow each other, those of several host threads as well:
+the library keeps a call's launches together).  A captured call takes scratch of its
 own from the graph's memory pool, so graphs, and calls on other streams, never share it.
 
 The methods call the library directly with addresses and sizes: for a decode step's small

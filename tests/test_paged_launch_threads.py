@@ -1,5 +1,5 @@
-"""Two host threads in the decode attention at once, on a made-up CUDA runtime (no GPU): no thread lowers
-the shared-memory limit below what another launches with."""
+"""Two host threads in the decode attention at once, on a made-up CUDA runtime (no GPU): a call's two
+launches stay together, and no thread lowers the shared-memory limit below what another launches with."""
 import os
 import shutil
 import subprocess
@@ -28,6 +28,15 @@ def _run(program, mode):
     r = subprocess.run([program, mode], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stderr
     return dict(line.split(" ", 1) for line in r.stdout.strip().splitlines())
+
+
+def test_a_calls_launches_are_not_parted(program):
+    """The second launch reads what the first one left in the stream's scratch."""
+    out = _run(program, "launches")
+    assert out["status"] == "0 0"
+    order = out["order"]
+    assert len(order) == 20 and all(order[i] == order[i + 1] for i in range(0, 20, 2)), order
+    assert "ab" in order or "ba" in order  # the threads did meet
 
 
 def test_limits_of_shared_memory_only_grow(program):

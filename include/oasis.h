@@ -765,7 +765,8 @@ OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const v
  * of request b (sel NULL), or those that sel lists for (b, h), and query head
  * hq = h*G + g:
  *   out[b][hq] = sum over tokens t < ctx_len[b] of A_bh of softmax_t(scale * q.k_t) v_t,
- *   or zero when A_bh has no valid token.
+ *   or zero when A_bh has no valid token.  A query row that holds NaN or an
+ *   infinity, or whose scores are all -inf, gives NaN in its own output row alone.
  * Arguments:
  *   q         device bf16, B rows of [Hq][d], stride q_stride
  *   kv_pages, kv_scale, block_table   as above (read only)

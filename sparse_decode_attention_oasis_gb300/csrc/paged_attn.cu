@@ -53,6 +53,9 @@ constexpr int kJoinWarps = 4;
 constexpr int kMaxG = 8;
 constexpr int kRowFloats = kD + 2;
 constexpr float kSlack = 8.0f;  // log2 of the largest weight
+// The least running reference of a row that has seen a token: a row without tokens keeps -inf and gets zeros, one
+// whose scores are all NaN or -inf gets the softmax's NaN (its sum is NaN or 0), however its pages are split.
+constexpr float kLowest = -3e38f;
 
 struct Args {
   const uint16_t* q;
@@ -121,6 +124,9 @@ struct State {
     sum[0] = sum[1] = 0.f;
   }
 };
+
+// What a row's accumulators are multiplied with at the end: 0 where it has no token.
+__device__ __forceinline__ float inverse(float top, float sum) { return top == neg_inf() ? 0.f : 1.0f / sum; }
 
 struct Rows {  // a lane's 16-byte pieces of a page's keys and values
   uint4 v[4];
@@ -367,7 +373,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
             if (t + 8 >= valid) vr.v[2] = make_uint4(0u, 0u, 0u, 0u);
             if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
           }
-          float m0 = fmaxf(s0, s2), m1 = fmaxf(s1, s3);
+          float m0 = fmaxf(fmaxf(s0, s2), kLowest), m1 = fmaxf(fmaxf(s1, s3), kLowest);
           if (__any_sync(0xffffffffu, m0 > st.top[0] + kSlack || m1 > st.top[1] + kSlack)) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -375,8 +381,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
               m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
             }
             const float n0 = fmaxf(st.top[0], m0), n1 = fmaxf(st.top[1], m1);
-            const float c0 = st.top[0] == neg_inf() ? 0.f : exp2f(st.top[0] - n0);
-            const float c1 = st.top[1] == neg_inf() ? 0.f : exp2f(st.top[1] - n1);
+            const float c0 = exp2f(st.top[0] - n0), c1 = exp2f(st.top[1] - n1);  // 0 for the first page
             st.top[0] = n0;
             st.top[1] = n1;
             st.sum[0] *= c0;
@@ -389,8 +394,8 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
               st.acc[m][3] *= c1;
             }
           }
-          const float r0 = st.top[0] == neg_inf() ? 0.f : st.top[0], r1 = st.top[1] == neg_inf() ? 0.f : st.top[1];
-          const float w0 = exp2f(s0 - r0), w1 = exp2f(s1 - r1), w2 = exp2f(s2 - r0), w3 = exp2f(s3 - r1);
+          const float w0 = exp2f(s0 - st.top[0]), w1 = exp2f(s1 - st.top[1]);
+          const float w2 = exp2f(s2 - st.top[0]), w3 = exp2f(s3 - st.top[1]);
           const float iv = pow2f(-(int)lv);
           st.sum[0] = fmaf(w0 + w2, iv, st.sum[0]);
           st.sum[1] = fmaf(w1 + w3, iv, st.sum[1]);
@@ -422,7 +427,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         const int r = (lane & 3) * 2 + i;
         if (r >= G) continue;
         if (whole) {
-          const float inv = st.sum[i] > 0.f ? 1.0f / st.sum[i] : 0.f;
+          const float inv = inverse(st.top[i], st.sum[i]);
           uint32_t w[8];
 #pragma unroll
           for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(st.acc[m][i] * inv, st.acc[m][2 + i] * inv);
@@ -489,7 +494,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     const int e = sh.slot_pair[lead];
     const bool starts = sh.slot_lo[lead] >= c_lo;
     if (starts && sh.slot_hi[lead] <= c_hi && !(kClustered && team > 1)) {
-      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+      const float inv = inverse(top, sum);
       reinterpret_cast<uint2*>(a.out + ((long long)e * G + r) * kD)[lane] =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     } else {
@@ -503,7 +508,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
   if constexpr (kClustered) {
     if (team == 1) return;
     if (leads == 0)  // no page of the pair for this block
-      for (int r = tid; r < G; r += kThreads) *reinterpret_cast<float2*>(piece + r * kRowFloats + kD) = make_float2(neg_inf(), 0.f);
+      for (int i = tid; i < G * kRowFloats; i += kThreads) piece[i] = i % kRowFloats == kD ? neg_inf() : 0.f;
     cluster_sync();
     // row r is joined by warp r / team of block r % team
     const int r = warp * team + rank;
@@ -514,13 +519,13 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
       const float f = ts.x == neg_inf() ? 0.f : exp2f(ts.x - top);
       const float sum = warp_sum(f * ts.y);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int c = 0; c < team; ++c) {
         const float fc = __shfl_sync(0xffffffffu, f, c);
-        if (fc == 0.f) continue;  // nothing there, or as good as nothing
         const float2 u = load_remote(row + lane * 4, c), v = load_remote(row + lane * 4 + 2, c);
         o = make_float4(fmaf(fc, u.x, o.x), fmaf(fc, u.y, o.y), fmaf(fc, v.x, o.z), fmaf(fc, v.y, o.w));
       }
-      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+      const float inv = inverse(top, sum);
       reinterpret_cast<uint2*>(a.out + ((long long)(blockIdx.x / team) * G + r) * kD)[lane] =
           make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
@@ -574,7 +579,7 @@ paged_decode_join_kernel(PagedShape s, const float* parts, const int2* tails,
       o1 = fmaf(f, rows[w][2 * d + 1], o1);
     }
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  const float inv = inverse(m, l);
   *reinterpret_cast<uint32_t*>(out + ((long long)t.x * G + r) * kD + 2 * d) = pack_bf16x2(o0 * inv, o1 * inv);
 }
 

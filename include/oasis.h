@@ -767,6 +767,11 @@ OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const v
  *   out[b][hq] = sum over tokens t < ctx_len[b] of A_bh of softmax_t(scale * q.k_t) v_t,
  *   or zero when A_bh has no valid token.  A query row that holds NaN or an
  *   infinity, or whose scores are all -inf, gives NaN in its own output row alone.
+ *   Scores, weights and sums are fp32.  For the product with the values a weight
+ *   is rounded to fp16: by 2^-11 of itself at most, and where weight times value
+ *   scale is below 2^-25 of its largest, by 2^-36 of that.  Value scales of one
+ *   request may lie up to 2^100 apart; beyond that, tokens of the small ones
+ *   can drop out of the softmax's sum.
  * Arguments:
  *   q         device bf16, B rows of [Hq][d], stride q_stride
  *   kv_pages, kv_scale, block_table   as above (read only)

@@ -4,8 +4,9 @@
 // row: w_t = 2^(c s_t + lv_t - M), o = sum w_t v8_t / sum w_t 2^-lv_t, where
 // s_t = q . k8_t * 2^lk_t, lk and lv the exponents of the page's key and value scale
 // and c = scale * log2(e).  Taking lv into the exponent keeps the weights of pages
-// with different scales inside one fp16 range; M moves only when a score passes it
-// by more than 2^8, so most pages need no rescaling of the accumulators.
+// with different scales inside one fp16 range.  M lies 11 below the score that set it and
+// moves only when a score passes it by more than 15, so most pages need no rescaling of
+// the accumulators and the largest weight is always 2^11 to 2^15 of fp16's 2^16.
 //
 // Work: one warp takes one page (16 tokens of one KV head) at a time, straight from
 // global memory into mma.sync fragments, without shared memory:
@@ -18,9 +19,11 @@
 // e4m3 converts to fp16 exactly; q is scaled by a power of two for each row so that
 // its largest value lies in [2^14, 2^15), then converts to fp16 without rounding
 // (bf16 has 8 significant bits, fp16 11; values 2^29 below the row's largest lose
-// bits, 2^-40 of the score).  Roundings: w to fp16 (2^-11 of its value at most) for the product
-// with V, the output to bf16 (2^-8, which dominates); s, w, the sums and the
-// accumulators are fp32.
+// bits, 2^-40 of the score).  Roundings: w to fp16 for the product with V (2^-11 of its value at
+// most; below 2^-25 of the largest weight of the warp's tokens, scales included, 2^-36 of that), the
+// output to bf16 (2^-8, which dominates); s, w, the sums and the accumulators are fp32.
+// The largest weight near 1 lost the others at 2^-25 of it: beside a leader of 20 nats
+// with a zero value nothing was left of its warp's other tokens.  Lifts of 7, 11 and 13 bits cost the same time.
 //
 // Split: the pages of all (request, KV head) pairs form one sequence, cut into equal
 // ranges for the thread blocks and again for their warps, whatever the lengths are.
@@ -52,7 +55,7 @@ constexpr int kMinPages = 8;  // pages a thread block gets at least, when there 
 constexpr int kJoinWarps = 4;
 constexpr int kMaxG = 8;
 constexpr int kRowFloats = kD + 2;
-constexpr float kSlack = 8.0f;  // log2 of the largest weight
+constexpr float kLift = 11.0f, kMostBits = 15.0f;  // log2 of the weight of the score that sets M, of the largest weight
 // The least running reference of a row that has seen a token: a row without tokens keeps -inf and gets zeros, one
 // whose scores are all NaN or -inf gets the softmax's NaN (its sum is NaN or 0), however its pages are split.
 constexpr float kLowest = -3e38f;
@@ -374,13 +377,13 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
             if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
           }
           float m0 = fmaxf(fmaxf(s0, s2), kLowest), m1 = fmaxf(fmaxf(s1, s3), kLowest);
-          if (__any_sync(0xffffffffu, m0 > st.top[0] + kSlack || m1 > st.top[1] + kSlack)) {
+          if (__any_sync(0xffffffffu, m0 > st.top[0] + kMostBits || m1 > st.top[1] + kMostBits)) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
               m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
               m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
             }
-            const float n0 = fmaxf(st.top[0], m0), n1 = fmaxf(st.top[1], m1);
+            const float n0 = fmaxf(st.top[0], m0 - kLift), n1 = fmaxf(st.top[1], m1 - kLift);
             const float c0 = exp2f(st.top[0] - n0), c1 = exp2f(st.top[1] - n1);  // 0 for the first page
             st.top[0] = n0;
             st.top[1] = n1;

@@ -14,9 +14,10 @@ share the tables:
 A prompt's pass, layer by layer, and a decode step::
 
     plan = cache.extend(lens, n_rows)                  # pages and slots of the new tokens
-    out = prompt_attn(q, k, v, plan.row_start)         # requests that held nothing before
+    out = cache.prompt(q, k, v, plan)                  # requests that held nothing before
     cache.store(k, v, plan.slot_map, layer)
     cache.commit(plan)
+    cache.check()                                      # raises what the kernels reported
     ...
     plan = cache.extend(cache.lens + 1, batch)
     cache.store(k, v, plan.slot_map, layer)
@@ -98,7 +99,11 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: to
                 err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Causal attention over packed prompts: q [rows, Hq, 128], k and v [rows, Hkv, 128] in
     bf16 (slices of one buffer as well), sequence b in rows row_start[b] .. row_start[b+1] - 1.
-    Rows of no sequence are left as they are in out (zero where out is allocated here)."""
+    Rows of no sequence are left as they are in out (zero where out is allocated here).
+
+    A row attends the call's own rows of its sequence and nothing that a cache holds.  Errors
+    (a bad row_start, a wait inside the kernel that gave up: incomplete output) go to err and
+    nowhere else; :meth:`PagedKV.prompt` passes the cache's."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [rows, heads, 128]")
     n, hq, hkv, device = q.shape[0], q.shape[1], k.shape[1], q.device
@@ -198,6 +203,14 @@ class PagedKV:
             self.n_free.copy_(left)
             kept = (keep_len >= 0) & (keep_len <= self.lens)  # the others released nothing
             self.lens.copy_(torch.where(kept, keep_len, self.lens))
+
+    def prompt(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Plan, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """:func:`prompt_attn` over a plan's rows; :meth:`check` raises its errors.  For plans whose
+        new rows are all of requests that held nothing before: earlier tokens are not attended."""
+        if q.dim() != 3 or q.shape[1] != self.n_q_heads or k.dim() != 3 or k.shape[1] != self.n_kv_heads:
+            raise ValueError(f"q must be [rows, {self.n_q_heads}, 128], k and v [rows, {self.n_kv_heads}, 128]")
+        return prompt_attn(q, k, v, plan.row_start, scale, out, self.err)
 
     def store(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, layer: int = 0) -> None:
         """Rows k, v [rows, Hkv, 128] (bf16) into the layer's pages at slot_map's slots."""

@@ -666,7 +666,8 @@ OASIS_API oasis_status oasis_trace_set(void* dev_buf, int32_t capacity);
  * A scale is a power of two, 2^e with e in [-60, 119]: the format's relative
  * precision does not depend on it, and moving a page to a larger scale is exact
  * but for values that become subnormal.  e is the least one with
- * amax <= 448 * 2^e, amax over the page's tokens of that head's keys (values).
+ * amax <= 448 * 2^e, amax over the page's tokens of that head's keys (values);
+ * magnitudes above 448 * 2^119 = 1.75 * 2^127 are stored as that.
  *   block_table  device int32 [B][nb_max]   page of request b's block x (tokens
  *                16x .. 16x+15), the same for every layer and head; entries of
  *                blocks past the request's length are never read
@@ -753,7 +754,9 @@ OASIS_API oasis_status oasis_release_tables(const oasis_paged_shape* shape, cons
  *              skipped with OASIS_EW_BAD_COUNT
  *   kv_pages, kv_scale   one layer's, in/out
  *   err_word   device uint32 [1] or NULL
- * n_rows may be 0.  A non-finite input saturates the page's scale (e = 119).
+ * n_rows may be 0.  A non-finite input saturates the page's scale (e = 119): an
+ * infinity is stored as 448 * 2^119, NaN as NaN, and other values of the page and
+ * head up to 2^109 as zero.
  */
 OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const void* k, size_t k_stride,
                                          const void* v, size_t v_stride, const int32_t* slot_map,

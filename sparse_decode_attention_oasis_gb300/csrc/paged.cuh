@@ -10,8 +10,9 @@ struct PagedShape {
   __host__ __device__ int G() const { return Hq / Hkv; }
 };
 
-// Exponent range of a page's scale 2^e (what amax <= 448 * 2^e needs for any
-// finite bf16 is at most 119; below -60 a page's values are as good as zero).
+// Exponent range of a page's scale 2^e.  High: 448 * 2^119 = 1.75 * 2^127 is the largest page value
+// that fp32 holds (448 * 2^120 does not fit), so the finite bf16 above it (up to 1.9922 * 2^127)
+// saturate there, by an eighth at most.  Low: below -60 a page's values are as good as zero.
 constexpr int kScaleELow = -60, kScaleEHigh = 119;
 constexpr long long kHeadPageBytes = 2LL * kBS * kD;  // keys and values of one head in one page
 

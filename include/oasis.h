@@ -808,7 +808,9 @@ OASIS_API oasis_status oasis_paged_decode_attn_q8(const oasis_paged_shape* shape
  * row_start[b+1] - 1; for row i of it and query head hq = h*G + g:
  *   out[i][hq] = sum over rows j <= i of sequence b of softmax_j(scale * q_i.k_j) v_j.
  * Rows that belong to no sequence are not written, and what they hold (NaN
- * included) does not matter.
+ * included) does not matter.  A row whose scores are NaN or all -inf gives NaN.
+ * Scores, weights and sums are fp32; for the product with the values a weight is
+ * rounded to bf16 (2^-8 of itself at most), the sums keep it unrounded.
  *   q, k, v    device bf16, n_rows rows of [Hq][d], [Hkv][d], [Hkv][d], with strides
  *   row_start  device int32 [B+1], not decreasing, inside [0, n_rows] (the row_start
  *              of oasis_extend_tables when every old_len is 0); a sequence that

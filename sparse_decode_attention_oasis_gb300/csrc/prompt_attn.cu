@@ -64,6 +64,8 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(12 * kLaunchRegs >= 8 * kSoftmaxRegs + 4 * kOtherRegs, "register split");
 constexpr int kConsumers = 11;               // warps that read an item: softmax, MMA, producer
 constexpr float kSlack = 8.0f;
+// The least reference: a first tile whose scores are all -inf leaves it there, below every finite score.
+constexpr float kLowest = -3e38f;
 
 struct Item {
   int row0;   // first row of the sequence, -1: no more items
@@ -404,7 +406,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                : fmaxf(m[d], __uint_as_float(x[c + d]));
         const float big = scale_log2 * max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
         if (j == 0) {
-          ref = big == neg_inf() ? 0.f : big;
+          ref = fmaxf(big, kLowest);
         } else if (__any_sync(0xffffffffu, big > ref + kSlack)) {
           // S_j is there, so the product with V_(j-1) is complete and O is at rest until P_j is handed over
           const float next = fmaxf(ref, big), f = ex2(ref - next);
@@ -458,7 +460,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       unpack2(sum_a, a, b);
       unpack2(sum_b, d, e);
       const float total = (a + b) + (d + e);
-      const float inv = total > 0.f ? 1.0f / total : 0.f;
+      const float inv = 1.0f / total;  // every row has a key; no finite score at all gives NaN
       const bool live = row < per * G && tok < it.len;
       uint16_t* dst = out + (size_t)(it.row0 + (live ? tok : 0)) * out_stride + (size_t)(it.h * G + g) * kD;
 #pragma unroll 1

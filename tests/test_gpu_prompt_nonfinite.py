@@ -47,26 +47,6 @@ def _inputs(seed, n, hkv, G):
     return (torch.randn((n, h, 128), generator=g).to(torch.bfloat16) for h in (hkv * G, hkv, hkv))
 
 
-PLACES = [[0], [1], [77], [126, 128], [127], [255], [299], [302], [40, 41, 200, 430], list(range(60, 300, 7))]
-
-
-@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("places", PLACES, ids=str)
-@pytest.mark.parametrize("G", [1, 3, 4, 8])
-def test_a_value_reaches_no_earlier_row(G, places, value):
-    q, k, v = _inputs(G, 440, 2, G)
-    for i, p in enumerate(places):
-        v[p, i % 2, (p * 37) % 128] = value if i % 3 < 2 else -value
-    _check(q, k, v, [0, 300, 305, 435])
-
-
-@pytest.mark.parametrize("G", [1, 4])
-def test_rows_of_values_that_are_all_nan(G):
-    q, k, v = _inputs(9, 700, 1, G)
-    v[333:] = float("nan")
-    _check(q, k, v, [0, 600, 690])
-
-
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("G", [1, 4])
 def test_a_key_reaches_no_earlier_row(G, value):

@@ -808,7 +808,8 @@ OASIS_API oasis_status oasis_paged_decode_attn_q8(const oasis_paged_shape* shape
  * row_start[b+1] - 1; for row i of it and query head hq = h*G + g:
  *   out[i][hq] = sum over rows j <= i of sequence b of softmax_j(scale * q_i.k_j) v_j.
  * Rows that belong to no sequence are not written, and what they hold (NaN
- * included) does not matter.  A row whose scores are NaN or all -inf gives NaN.
+ * included) does not matter; an infinity or NaN in a sequence's row reaches that
+ * row and later ones only.  A row whose scores are NaN or all -inf gives NaN.
  * Scores, weights and sums are fp32; for the product with the values a weight is
  * rounded to bf16 (2^-8 of itself at most), the sums keep it unrounded.
  *   q, k, v    device bf16, n_rows rows of [Hq][d], [Hkv][d], [Hkv][d], with strides

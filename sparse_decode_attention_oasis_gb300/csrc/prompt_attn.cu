@@ -25,10 +25,18 @@
 //                     both tiles and general loops a pair of tiles took 3,200 cycles, so it now is a warp for
 //                     each tile, one lane from end to end, and loops without a condition to spare;
 //   warp 9            TMA producer: Q tiles, and K and V tiles of 128 tokens in a ring of 5;
-//   warp 10           scheduler: finds this block's work items and hands them to the others.
+//   warp 10           scheduler: finds this block's work items and hands them to the others; and it looks over
+//                     the V tiles with tokens that not all rows of an item attend.
 // TMEM: two S/P and two O tiles of 128 columns, all 512.  Shared memory: 64 KB of Q and a ring
-// of 160 KB.  V rows behind a sequence's last token (another sequence's, or padding that
-// may hold NaN) are zeroed in shared memory before the product: zero times NaN is not zero.
+// of 160 KB.
+//
+// Zero times NaN is not zero: a masked weight does not keep an infinity or NaN of V out.  So V rows behind
+// a sequence's last token (another sequence's, or padding) are zeroed in shared memory before the product, and
+// infinities and NaN in rows after an item's first token as well; the output rows that do attend those get them
+// back at the block's end, from global memory.  The look at a tile runs beside its scores' product and softmax and
+// costs where an item has few tiles: one prompt of 128 tokens 8.1 -> 8.4 us, 16 of 512 52.2 -> 53.4, twelve
+// packed 163.5 -> 164.8, one of 16,384 within its noise; what a warp of its own for the ragged tiles saves the producer
+// outweighs it for 700 prompts of 20 tokens (108 -> 105).  By the softmax warps at their output it was 8 to 12% more.
 //
 // Bound: the tensor cores, 4 x 128 x 128 x 128 multiply-adds for a pair of tiles, 2,048 cycles; a
 // pair takes 2,300 to 2,600, the chain S -> softmax (1,250 cycles) -> product of one tile being longer than
@@ -79,11 +87,13 @@ struct Bars {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: the weights of a tile's first and second 64 tokens
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t tail, done[2];
+  uint64_t raw_full[kRing];  // V tiles that the scheduler warp has to look over first
+  uint64_t done[2];
   Item items[kItems];
   uint32_t tmem_base;
   int abort_flag;
   int token;  // 1: a row tile's products are being issued
+  int cleaned;  // 1: infinities or NaN of V were taken out of a tile
 };
 
 constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars);
@@ -175,6 +185,43 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ bool finite(uint32_t w) { return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u; }
+// Whether 16-byte pieces c0 .. c1 - 1 of both halves of a tile hold no infinity and no NaN: one warp.
+__device__ __forceinline__ bool all_finite(uint32_t at, int c0, int c1, int lane) {
+  uint32_t odd[4] = {0, 0, 0, 0};  // sums of products: not finite if a value is not (or at 2^64, which costs a second look)
+  for (int c = c0 + lane; c - lane < c1; c += 2 * 32) {
+    uint4 x[4];  // pieces c and c + 32 of both halves; behind the last one, that again
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = lds16(at + (u & 1) * kHalf + min(c + (u >> 1) * 32, c1 - 1) * 16);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      odd[2 * (u & 1)] = fma_bf16x2(x[u].x, x[u].y, odd[2 * (u & 1)]);
+      odd[2 * (u & 1) + 1] = fma_bf16x2(x[u].z, x[u].w, odd[2 * (u & 1) + 1]);
+    }
+  }
+  return __all_sync(0xffffffffu, finite(odd[0]) && finite(odd[1]) && finite(odd[2]) && finite(odd[3]));
+}
+
+// A pair of bf16 with infinities and NaN as zeros.
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// The first K/V tile of an item with tokens after the item's first one.
+__device__ __forceinline__ int first_masked(const Item& it) { return (it.tok0 + 1) / kTile; }
 
 // K/V tiles that query tile i of an item reads (0: the tile has no token).
 __device__ __forceinline__ int kv_tiles(const Item& it, int i, int per) {
@@ -290,12 +337,117 @@ struct Schedule {
     }
     return false;
   }
+  // Item k of this block (row0 -1: there are no more; calls with rising k): rounds of gridDim.x items, every second one
+  // in the other direction (32 bits: the rows of K alone limit items to a 32nd of what the GPU's memory holds).
+  __device__ Item item(int k, int heads) {
+    const unsigned at = (unsigned)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    int a = 0, z = 0, place = 0;
+    if (!find((int)(at / (unsigned)heads), a, z, place)) return Item{-1, 0, 0, 0};
+    return Item{a, z - a, place * pair, (int)(at % (unsigned)heads)};
+  }
 };
+
+// Adds to a block's output rows what was taken out of V: infinities and NaN of the tokens from an item's second to each
+// row's own.  An item to a warp of the first eight, four dimensions to a lane; rare, so out of the kernel's own code.
+__device__ __noinline__ void give_back(int sequences, int heads, int G, const int* row_start, int n_rows, const uint16_t* v,
+                                       size_t v_stride, uint16_t* out, size_t out_stride) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tokens = 2 * (kTile / G);
+  Schedule sch;
+  sch.init(row_start, sequences, n_rows, tokens, lane);
+  for (int k = 0;; ++k) {
+    const Item it = sch.item(k, heads);
+    if (it.row0 < 0) return;
+    if (k % 8 != warp) continue;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t = it.tok0 + 1; t < min(it.len, it.tok0 + tokens); ++t) {
+      const uint2 x = *reinterpret_cast<const uint2*>(v + (size_t)(it.row0 + t) * v_stride + (size_t)it.h * kD + lane * 4);
+      const uint32_t w[4] = {x.x << 16, x.x & 0xffff0000u, x.y << 16, x.y & 0xffff0000u};
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        if ((w[d] & 0x7f800000u) == 0x7f800000u) sum[d] += __uint_as_float(w[d]);
+      if (sum[0] == 0.f && sum[1] == 0.f && sum[2] == 0.f && sum[3] == 0.f) continue;
+      for (int g = 0; g < G; ++g) {
+        uint2* dst = reinterpret_cast<uint2*>(out + (size_t)(it.row0 + t) * out_stride + (size_t)(it.h * G + g) * kD + lane * 4);
+        const uint2 o = *dst;
+        *dst = make_uint2(pack_bf16x2(bf_lo(o.x) + sum[0], bf_hi(o.x) + sum[1]),
+                          pack_bf16x2(bf_lo(o.y) + sum[2], bf_hi(o.y) + sum[3]));
+      }
+    }
+  }
+}
+
+// The scheduler warp: hands out the block's items, and looks over the V tiles with tokens that not all rows of an item
+// attend.  False: a wait gave up.  Out of the kernel's own code (56 registers of the warp's 88): inlined, it crowded
+// the other roles, and the whole kernel took 4 to 5% longer.
+__device__ __noinline__ bool schedule(Bars* bars, uint8_t* ring, int sequences, int heads, int per, const int* row_start,
+                                      int n_rows, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort_flag;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+  };
+  bool ok = true;
+  Schedule sch;
+  sch.init(row_start, sequences, n_rows, 2 * per, lane);
+  unsigned slot = 0, raw_uses = 0;  // ring places of the items before, uses of raw_full (odd: 1)
+  // Rows behind the sequence's last token become zeros, infinities and NaN after the item's first token too.
+  auto look_over = [&](const Item& it) {
+    const int n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
+    for (int j = first_masked(it); j < n; ++j) {
+      const unsigned place = (slot + 2 * (unsigned)j + 1) % kRing;
+      if (!wait_all(&bars->raw_full[place], raw_uses >> place & 1)) return false;
+      raw_uses ^= 1u << place;
+      uint8_t* buf = ring + (size_t)place * kTileBytes;
+      const int held = min(kTile, it.len - j * kTile);                    // rows of the sequence
+      const int c0 = max(0, it.tok0 + 1 - j * kTile) * 8, c1 = held * 8;  // in pieces of 16 bytes
+      const bool clean = all_finite(smem_u32(buf), c0, c1, lane);
+      if (!clean) {
+        for (int c = c0 + lane; c < c1; c += 32)
+          for (int half = 0; half < 2; ++half) {
+            uint4* at = reinterpret_cast<uint4*>(buf + half * kHalf + c * 16);
+            const uint4 x = *at;
+            *at = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z), finite_or_zero(x.w));
+          }
+        if (lane == 0) *reinterpret_cast<volatile int*>(&bars->cleaned) = 1;
+      }
+      for (int c = c1 + lane; c < kTile * 8; c += 32) {
+        *reinterpret_cast<uint4*>(buf + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(buf + kHalf + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (!clean || held < kTile) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->kv_full[place]);
+    }
+    slot += 2 * (unsigned)n;
+    return true;
+  };
+  // An item's tiles are looked over when the next item is out, so that the producer need not wait for it.
+  for (int k = 0;; ++k) {
+    const Item it = sch.item(k, heads);
+    const int st = k % kItems;
+    if (!wait_all(&bars->item_empty[st], ((k / kItems) & 1) ^ 1)) {
+      ok = false;
+      break;
+    }
+    if (lane == 0) {
+      bars->items[st] = it;
+      mbar_arrive(&bars->item_full[st]);
+    }
+    __syncwarp();
+    if (k > 0 && !look_over(bars->items[(k - 1) % kItems])) {
+      ok = false;
+      break;
+    }
+    if (it.row0 < 0) break;
+  }
+  set_err(err, sch.bits);
+  return ok;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, PagedShape s, const int* row_start,
-                   int n_rows, float scale_log2, uint16_t* out, size_t out_stride,
+                   const __grid_constant__ CUtensorMap map_v, PagedShape s, const uint16_t* v, size_t v_stride,
+                   const int* row_start, int n_rows, float scale_log2, uint16_t* out, size_t out_stride,
                    unsigned* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -317,16 +469,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bars->kv_full[i], 1);
       mbar_init(&bars->kv_empty[i], 2);  // both tiles' MMAs
+      mbar_init(&bars->raw_full[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
       mbar_init(&bars->item_empty[i], kConsumers);
     }
-    mbar_init(&bars->tail, 1);
     mbar_init(&bars->done[0], 1);
     mbar_init(&bars->done[1], 1);
     bars->abort_flag = 0;
     bars->token = 0;
+    bars->cleaned = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -588,7 +741,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     timed_out = __any_sync(0xffffffffu, timed_out);
   } else if (warp == 9) {
     // ------------------------------------------------------------ TMA producer
-    unsigned slot = 0, q_uses[2] = {0, 0}, tails = 0;
+    unsigned slot = 0, q_uses[2] = {0, 0};
+    unsigned raw_uses = 0, raw_now = 0;  // a bit to a ring place: uses for raw_full so far (odd: 1), its latest use is one
     if (lane < 3) {
       const CUtensorMap* map = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -600,8 +754,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       for (int j = 0; j < n && !timed_out; ++j) {
         for (int part = 0; part < 2 && !timed_out; ++part, ++slot) {  // K_j, V_j
           const bool q_here = j == 0 && kv_tiles(it, part, per) > 0;   // Q_0 before K_0, Q_1 before V_0
-          const bool tail = part == 1 && (j + 1) * kTile > it.len;
-          uint8_t* buf = ring + (size_t)(slot % kRing) * kTileBytes;
+          const bool raw = part == 1 && j >= first_masked(it);         // to be looked over before it is full
+          const unsigned place = slot % kRing;
+          uint8_t* buf = ring + (size_t)place * kTileBytes;
           bool ok = true;
           if (lane == 0) {
             if (q_here) {
@@ -613,9 +768,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tma_load_3d(qb + kHalf, &map_q, 64, it.h * G, it.row0 + it.tok0 + part * per, &bars->q_full[part]);
               }
             }
-            ok = ok && mbar_wait(&bars->kv_empty[slot % kRing], ((slot / kRing) & 1) ^ 1, abort_flag);
+            ok = ok && mbar_wait(&bars->kv_empty[place], ((slot / kRing) & 1) ^ 1, abort_flag);
             if (ok) {
-              uint64_t* bar = tail ? &bars->tail : &bars->kv_full[slot % kRing];
+              uint64_t* bar = raw ? &bars->raw_full[place] : &bars->kv_full[place];
               const CUtensorMap* map = part ? &map_v : &map_k;
               mbar_expect_tx(bar, kTileBytes);
               tma_load_3d(buf, map, 0, it.h, it.row0 + j * kTile, bar);
@@ -624,55 +779,25 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
           }
           if (q_here) ++q_uses[part];
           timed_out = !__all_sync(0xffffffffu, ok);
-          if (tail && !timed_out) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->tail, tails & 1, abort_flag))) {
-              timed_out = true;
-              mbar_drain(&bars->tail, tails & 1);
-              break;
-            }
-            ++tails;
-            const int first = it.len - j * kTile;  // 1 .. 127: rows from here on belong to no key of the sequence
-            for (int c = lane; c < (kTile - first) * 8; c += 32) {
-              *reinterpret_cast<uint4*>(buf + first * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(buf + kHalf + first * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->kv_full[slot % kRing]);
+          if (!timed_out) {
+            raw_uses ^= raw ? 1u << place : 0u;
+            raw_now = raw ? raw_now | 1u << place : raw_now & ~(1u << place);
           }
         }
       }
     }
     if (timed_out && lane == 0) {  // copies that were issued have to land before the block leaves
-      for (unsigned u = slot > kRing ? slot - kRing : 0; u < slot; ++u) mbar_drain(&bars->kv_full[u % kRing], (u / kRing) & 1);
+      for (unsigned u = slot > kRing ? slot - kRing : 0; u < slot; ++u) {
+        const unsigned place = u % kRing;
+        if (raw_now >> place & 1) mbar_drain(&bars->raw_full[place], (raw_uses >> place & 1) ^ 1);
+        else mbar_drain(&bars->kv_full[place], (u / kRing) & 1);
+      }
       for (int i = 0; i < 2; ++i)
         if (q_uses[i]) mbar_drain(&bars->q_full[i], (q_uses[i] - 1) & 1);
     }
     __syncwarp();
   } else if (warp == 10) {
-    // ------------------------------------------------------------ scheduler
-    Schedule sch;
-    sch.init(row_start, s.B, n_rows, 2 * per, lane);
-    for (int k = 0;; ++k) {
-      // rounds of gridDim.x items, every second one in the other direction
-      // (32 bits: the rows of K alone limit items to a 32nd of what the GPU's memory holds)
-      const unsigned at = (unsigned)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      int a = 0, z = 0, place = 0;
-      Item it{-1, 0, 0, 0};
-      if (sch.find((int)(at / (unsigned)s.Hkv), a, z, place)) it = Item{a, z - a, place * 2 * per, (int)(at % (unsigned)s.Hkv)};
-      const int st = k % kItems;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[st], ((k / kItems) & 1) ^ 1, abort_flag))) {
-        timed_out = true;
-        break;
-      }
-      if (lane == 0) {
-        bars->items[st] = it;
-        mbar_arrive(&bars->item_full[st]);
-      }
-      __syncwarp();
-      if (it.row0 < 0) break;
-    }
-    set_err(err, sch.bits);
+    timed_out = !schedule(bars, ring, s.B, s.Hkv, per, row_start, n_rows, err);
   }
 
   if (timed_out) {
@@ -682,6 +807,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (warp < 8 && bars->cleaned)  // the block's outputs are written
+    give_back(s.B, s.Hkv, G, row_start, n_rows, v, v_stride, out, out_stride);
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
@@ -724,8 +851,8 @@ cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_
     regs = fa.numRegs;
   }
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_chained(prompt_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, 1, mq, mk, mv, s, row_start, n_rows,
-                        scale * 1.4426950408889634f, out, out_stride, err);
+  return launch_chained(prompt_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, 1, mq, mk, mv, s, v, v_stride,
+                        row_start, n_rows, scale * 1.4426950408889634f, out, out_stride, err);
 }
 
 }  // namespace oasis

@@ -47,6 +47,42 @@ def _inputs(seed, n, hkv, G):
     return (torch.randn((n, h, 128), generator=g).to(torch.bfloat16) for h in (hkv * G, hkv, hkv))
 
 
+PLACES = [[0], [1], [77], [126, 128], [127], [255], [299], [302], [40, 41, 200, 430], list(range(60, 300, 7))]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("places", PLACES, ids=str)
+@pytest.mark.parametrize("G", [1, 3, 4, 8])
+def test_a_value_reaches_no_earlier_row(G, places, value):
+    q, k, v = _inputs(G, 440, 2, G)
+    for i, p in enumerate(places):
+        v[p, i % 2, (p * 37) % 128] = value if i % 3 < 2 else -value
+    _check(q, k, v, [0, 300, 305, 435])
+
+
+@pytest.mark.parametrize("count", [320, 400])
+def test_among_many_sequences(count):
+    """Both schedules (up to 320 sequences sorted, more in their order), empty sequences among them, several
+    items to a block: what was taken out goes back to the right rows."""
+    rng = np.random.default_rng(count)
+    lens = rng.integers(0, 12, count)
+    lens[[3, count // 2]] = 150
+    start = np.concatenate([[0], np.cumsum(lens)])
+    n = int(start[-1])
+    q, k, v = _inputs(count, n + 3, 4, 4)
+    for p in rng.integers(0, n, 60):
+        v[p, int(rng.integers(0, 4)), int(rng.integers(0, 128))] = [np.inf, -np.inf, np.nan][int(rng.integers(0, 3))]
+    v[n:] = float("nan")
+    _check(q, k, v, start.tolist())
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_rows_of_values_that_are_all_nan(G):
+    q, k, v = _inputs(9, 700, 1, G)
+    v[333:] = float("nan")
+    _check(q, k, v, [0, 600, 690])
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("G", [1, 4])
 def test_a_key_reaches_no_earlier_row(G, value):

@@ -2,10 +2,10 @@
 // tcgen05.mma -> TMEM, one persistent thread block per SM.
 //
 // Mathematics: one pass over the keys with a running reference M and sum of a
-// softmax, w_j = 2^(c s_j - M), o = sum_j w_j v_j / sum_j w_j, c = scale * log2(e).  M moves
-// only when a row's scores pass it by more than 2^8 (weights stay below 256, which
-// costs no precision in fp32 or bf16), so the accumulators are rescaled a few times in a
-// whole row, not at every tile.
+// softmax, w_j = 2^(c s_j - M), o = sum_j w_j v_j / sum_j w_j, c = scale * log2(e).  M lies
+// 34 above the score that sets it and moves only when a score is more than 8 above that one, so the
+// accumulators are rescaled a few times in a whole row, not at every tile; weights of at most 2^-26
+// cost no precision in fp32 or bf16 and keep sums of large values finite.
 //
 // Rows: the G query heads of a KV head and consecutive tokens are packed into the
 // rows of a tile (row = token * G + head), so that every K/V tile is read once for
@@ -72,7 +72,10 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(12 * kLaunchRegs >= 8 * kSoftmaxRegs + 4 * kOtherRegs, "register split");
 constexpr int kConsumers = 11;               // warps that read an item: softmax, MMA, producer
 constexpr float kSlack = 8.0f;
-// The least reference: a first tile whose scores are all -inf leaves it there, below every finite score.
+// 2^26 weights of up to 2^(8 - 34) times the largest bf16 do not pass fp32's largest value.  At the other end products
+// of values under 2^-92 leave fp32's normal range.
+constexpr float kDrop = 34.0f;
+// The least score that sets M: a first tile whose scores are all -inf leaves it there, below every finite score.
 constexpr float kLowest = -3e38f;
 
 struct Item {
@@ -559,10 +562,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                : fmaxf(m[d], __uint_as_float(x[c + d]));
         const float big = scale_log2 * max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
         if (j == 0) {
-          ref = fmaxf(big, kLowest);
-        } else if (__any_sync(0xffffffffu, big > ref + kSlack)) {
+          ref = fmaxf(big, kLowest) + kDrop;
+        } else if (__any_sync(0xffffffffu, big > ref + (kSlack - kDrop))) {
           // S_j is there, so the product with V_(j-1) is complete and O is at rest until P_j is handed over
-          const float next = fmaxf(ref, big), f = ex2(ref - next);
+          const float next = fmaxf(ref, big + kDrop), f = ex2(ref - next);
           ref = next;
           float a, b;
           unpack2(sum_a, a, b);

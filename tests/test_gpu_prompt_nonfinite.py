@@ -76,6 +76,29 @@ def test_among_many_sequences(count):
     _check(q, k, v, start.tolist())
 
 
+@pytest.mark.parametrize("size", [1e19, 3e38])
+def test_large_finite_values_stay(size):
+    """Products of such values pass the largest bf16 where the kernel looks for infinities; the values are finite."""
+    q, k, v = _inputs(40, 300, 1, 4)
+    q[:] = 0  # equal weights: their sums stay finite
+    v[:] = torch.where(v > 0, size, -size).to(torch.bfloat16)
+    _check(q, k, v, [0, 200, 299])
+
+
+def test_small_values_stay():
+    """Values of 2^-100, whose products with the weights lie below fp32's normal range."""
+    from paged_helpers import BF16_HALF_STEP, check_attention, ints
+
+    from sparse_decode_attention_oasis_gb300.paged import prompt_attn
+
+    q, k, v = _inputs(41, 300, 1, 4)
+    small = (v.float() * 2.0 ** -100).to(torch.bfloat16)
+    got = prompt_attn(q.cuda(), k.cuda(), small.cuda(), ints([0, 300])).double().cpu().numpy() * 2.0 ** 100
+    want, mass, size = ref.prompt(*(t.double().numpy() for t in (q, k, v)), [0, 300], SCALE)
+    # half of fp32's smallest step, 2^-150, is 2^-16 of a weight of 2^-34 times 2^-100: inside what the sums are allowed
+    check_attention(got, want, mass, size, BF16_HALF_STEP)
+
+
 @pytest.mark.parametrize("G", [1, 4])
 def test_rows_of_values_that_are_all_nan(G):
     q, k, v = _inputs(9, 700, 1, G)

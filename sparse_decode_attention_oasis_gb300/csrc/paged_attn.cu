@@ -37,8 +37,8 @@
 // GB): 170 us, 6.3 TB/s, 0.93 of the measured copy rate; ncu: DRAM bytes equal the
 // algorithmic ones, 32% of the issue slots used.  The time is 9 to 12 us (launch, tables and
 // first pages 4, the blocks' uneven ends 3, the two joins 4) and the bytes at the copy rate,
-// so 128 pages for each of 256 pairs (134 MB) took 31 us; by clusters they take 28, and one
-// request of 700 tokens 6.8 against 8.4.  Measured and not kept: pages in a ring of three in shared memory by bulk
+// so 128 pages for each of 256 pairs (134 MB) take 30 us; by clusters they take 28, and one
+// request of 700 tokens 6.7 against 8.2.  Measured and not kept: pages in a ring of three in shared memory by bulk
 // copies (186 against 174 us: the deeper queues end more unevenly), L2 prefetch 2 to 8
 // pages ahead (177 to 197), queries loaded before the tables but converted after (205:
 // the live registers cost the loop), 4 or 16 warps to a block (no change), one join
@@ -610,10 +610,11 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   const long long pairs = (long long)s.B * s.Hkv;
   const int pair_max = sel ? sel_max : s.nb_max;
   // A cluster for each pair needs no prefix over the pairs, no workspace and no second kernel, but leaves blocks
-  // idle that other pairs could use: taken while a pair's most pages keep its blocks busy for a few us.  32/8 heads, one
-  // cluster a pair against equal ranges: 1 x 700 tokens 6.5 against 7.9 us, 1 x 4,096 9.6 against 11.0, 1 x
-  // 8,192 (64 pages for each of 64 blocks) 14.0 against 13.6, 32 x 1,000 16.8 against 19.6, 32 x 2,000
-  // (125 pages for each of 256 blocks) 27.5 against 29.8.
+  // idle that other pairs could use: taken while a pair's most pages (by the width of the table or selection; the lengths are
+  // not known here) keep its blocks busy for a few us.  32/8 heads, clusters against equal ranges: 1 x 700 tokens 6.7
+  // against 8.2 us, 1 x 4,096 9.2 against 11.3, 1 x 8,192 (64 pages for each of 64 blocks) 14.0 against 13.6, 32 x
+  // 1,000 16.7 against 19.7.  With more of the places filled the gain lasts longer: of 304, 208 pairs of 96 pages 21.3 against
+  // 22.3 and of 128 26.4 against 25.9, 256 pairs of 128 27.8 against 30.3, of 192 38.6 against 40.3, of 256 49.1 against 50.0.
   while (a.team < 8 && pairs * a.team * 2 <= most && pair_max > kMinPages * a.team) a.team *= 2;
   const int team_pages = pairs * a.team * 3 >= most * 2LL ? 128 : 56;  // two thirds of the GPU's places filled, or fewer
   if (pairs * a.team <= most && pair_max <= team_pages * a.team) {

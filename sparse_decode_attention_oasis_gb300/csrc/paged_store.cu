@@ -12,7 +12,7 @@
 // bytes in 16-byte loads, two rows to an instruction, held in registers from the
 // maximum to the conversion, so that every row is read once.  Bound: HBM.  15,170 tokens of
 // 8 heads (93 MB): 17.1 us, 5.5 TB/s, 0.81 of the measured copy rate, of which 2 us are launch
-// and first loads; 32 tokens of a decode step: 2.4 us.
+// and first loads; 32 tokens of a decode step: 2.3 us, 4.7 to 6.0 where every page's scale grows.
 #include "paged.cuh"
 
 namespace oasis {

@@ -42,8 +42,8 @@
 // pair takes 2,300 to 2,600, the chain S -> softmax (1,250 cycles) -> product of one tile being longer than
 // twice the other's MMAs; and the power cap: in long calls the SM clock settles at 1.7 to 1.85 GHz.  One
 // prompt of 16,384 tokens, 32/8 heads: 1.20 ms (1.83 PFLOP/s, 0.94 of the measured matrix product),
-// 1.34 ms in calls that follow each other for seconds; ncu at 8,192 tokens: tensor pipe 77% of
-// elapsed cycles, issue slots 45%.  Twelve packed prompts (11,430 tokens): 163 us; an item pays
+// 1.34 ms in calls that follow each other for seconds; ncu at 8,192 tokens: tensor pipe 78% of
+// elapsed cycles, issue slots 45%.  Twelve packed prompts (11,430 tokens): 162 us in a graph, 177 as calls; an item pays
 // some 4,000 cycles at its ends beside its tiles.  Measured and not kept: two softmax warps to 32 rows
 // (2,300 against 1,500 us then: the issuing lane starves), output by warps of its own (1,250 against
 // 1,200: fewer registers for the softmax), 200 or 216 registers for the softmax (3% more), scores

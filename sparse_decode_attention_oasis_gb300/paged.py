@@ -270,10 +270,12 @@ class PagedKV:
         return out
 
     def check(self) -> None:
-        """Waits for the device and raises if a kernel reported an error; clears the word."""
+        """Waits for the device (every stream) and raises if a kernel reported an error; clears the word."""
+        torch.cuda.synchronize(self.device)
         bits = int(self.err.item())
         if bits:
             self.err.zero_()
+            torch.cuda.synchronize(self.device)  # a call that follows on another stream finds it clear
             names = [n for n in ("BAD_BLOCK", "BAD_SLOT", "NO_SLOT", "BAD_COUNT", "TIMEOUT")
                      if bits & getattr(B, "EW_" + n)]
             raise B.OasisError("paged cache", 1, "device error word: " + ", ".join(names))

@@ -772,9 +772,10 @@ OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const v
  *   infinity, or whose scores are all -inf, gives NaN in its own output row alone.
  *   Scores, weights and sums are fp32.  For the product with the values a weight
  *   is rounded to fp16: by 2^-11 of itself at most, and where weight times value
- *   scale is below 2^-25 of its largest, by 2^-36 of that.  Value scales of one
- *   request may lie up to 2^100 apart; beyond that, tokens of the small ones
- *   can drop out of the softmax's sum.
+ *   scale is below 2^-25 of its largest, by 2^-36 of that (an infinity that was
+ *   stored, as 448 * 2^119, leaves the head's other values as zero).  Value scales
+ *   of one request may lie up to 2^100 apart; beyond that, tokens of the small
+ *   ones can drop out of the softmax's sum.
  * Arguments:
  *   q         device bf16, B rows of [Hq][d], stride q_stride
  *   kv_pages, kv_scale, block_table   as above (read only)

@@ -651,16 +651,18 @@ OASIS_API size_t oasis_trace_bytes(int32_t capacity);
 OASIS_API oasis_status oasis_trace_set(void* dev_buf, int32_t capacity);
 
 /*
- * Paged KV cache in 8 bits (the pages have no counterpart: the dense part of a
- * model that serves beside the sparse path - the prompt's own attention, layers
- * that stay dense, and a whole context kept in HBM).  Four operators share it:
+ * Paged KV cache in 8 or in 4 bits (the pages have no counterpart: the dense part
+ * of a model that serves beside the sparse path - the prompt's own attention, layers
+ * that stay dense, and a whole context kept in HBM).  These operators share it:
  *
- *   oasis_extend_tables         pages for new tokens, and every new token's slot
- *   oasis_store_kv_q8           new K/V rows, quantised into their pages
- *   oasis_paged_decode_attn_q8  attention of one query token per request
- *   oasis_prompt_attn           causal attention over packed prompts (bf16 K/V)
+ *   oasis_extend_tables             pages for new tokens, and every new token's slot
+ *   oasis_store_kv_q8, _q4          new K/V rows, quantised into their pages
+ *   oasis_paged_decode_attn_q8, _q4 attention of one query token per request
+ *   oasis_read_kv_q8, _q4           held tokens as packed bf16 rows, new rows behind
+ *   oasis_prompt_attn               causal attention over packed prompts (bf16 K/V)
+ *   oasis_resume_attn               the same where keys lie before the new rows
  *
- * A page holds bs = 16 tokens of one layer, all KV heads:
+ * A page holds bs = 16 tokens of one layer, all KV heads.  In 8 bits:
  *   kv_pages  device e4m3 [n_pages][Hkv][2][bs][d]   [..][0] keys, [..][1] values
  *   kv_scale  device float [n_pages][Hkv][2]         value = e4m3 * scale
  * A scale is a power of two, 2^e with e in [-60, 119]: the format's relative
@@ -668,6 +670,17 @@ OASIS_API oasis_status oasis_trace_set(void* dev_buf, int32_t capacity);
  * but for values that become subnormal.  e is the least one with
  * amax <= 448 * 2^e, amax over the page's tokens of that head's keys (values);
  * magnitudes above 448 * 2^119 = 1.75 * 2^127 are stored as that.
+ * In 4 bits every token of a head has its own scales, one for 16 dimensions:
+ *   kv_pages  device e2m1 [n_pages][Hkv][2][bs][d/2 bytes]  dimension 2j in the low
+ *             and 2j+1 in the high half of byte j; codes 0 .. 7 are 0, 0.5, 1, 1.5,
+ *             2, 3, 4, 6, code + 8 the negative
+ *   kv_scale  device byte [n_pages][Hkv][2][128]  keys as [bs][d/16], values as
+ *             [d/16][bs] (the order in which decode reads them); value = code * scale
+ * A scale byte is an unsigned float, 5 exponent and 3 fraction bits: byte b is the
+ * half with bits b << 7.  It is the least one with amax <= 6 * scale over the 16
+ * dimensions, from 2^-17 (0 where all are zero) to 10240 (b = 226): magnitudes above
+ * 61440 are stored as that.  b = 255 marks a group that held a NaN: its 16 values
+ * are NaN.  Other bytes above 226 are not used.
  *   block_table  device int32 [B][nb_max]   page of request b's block x (tokens
  *                16x .. 16x+15), the same for every layer and head; entries of
  *                blocks past the request's length are never read
@@ -831,6 +844,109 @@ OASIS_API oasis_status oasis_prompt_attn(const oasis_paged_shape* shape, const v
                                          size_t v_stride, const int32_t* row_start, int32_t n_rows,
                                          float scale, void* out, size_t out_stride,
                                          uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Quantises K/V rows into 4-bit pages.  With s the scale of 16 dimensions of a row
+ * (above), each is stored as the e2m1 value nearest to x / s, ties to the even
+ * code; what rounds to zero is code 0.  Rows are independent: any order, and what
+ * a page holds beside the slots that are named stays as it is.
+ *   k, v       device bf16, n_rows rows of [Hkv][d], strides k_stride, v_stride
+ *   slot_map   device int32 [n_rows]; -1 = the row is skipped; another slot
+ *              outside [0, n_pages*bs) is skipped with OASIS_EW_BAD_SLOT.  No slot
+ *              may be named twice in one call.
+ *   kv_pages, kv_scale   one layer's, in/out, 16-byte aligned
+ *   err_word   device uint32 [1] or NULL
+ * n_rows may be 0.  An infinity is stored as 61440 of its sign, a NaN makes its
+ * group's 16 values NaN.
+ */
+OASIS_API oasis_status oasis_store_kv_q4(const oasis_paged_shape* shape, const void* k, size_t k_stride,
+                                         const void* v, size_t v_stride, const int32_t* slot_map,
+                                         int32_t n_rows, void* kv_pages, void* kv_scale,
+                                         uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Decode attention over the 4-bit pages: oasis_paged_decode_attn_q8 in every
+ * respect (definition, roundings, arguments, workspace) but for the pages' format.
+ * Scores and products are formed from the stored values, which fp16 holds exactly.
+ * A key group that holds NaN gives NaN in the rows that attend its token, a value
+ * group of NaN gives NaN in its 16 dimensions.
+ */
+OASIS_API oasis_status oasis_paged_decode_attn_q4(const oasis_paged_shape* shape, const void* q,
+                                                  size_t q_stride, const void* kv_pages,
+                                                  const void* kv_scale, const int32_t* block_table,
+                                                  const int32_t* ctx_len, const int32_t* sel,
+                                                  const int32_t* nsel, int32_t sel_max, float scale,
+                                                  void* workspace, size_t ws_bytes, void* out,
+                                                  uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Reads a cache back: the first ctx_len[b] tokens of every request as packed bf16
+ * rows, and behind them the request's new rows, which are copied - the keys and
+ * values that oasis_resume_attn takes.  With total_b = ctx_len[b] + new rows of b:
+ *   kv_start[b] = sum of total_i over i < b; rows kv_start[b] .. kv_start[b+1] - 1
+ *   of k_out and v_out are request b's tokens in order.
+ * Stored values are bf16 values exactly; nothing is rounded.  Requests from the
+ * first one whose rows pass n_rows get none (kv_start stays where it is, their rows
+ * are not written, OASIS_EW_BAD_COUNT).  Rows past kv_start[B] are not written.
+ *   kv_pages, kv_scale, block_table   as above (read only)
+ *   ctx_len    device int32 [B]; clamped to [0, nb_max*bs]; rows of a page outside
+ *              the pool are zero (OASIS_EW_BAD_SLOT)
+ *   k_new, v_new   device bf16, n_new rows of [Hkv][d] with strides; request b's are
+ *              rows new_start[b] .. new_start[b+1] - 1 (the row_start of
+ *              oasis_extend_tables).  A request whose bounds decrease or leave
+ *              [0, n_new] has no new rows, with OASIS_EW_BAD_COUNT.
+ *   new_start  device int32 [B+1], or NULL: no new rows
+ *   kv_start   device int32 [B+1]    out
+ *   k_out, v_out   device bf16 [n_rows][Hkv][d], 32-byte aligned; must not overlap
+ *              k_new or v_new
+ *   n_rows     0 .. 2^28
+ *   err_word   device uint32 [1] or NULL
+ */
+OASIS_API oasis_status oasis_read_kv_q8(const oasis_paged_shape* shape, const void* kv_pages,
+                                        const float* kv_scale, const int32_t* block_table,
+                                        const int32_t* ctx_len, const void* k_new, size_t k_stride,
+                                        const void* v_new, size_t v_stride, const int32_t* new_start,
+                                        int32_t n_new, int32_t* kv_start, void* k_out, void* v_out,
+                                        int32_t n_rows, uint32_t* err_word, oasis_stream_t stream);
+OASIS_API oasis_status oasis_read_kv_q4(const oasis_paged_shape* shape, const void* kv_pages,
+                                        const void* kv_scale, const int32_t* block_table,
+                                        const int32_t* ctx_len, const void* k_new, size_t k_stride,
+                                        const void* v_new, size_t v_stride, const int32_t* new_start,
+                                        int32_t n_new, int32_t* kv_start, void* k_out, void* v_out,
+                                        int32_t n_rows, uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * Causal attention of new rows that continue a context.  Sequence b owns query rows
+ * q_start[b] .. q_start[b+1] - 1, n_b of them, and rows kv_start[b] ..
+ * kv_start[b+1] - 1 of k and v, m_b >= n_b of them, the last n_b of which belong to
+ * its query rows.  For query row i of it and query head hq = h*G + g:
+ *   out[i][hq] = sum over rows j <= m_b - n_b + i of softmax_j(scale * q_i.k_j) v_j.
+ * With n_b = m_b for every b this is oasis_prompt_attn, whose roundings, treatment of
+ * infinities and NaN and conditions on rows hold here too.
+ *   q, out     device bf16, n_rows rows of [Hq][d] with strides; out must not overlap
+ *              q, k or v
+ *   k, v       device bf16, n_kv_rows rows of [Hkv][d] with strides
+ *   q_start, kv_start   device int32 [B+1], not decreasing, inside [0, n_rows] and
+ *              [0, n_kv_rows]; a sequence that breaks this, or with fewer rows of
+ *              keys than of queries, is skipped with OASIS_EW_BAD_COUNT
+ *   n_rows, n_kv_rows   0 .. 2^26, n_kv_rows >= 1 where n_rows is
+ *   scale      softmax scale, > 0 and finite
+ *   workspace  device scratch, 32-byte aligned, ws_bytes >=
+ *              oasis_resume_attn_workspace_bytes(shape); contents on entry are
+ *              ignored; calls that may overlap need different ones (calls
+ *              on one stream do not, from whichever host threads they come)
+ *   err_word   device uint32 [1] or NULL; OASIS_EW_TIMEOUT as for oasis_prompt_attn
+ * Only B, Hq, Hkv and d of the shape are used; the others are checked as for
+ * every call.
+ */
+OASIS_API size_t oasis_resume_attn_workspace_bytes(const oasis_paged_shape* shape);
+
+OASIS_API oasis_status oasis_resume_attn(const oasis_paged_shape* shape, const void* q, size_t q_stride,
+                                         const void* k, size_t k_stride, const void* v,
+                                         size_t v_stride, const int32_t* q_start, int32_t n_rows,
+                                         const int32_t* kv_start, int32_t n_kv_rows, float scale,
+                                         void* workspace, size_t ws_bytes, void* out,
+                                         size_t out_stride, uint32_t* err_word, oasis_stream_t stream);
 
 #ifdef __cplusplus
 }

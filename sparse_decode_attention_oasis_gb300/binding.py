@@ -47,7 +47,7 @@ class Shape(ctypes.Structure):
 
 
 class PagedShape(ctypes.Structure):
-    """Sizes of a paged 8-bit cache (oasis_paged_shape)."""
+    """Sizes of a paged cache (oasis_paged_shape)."""
 
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "d", "bs", "nb_max", "n_pages")]
 
@@ -113,6 +113,15 @@ _SIGS = {
                                     ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP, _VP], ctypes.c_int),
     "oasis_prompt_attn": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP,
                            ctypes.c_int32, ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP], ctypes.c_int),
+    "oasis_store_kv_q4": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP, _VP, _VP, _VP],
+                          ctypes.c_int),
+    "oasis_paged_decode_attn_q4": ([_PS, _VP, ctypes.c_size_t, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32,
+                                    ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP, _VP], ctypes.c_int),
+    **{f"oasis_read_kv_{bits}": ([_PS, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP,
+                                  _VP, _VP, ctypes.c_int32, _VP, _VP], ctypes.c_int) for bits in ("q8", "q4")},
+    "oasis_resume_attn_workspace_bytes": ([_PS], ctypes.c_size_t),
+    "oasis_resume_attn": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP,
+                           ctypes.c_int32, ctypes.c_float, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, _VP], ctypes.c_int),
 }
 
 _lib = None
@@ -424,3 +433,55 @@ def oasis_prompt_attn(shape: PagedShape, q, q_stride: int, k, k_stride: int, v, 
     _check("oasis_prompt_attn", load().oasis_prompt_attn(
         ctypes.byref(shape), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(row_start), n_rows, scale,
         _ptr(out), out_stride, _ptr(err_word), _stream(stream)))
+
+
+def oasis_store_kv_q4(shape: PagedShape, k, k_stride: int, v, v_stride: int, slot_map, n_rows: int, kv_pages,
+                      kv_scale, err_word=None, stream=None):
+    """bf16 K/V rows into 4-bit pages with a scale byte for every 16 dimensions of a token."""
+    _check("oasis_store_kv_q4", load().oasis_store_kv_q4(
+        ctypes.byref(shape), _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slot_map), n_rows, _ptr(kv_pages),
+        _ptr(kv_scale), _ptr(err_word), _stream(stream)))
+
+
+def oasis_paged_decode_attn_q4(shape: PagedShape, q, q_stride: int, kv_pages, kv_scale, block_table, ctx_len, sel,
+                               nsel, sel_max: int, scale: float, workspace, ws_bytes: int, out, err_word=None,
+                               stream=None):
+    """Attention of one query token per request over its 4-bit pages (sel/nsel None: all of them)."""
+    _check("oasis_paged_decode_attn_q4", load().oasis_paged_decode_attn_q4(
+        ctypes.byref(shape), _ptr(q), q_stride, _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len),
+        _ptr(sel), _ptr(nsel), sel_max, scale, _ptr(workspace), ws_bytes, _ptr(out), _ptr(err_word),
+        _stream(stream)))
+
+
+def oasis_read_kv_q8(shape: PagedShape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride: int, v_new,
+                     v_stride: int, new_start, n_new: int, kv_start, k_out, v_out, n_rows: int, err_word=None,
+                     stream=None):
+    """Held tokens of 8-bit pages as packed bf16 rows, each request's new rows behind them."""
+    _check("oasis_read_kv_q8", load().oasis_read_kv_q8(
+        ctypes.byref(shape), _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len), _ptr(k_new), k_stride,
+        _ptr(v_new), v_stride, _ptr(new_start), n_new, _ptr(kv_start), _ptr(k_out), _ptr(v_out), n_rows,
+        _ptr(err_word), _stream(stream)))
+
+
+def oasis_read_kv_q4(shape: PagedShape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride: int, v_new,
+                     v_stride: int, new_start, n_new: int, kv_start, k_out, v_out, n_rows: int, err_word=None,
+                     stream=None):
+    """Held tokens of 4-bit pages as packed bf16 rows, each request's new rows behind them."""
+    _check("oasis_read_kv_q4", load().oasis_read_kv_q4(
+        ctypes.byref(shape), _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len), _ptr(k_new), k_stride,
+        _ptr(v_new), v_stride, _ptr(new_start), n_new, _ptr(kv_start), _ptr(k_out), _ptr(v_out), n_rows,
+        _ptr(err_word), _stream(stream)))
+
+
+def oasis_resume_attn_workspace_bytes(shape: PagedShape) -> int:
+    return int(load().oasis_resume_attn_workspace_bytes(ctypes.byref(shape)))
+
+
+def oasis_resume_attn(shape: PagedShape, q, q_stride: int, k, k_stride: int, v, v_stride: int, q_start, n_rows: int,
+                      kv_start, n_kv_rows: int, scale: float, workspace, ws_bytes: int, out, out_stride: int,
+                      err_word=None, stream=None):
+    """Causal attention of packed new rows over their sequences' keys and values (bf16 in and out)."""
+    _check("oasis_resume_attn", load().oasis_resume_attn(
+        ctypes.byref(shape), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q_start), n_rows,
+        _ptr(kv_start), n_kv_rows, scale, _ptr(workspace), ws_bytes, _ptr(out), out_stride, _ptr(err_word),
+        _stream(stream)))

@@ -1,4 +1,4 @@
-// Types and device helpers shared by the paged 8-bit cache's kernels.
+// Types and device helpers shared by the kernels of the paged cache, in 8 and in 4 bits.
 #pragma once
 
 #include "common.cuh"
@@ -15,6 +15,15 @@ struct PagedShape {
 // saturate there, by an eighth at most.  Low: below -60 a page's values are as good as zero.
 constexpr int kScaleELow = -60, kScaleEHigh = 119;
 constexpr long long kHeadPageBytes = 2LL * kBS * kD;  // keys and values of one head in one page
+
+// Pages in 4 bits: groups of 16 dimensions of a token share a scale byte.
+constexpr int kGroup = 16, kGroups = kD / kGroup;
+constexpr long long kHeadPageBytes4 = kHeadPageBytes / 2;        // codes of one head in one page
+constexpr long long kHeadScaleBytes4 = 2LL * kBS * kGroups;      // its scales: keys [token][group], values [group][token]
+// A scale byte is an unsigned float with 5 exponent and 3 fraction bits: the half with bits b << 7.  The largest in use,
+// 10,240 = 1.25 * 2^13, keeps 6 * scale = 61,440 below fp16's largest value, so that every stored value (2 + 4 significant
+// bits, a multiple of 2^-18) is a half, and a bf16, exactly.  0xff (a NaN as a half) marks a group that held a NaN.
+constexpr int kScaleByteHigh = 226, kScaleByteNaN = 255;
 
 // 16-byte loads (coherent: see launch_chained); the second leaves no line in L1.
 __device__ __forceinline__ uint4 load16(const void* p) {
@@ -42,6 +51,39 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t w) {
   uint32_t r;
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ uint2 load8_stream(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t load2_stream(const void* p) {
+  uint16_t r;
+  asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p) : "memory");
+  return r;
+}
+
+// Byte kByte of w, two e2m1 codes (the lower in its lower bits) -> two halves, exact.
+template <int kByte>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  if constexpr (kByte == 0) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(r) : "r"(w));
+  if constexpr (kByte == 1) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}" : "=r"(r) : "r"(w));
+  if constexpr (kByte == 2) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, c;\n}" : "=r"(r) : "r"(w));
+  if constexpr (kByte == 3) asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, d;\n}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Scale bytes 0 and 1 of w as the two halves of a word; scale byte kByte of w in both.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w) { return __byte_perm(w, 0, 0x4140) << 7; }
+template <int kByte>
+__device__ __forceinline__ uint32_t scale_twice(uint32_t w) { return __byte_perm(w, 0, 0x4040 + 0x0101 * kByte) << 7; }
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 

@@ -1,4 +1,4 @@
-// C ABI entry points of the paged 8-bit cache: argument validation, then the launches.
+// C ABI entry points of the paged cache: argument validation, then the launches.
 // No exception leaves an entry point: a message that cannot be built is a failed call.
 #include <cmath>
 #include <string>
@@ -17,6 +17,16 @@ size_t paged_attn_workspace_bytes(const PagedShape&);
 cudaError_t launch_paged_decode_attn(const PagedShape&, const uint16_t*, size_t, const uint8_t*, const float*,
                                      const int*, const int*, const int*, const int*, int, float, void*, uint16_t*,
                                      unsigned*, cudaStream_t);
+cudaError_t launch_store_kv_q4(const PagedShape&, const uint16_t*, size_t, const uint16_t*, size_t, const int*, int,
+                               uint8_t*, uint8_t*, unsigned*, cudaStream_t);
+cudaError_t launch_paged_decode_attn_q4(const PagedShape&, const uint16_t*, size_t, const uint8_t*, const uint8_t*,
+                                        const int*, const int*, const int*, const int*, int, float, void*, uint16_t*,
+                                        unsigned*, cudaStream_t);
+cudaError_t launch_read_kv(int, const PagedShape&, const uint8_t*, const void*, const int*, const int*, const uint16_t*, size_t,
+                           const uint16_t*, size_t, const int*, int, int*, uint16_t*, uint16_t*, int, unsigned*, cudaStream_t);
+size_t resume_workspace_bytes();
+cudaError_t launch_resume_attn(const PagedShape&, const uint16_t*, size_t, const uint16_t*, size_t, const uint16_t*, size_t,
+                               const int*, int, const int*, int, float, void*, uint16_t*, size_t, unsigned*, cudaStream_t);
 cudaError_t launch_prompt_attn(const PagedShape&, const uint16_t*, size_t, const uint16_t*, size_t, const uint16_t*,
                                size_t, const int*, int, float, uint16_t*, size_t, unsigned*, cudaStream_t);
 }  // namespace oasis
@@ -77,6 +87,52 @@ bool rows_ok(const void* p, size_t stride, int width) {
 }
 
 bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
+
+// The arguments of both decode calls; scale_align: bytes that kv_scale is aligned to.
+void check_decode(Call* c, const PagedShape& s, const void* q, size_t q_stride, const void* kv_pages, const void* kv_scale,
+                  size_t scale_align, const int32_t* block_table, const int32_t* ctx_len, const int32_t* sel,
+                  const int32_t* nsel, int32_t sel_max, float scale, const void* workspace, size_t ws_bytes, const void* out,
+                  const uint32_t* err_word) {
+  c->refuse(!rows_ok(q, q_stride, s.Hq * oasis::kD),
+            "q must be 16-byte aligned with a stride that is a multiple of 8 and at least Hq * d");
+  c->refuse(!kv_pages || !aligned(kv_pages, 16) || !kv_scale || !aligned(kv_scale, scale_align),
+            scale_align == 8 ? "kv_pages must be 16-byte and kv_scale 8-byte aligned device pointers"
+                             : "kv_pages and kv_scale must be 16-byte aligned device pointers");
+  c->refuse(!ints(block_table) || !ints(ctx_len), "block_table and ctx_len must be 4-byte aligned and non-NULL");
+  c->refuse((sel == nullptr) != (nsel == nullptr), "sel and nsel must be given together");
+  c->refuse(!aligned(sel, 4) || !aligned(nsel, 4) || !aligned(err_word, 4), "int32 arrays must be 4-byte aligned");
+  c->refuse(sel && (sel_max < 1 || sel_max > 65536), "sel_max must be in [1, 65536]");
+  c->refuse(!scale_ok(scale), "scale must be a positive finite number");
+  c->refuse(!out || !aligned(out, 16), "out must be a 16-byte aligned device pointer");
+  c->refuse(!workspace || !aligned(workspace, 16), "workspace must be a 16-byte aligned device pointer");
+  c->refuse(c->status == OASIS_OK && ws_bytes < oasis::paged_attn_workspace_bytes(s),
+            "workspace too small (see oasis_paged_attn_workspace_bytes)");
+}
+
+oasis_status read_kv(const char* fn, int bits, const oasis_paged_shape* shape, const void* kv_pages, const void* kv_scale,
+                     const int32_t* block_table, const int32_t* ctx_len, const void* k_new, size_t k_stride,
+                     const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new, int32_t* kv_start,
+                     void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word, oasis_stream_t stream) {
+  Call c;
+  const PagedShape s = check_shape(shape, &c);
+  c.refuse(n_rows < 0 || n_rows > (1 << 28) || n_new < 0 || n_new > (1 << 28), "n_rows and n_new must be in [0, 2^28]");
+  c.refuse(!kv_pages || !aligned(kv_pages, 16) || !kv_scale || !aligned(kv_scale, bits == 8 ? 8 : 16),
+           "kv_pages and kv_scale must be 16-byte (in 8 bits kv_scale 8-byte) aligned device pointers");
+  c.refuse(!ints(block_table) || !ints(ctx_len) || !ints(kv_start),
+           "block_table, ctx_len and kv_start must be 4-byte aligned and non-NULL");
+  c.refuse(!aligned(new_start, 4) || !aligned(err_word, 4), "int32 arrays must be 4-byte aligned");
+  if (new_start && n_new > 0)
+    c.refuse(!rows_ok(k_new, k_stride, s.Hkv * oasis::kD) || !rows_ok(v_new, v_stride, s.Hkv * oasis::kD),
+             "k_new and v_new must be 16-byte aligned with strides that are multiples of 8 and at least Hkv * d");
+  c.refuse(n_rows > 0 && (!k_out || !v_out || !aligned(k_out, 32) || !aligned(v_out, 32)),
+           "k_out and v_out must be 32-byte aligned device pointers");
+  cudaError_t e = cudaSuccess;
+  if (c.status == OASIS_OK)
+    e = oasis::launch_read_kv(bits, s, (const uint8_t*)kv_pages, kv_scale, block_table, ctx_len, (const uint16_t*)k_new, k_stride,
+                              (const uint16_t*)v_new, v_stride, new_start, n_new, kv_start, (uint16_t*)k_out,
+                              (uint16_t*)v_out, n_rows, err_word, (cudaStream_t)stream);
+  return finish(fn, c, e);
+}
 
 }  // namespace
 
@@ -148,6 +204,28 @@ oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const void* k, si
   return finish(fn, c, e);
 }
 
+oasis_status oasis_store_kv_q4(const oasis_paged_shape* shape, const void* k, size_t k_stride, const void* v,
+                               size_t v_stride, const int32_t* slot_map, int32_t n_rows, void* kv_pages,
+                               void* kv_scale, uint32_t* err_word, oasis_stream_t stream) {
+  static const char* fn = "oasis_store_kv_q4";
+  Call c;
+  const PagedShape s = check_shape(shape, &c);
+  c.refuse(n_rows < 0 || n_rows > (1 << 28), "n_rows must be in [0, 2^28]");
+  if (n_rows > 0) {
+    c.refuse(!rows_ok(k, k_stride, s.Hkv * oasis::kD) || !rows_ok(v, v_stride, s.Hkv * oasis::kD),
+             "k and v must be 16-byte aligned with strides that are multiples of 8 and at least Hkv * d");
+    c.refuse(!ints(slot_map), "slot_map must be 4-byte aligned and non-NULL");
+  }
+  c.refuse(!kv_pages || !aligned(kv_pages, 16) || !kv_scale || !aligned(kv_scale, 16),
+           "kv_pages and kv_scale must be 16-byte aligned device pointers");
+  c.refuse(!aligned(err_word, 4), "err_word must be 4-byte aligned");
+  cudaError_t e = cudaSuccess;
+  if (c.status == OASIS_OK)
+    e = oasis::launch_store_kv_q4(s, (const uint16_t*)k, k_stride, (const uint16_t*)v, v_stride, slot_map, n_rows,
+                                  (uint8_t*)kv_pages, (uint8_t*)kv_scale, err_word, (cudaStream_t)stream);
+  return finish(fn, c, e);
+}
+
 size_t oasis_paged_attn_workspace_bytes(const oasis_paged_shape* shape) {
   Call c;
   const PagedShape s = check_shape(shape, &c);
@@ -163,25 +241,50 @@ oasis_status oasis_paged_decode_attn_q8(const oasis_paged_shape* shape, const vo
   static const char* fn = "oasis_paged_decode_attn_q8";
   Call c;
   const PagedShape s = check_shape(shape, &c);
-  c.refuse(!rows_ok(q, q_stride, s.Hq * oasis::kD),
-           "q must be 16-byte aligned with a stride that is a multiple of 8 and at least Hq * d");
-  c.refuse(!kv_pages || !aligned(kv_pages, 16) || !kv_scale || !aligned(kv_scale, 8),
-           "kv_pages must be 16-byte and kv_scale 8-byte aligned device pointers");
-  c.refuse(!ints(block_table) || !ints(ctx_len), "block_table and ctx_len must be 4-byte aligned and non-NULL");
-  c.refuse((sel == nullptr) != (nsel == nullptr), "sel and nsel must be given together");
-  c.refuse(!aligned(sel, 4) || !aligned(nsel, 4) || !aligned(err_word, 4), "int32 arrays must be 4-byte aligned");
-  c.refuse(sel && (sel_max < 1 || sel_max > 65536), "sel_max must be in [1, 65536]");
-  c.refuse(!scale_ok(scale), "scale must be a positive finite number");
-  c.refuse(!out || !aligned(out, 16), "out must be a 16-byte aligned device pointer");
-  c.refuse(!workspace || !aligned(workspace, 16), "workspace must be a 16-byte aligned device pointer");
-  c.refuse(c.status == OASIS_OK && ws_bytes < oasis::paged_attn_workspace_bytes(s),
-           "workspace too small (see oasis_paged_attn_workspace_bytes)");
+  check_decode(&c, s, q, q_stride, kv_pages, kv_scale, 8, block_table, ctx_len, sel, nsel, sel_max, scale, workspace, ws_bytes,
+               out, err_word);
   cudaError_t e = cudaSuccess;
   if (c.status == OASIS_OK)
     e = oasis::launch_paged_decode_attn(s, (const uint16_t*)q, q_stride, (const uint8_t*)kv_pages, kv_scale,
                                         block_table, ctx_len, sel, nsel, sel_max, scale, workspace, (uint16_t*)out,
                                         err_word, (cudaStream_t)stream);
   return finish(fn, c, e);
+}
+
+oasis_status oasis_paged_decode_attn_q4(const oasis_paged_shape* shape, const void* q, size_t q_stride,
+                                        const void* kv_pages, const void* kv_scale, const int32_t* block_table,
+                                        const int32_t* ctx_len, const int32_t* sel, const int32_t* nsel,
+                                        int32_t sel_max, float scale, void* workspace, size_t ws_bytes, void* out,
+                                        uint32_t* err_word, oasis_stream_t stream) {
+  static const char* fn = "oasis_paged_decode_attn_q4";
+  Call c;
+  const PagedShape s = check_shape(shape, &c);
+  check_decode(&c, s, q, q_stride, kv_pages, kv_scale, 16, block_table, ctx_len, sel, nsel, sel_max, scale, workspace, ws_bytes,
+               out, err_word);
+  cudaError_t e = cudaSuccess;
+  if (c.status == OASIS_OK)
+    e = oasis::launch_paged_decode_attn_q4(s, (const uint16_t*)q, q_stride, (const uint8_t*)kv_pages, (const uint8_t*)kv_scale,
+                                           block_table, ctx_len, sel, nsel, sel_max, scale, workspace, (uint16_t*)out,
+                                           err_word, (cudaStream_t)stream);
+  return finish(fn, c, e);
+}
+
+oasis_status oasis_read_kv_q8(const oasis_paged_shape* shape, const void* kv_pages, const float* kv_scale,
+                              const int32_t* block_table, const int32_t* ctx_len, const void* k_new, size_t k_stride,
+                              const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new,
+                              int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word,
+                              oasis_stream_t stream) {
+  return read_kv("oasis_read_kv_q8", 8, shape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride, v_new, v_stride,
+                 new_start, n_new, kv_start, k_out, v_out, n_rows, err_word, stream);
+}
+
+oasis_status oasis_read_kv_q4(const oasis_paged_shape* shape, const void* kv_pages, const void* kv_scale,
+                              const int32_t* block_table, const int32_t* ctx_len, const void* k_new, size_t k_stride,
+                              const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new,
+                              int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word,
+                              oasis_stream_t stream) {
+  return read_kv("oasis_read_kv_q4", 4, shape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride, v_new, v_stride,
+                 new_start, n_new, kv_start, k_out, v_out, n_rows, err_word, stream);
 }
 
 oasis_status oasis_prompt_attn(const oasis_paged_shape* shape, const void* q, size_t q_stride, const void* k,
@@ -206,6 +309,42 @@ oasis_status oasis_prompt_attn(const oasis_paged_shape* shape, const void* q, si
     e = oasis::launch_prompt_attn(s, (const uint16_t*)q, q_stride, (const uint16_t*)k, k_stride, (const uint16_t*)v,
                                   v_stride, row_start, n_rows, scale, (uint16_t*)out, out_stride, err_word,
                                   (cudaStream_t)stream);
+  return finish(fn, c, e);
+}
+
+size_t oasis_resume_attn_workspace_bytes(const oasis_paged_shape* shape) {
+  Call c;
+  check_shape(shape, &c);
+  return finish("oasis_resume_attn_workspace_bytes", c, cudaSuccess) == OASIS_OK ? oasis::resume_workspace_bytes() : 0;
+}
+
+oasis_status oasis_resume_attn(const oasis_paged_shape* shape, const void* q, size_t q_stride, const void* k,
+                               size_t k_stride, const void* v, size_t v_stride, const int32_t* q_start, int32_t n_rows,
+                               const int32_t* kv_start, int32_t n_kv_rows, float scale, void* workspace, size_t ws_bytes,
+                               void* out, size_t out_stride, uint32_t* err_word, oasis_stream_t stream) {
+  static const char* fn = "oasis_resume_attn";
+  Call c;
+  const PagedShape s = check_shape(shape, &c);
+  c.refuse(n_rows < 0 || n_rows > (1 << 26) || n_kv_rows < 0 || n_kv_rows > (1 << 26),
+           "n_rows and n_kv_rows must be in [0, 2^26]");
+  c.refuse(n_rows > 0 && n_kv_rows == 0, "query rows need rows of keys and values");
+  c.refuse(!ints(q_start) || !ints(kv_start), "q_start and kv_start must be 4-byte aligned and non-NULL");
+  if (n_rows > 0) {
+    c.refuse(!rows_ok(q, q_stride, s.Hq * oasis::kD) || !rows_ok(out, out_stride, s.Hq * oasis::kD),
+             "q and out must be 16-byte aligned with strides that are multiples of 8 and at least Hq * d");
+    c.refuse(!rows_ok(k, k_stride, s.Hkv * oasis::kD) || !rows_ok(v, v_stride, s.Hkv * oasis::kD),
+             "k and v must be 16-byte aligned with strides that are multiples of 8 and at least Hkv * d");
+    c.refuse(!workspace || !aligned(workspace, 32), "workspace must be a 32-byte aligned device pointer");
+    c.refuse(c.status == OASIS_OK && ws_bytes < oasis::resume_workspace_bytes(),
+             "workspace too small (see oasis_resume_attn_workspace_bytes)");
+  }
+  c.refuse(!scale_ok(scale), "scale must be a positive finite number");
+  c.refuse(!aligned(err_word, 4), "err_word must be 4-byte aligned");
+  cudaError_t e = cudaSuccess;
+  if (c.status == OASIS_OK)
+    e = oasis::launch_resume_attn(s, (const uint16_t*)q, q_stride, (const uint16_t*)k, k_stride, (const uint16_t*)v, v_stride,
+                                  q_start, n_rows, kv_start, n_kv_rows, scale, workspace, (uint16_t*)out, out_stride,
+                                  err_word, (cudaStream_t)stream);
   return finish(fn, c, e);
 }
 

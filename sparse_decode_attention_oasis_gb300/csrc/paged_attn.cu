@@ -43,6 +43,8 @@
 // pages ahead (177 to 197), queries loaded before the tables but converted after (205:
 // the live registers cost the loop), 4 or 16 warps to a block (no change), one join
 // block for all query rows of a pair (1 us more).
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace oasis {
@@ -64,7 +66,7 @@ struct Args {
   const uint16_t* q;
   size_t q_stride;
   const uint8_t* pages;
-  const float* scales;
+  const void* scales;  // 8 bits: float, 4 bits: bytes
   const int* table;
   const int* ctx_len;
   const int* sel;
@@ -153,6 +155,74 @@ __device__ __forceinline__ void load_values(Rows& v, const uint8_t* page, int la
   v.v[3] = load16_stream(p + 9 * kD);
 }
 
+// The same in 4 bits, with their scales.  A lane's 16 dimensions of a value row are one group, its 32 of a key row two.
+struct Keys4 {  // rows lane / 4 and + 8, dimensions 32 (lane % 4) ..
+  uint4 v[2];
+  uint32_t scale[2];
+  __device__ __forceinline__ void load(const uint8_t* page, const uint8_t* scales, int lane) {
+    const uint8_t* p = page + (lane >> 2) * (kD / 2) + (lane & 3) * 16;
+    v[0] = load16_stream(p);
+    v[1] = load16_stream(p + 8 * (kD / 2));
+    const uint8_t* s = scales + (lane >> 2) * kGroups + (lane & 3) * 2;
+    scale[0] = load2_stream(s);
+    scale[1] = load2_stream(s + 8 * kGroups);
+  }
+};
+struct Values4 {  // tokens 2 (lane % 4), + 1, + 8, + 9, dimensions 16 (lane / 4) ..
+  uint2 v[4];
+  uint32_t scale[2];
+  __device__ __forceinline__ void load(const uint8_t* page, const uint8_t* scales, int lane) {
+    const uint8_t* p = page + kBS * (kD / 2) + (lane & 3) * kD + (lane >> 2) * 8;
+    v[0] = load8_stream(p);
+    v[1] = load8_stream(p + kD / 2);
+    v[2] = load8_stream(p + 8 * (kD / 2));
+    v[3] = load8_stream(p + 9 * (kD / 2));
+    const uint8_t* s = scales + kBS * kGroups + (lane >> 2) * kBS + (lane & 3) * 2;
+    scale[0] = load2_stream(s);
+    scale[1] = load2_stream(s + 8);
+  }
+};
+
+// S^T += K Q^T of a page in 4 bits: a step of the product takes 4 of the lane's 32 dimensions (step m: 4m ..).
+__device__ __forceinline__ void scores4(float* sc, const Keys4& k, const uint32_t* qf) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {  // a group of 16 dimensions
+    const uint32_t f0 = half ? scale_twice<1>(k.scale[0]) : scale_twice<0>(k.scale[0]);
+    const uint32_t f1 = half ? scale_twice<1>(k.scale[1]) : scale_twice<0>(k.scale[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = word(k.v[0], 2 * half + i), hi = word(k.v[1], 2 * half + i);
+      const int m = 4 * half + 2 * i;
+      mma_f16_16816(sc, mul_f16x2(e2m1x2_to_f16x2<0>(lo), f0), mul_f16x2(e2m1x2_to_f16x2<0>(hi), f1),
+                    mul_f16x2(e2m1x2_to_f16x2<1>(lo), f0), mul_f16x2(e2m1x2_to_f16x2<1>(hi), f1), qf[2 * m], qf[2 * m + 1]);
+      mma_f16_16816(sc, mul_f16x2(e2m1x2_to_f16x2<2>(lo), f0), mul_f16x2(e2m1x2_to_f16x2<2>(hi), f1),
+                    mul_f16x2(e2m1x2_to_f16x2<3>(lo), f0), mul_f16x2(e2m1x2_to_f16x2<3>(hi), f1), qf[2 * m + 2],
+                    qf[2 * m + 3]);
+    }
+  }
+}
+
+// O^T += V^T W^T of a page in 4 bits: bytes of a token's row hold two dimensions, the product takes pairs of tokens, so
+// the codes of two rows are exchanged (lo: the even dimensions of both, hi: the odd ones) before they become halves.
+__device__ __forceinline__ void outputs4(float (*acc)[4], const Values4& v, uint32_t b0, uint32_t b1) {
+  const uint32_t f0 = scale_pair(v.scale[0]), f1 = scale_pair(v.scale[1]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t0 = i ? v.v[0].y : v.v[0].x, t1 = i ? v.v[1].y : v.v[1].x;
+    const uint32_t t8 = i ? v.v[2].y : v.v[2].x, t9 = i ? v.v[3].y : v.v[3].x;
+    const uint32_t lo0 = (t0 & 0x0f0f0f0fu) | (t1 << 4 & 0xf0f0f0f0u), hi0 = (t0 >> 4 & 0x0f0f0f0fu) | (t1 & 0xf0f0f0f0u);
+    const uint32_t lo1 = (t8 & 0x0f0f0f0fu) | (t9 << 4 & 0xf0f0f0f0u), hi1 = (t8 >> 4 & 0x0f0f0f0fu) | (t9 & 0xf0f0f0f0u);
+    mma_f16_16816(acc[4 * i], mul_f16x2(e2m1x2_to_f16x2<0>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<0>(hi0), f0),
+                  mul_f16x2(e2m1x2_to_f16x2<0>(lo1), f1), mul_f16x2(e2m1x2_to_f16x2<0>(hi1), f1), b0, b1);
+    mma_f16_16816(acc[4 * i + 1], mul_f16x2(e2m1x2_to_f16x2<1>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<1>(hi0), f0),
+                  mul_f16x2(e2m1x2_to_f16x2<1>(lo1), f1), mul_f16x2(e2m1x2_to_f16x2<1>(hi1), f1), b0, b1);
+    mma_f16_16816(acc[4 * i + 2], mul_f16x2(e2m1x2_to_f16x2<2>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<2>(hi0), f0),
+                  mul_f16x2(e2m1x2_to_f16x2<2>(lo1), f1), mul_f16x2(e2m1x2_to_f16x2<2>(hi1), f1), b0, b1);
+    mma_f16_16816(acc[4 * i + 3], mul_f16x2(e2m1x2_to_f16x2<3>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<3>(hi0), f0),
+                  mul_f16x2(e2m1x2_to_f16x2<3>(lo1), f1), mul_f16x2(e2m1x2_to_f16x2<3>(hi1), f1), b0, b1);
+  }
+}
+
 struct Shared {
   float2 top_sum[2 * kWarps][kMaxG];  // of a piece's rows
   long long chunk_start[kThreads + 1];
@@ -172,8 +242,8 @@ __device__ __forceinline__ float2 load_remote(const float* mine, unsigned rank) 
   return v;
 }
 
-// kClustered: a cluster of `team` blocks for each pair, else all pages in equal ranges.
-template <bool kClustered>
+// kClustered: a cluster of `team` blocks for each pair, else all pages in equal ranges.  kBits: 8 or 4.
+template <bool kClustered, int kBits>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_decode_attn_kernel(PagedShape s, Args a) {
   extern __shared__ __align__(16) float slot_rows[];  // [2 * kWarps][G][kD], then (kClustered) [G][kRowFloats]
@@ -276,11 +346,12 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
         if ((lane >> 2) < G) {
-          const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * 16;
+          constexpr int kPiece = kBits == 8 ? 16 : 32, kNext = kBits == 8 ? 64 : 16;
+          const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * kPiece;
           w[0] = load16(src);
           w[1] = load16(src + 8);
-          w[2] = load16(src + 64);
-          w[3] = load16(src + 72);
+          w[2] = load16(src + kNext);
+          w[3] = load16(src + kNext + 8);
         }
         uint32_t m = 0;
 #pragma unroll
@@ -304,10 +375,11 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
       }
 
-      Rows kr, vr;
+      std::conditional_t<kBits == 8, Rows, Keys4> kr;
+      std::conditional_t<kBits == 8, Rows, Values4> vr;
       int my_page = -1, my_valid = 0;  // of page (group of 32) + lane
       float2 my_scale = make_float2(1.f, 1.f);
-      const long long head_stride = kHeadPageBytes;
+      const long long head_stride = kBits == 8 ? kHeadPageBytes : kHeadPageBytes4;
       auto lookup = [&](int at) {  // tables of pages at .. at + 31
         my_page = -1;
         my_valid = 0;
@@ -326,7 +398,8 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
             if (pg >= 0 && pg < s.n_pages) {
               my_page = pg;
               my_valid = min(kBS, ctx - blk * kBS);
-              my_scale = *reinterpret_cast<const float2*>(a.scales + ((long long)pg * s.Hkv + h) * 2);
+              if constexpr (kBits == 8)
+                my_scale = *reinterpret_cast<const float2*>(static_cast<const float*>(a.scales) + ((long long)pg * s.Hkv + h) * 2);
             } else {
               bits |= OASIS_EW_BAD_SLOT;
             }
@@ -334,35 +407,54 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
         }
       };
       auto head_page = [&](int page) { return a.pages + ((long long)page * s.Hkv + h) * head_stride; };
+      auto head_scales = [&](int page) {
+        return static_cast<const uint8_t*>(a.scales) + ((long long)page * s.Hkv + h) * kHeadScaleBytes4;
+      };
+      auto fetch_keys = [&](int page) {
+        if constexpr (kBits == 8) load_keys(kr, head_page(page), lane);
+        else kr.load(head_page(page), head_scales(page), lane);
+      };
+      auto fetch_values = [&](int page) {
+        if constexpr (kBits == 8) load_values(vr, head_page(page), lane);
+        else vr.load(head_page(page), head_scales(page), lane);
+      };
 
       lookup(first);
       int page = __shfl_sync(0xffffffffu, my_page, 0);
       if (page >= 0) {
-        load_keys(kr, head_page(page), lane);
-        load_values(vr, head_page(page), lane);
+        fetch_keys(page);
+        fetch_values(page);
       }
       State st;
       st.clear();
       for (int at = first; at < last; ++at) {
         const int in = (at - first) & 31;
         const int valid = __shfl_sync(0xffffffffu, my_valid, in);
-        const float ks = __shfl_sync(0xffffffffu, my_scale.x, in), vs = __shfl_sync(0xffffffffu, my_scale.y, in);
+        float ks = 1.f, vs = 1.f;
+        if constexpr (kBits == 8) {
+          ks = __shfl_sync(0xffffffffu, my_scale.x, in);
+          vs = __shfl_sync(0xffffffffu, my_scale.y, in);
+        }
         const bool here = page >= 0;
         if (in == 31) lookup(at + 1);
         page = at + 1 < last ? __shfl_sync(0xffffffffu, my_page, (at + 1 - first) & 31) : -1;
         float sc[4] = {0.f, 0.f, 0.f, 0.f};
         if (here) {
+          if constexpr (kBits == 8) {
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const uint32_t lo = word(kr.v[m >> 2], m & 3), hi = word(kr.v[2 + (m >> 2)], m & 3);
-            mma_f16_16816(sc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_hi_to_f16x2(lo),
-                          e4m3x2_hi_to_f16x2(hi), qf[2 * m], qf[2 * m + 1]);
+            for (int m = 0; m < 8; ++m) {
+              const uint32_t lo = word(kr.v[m >> 2], m & 3), hi = word(kr.v[2 + (m >> 2)], m & 3);
+              mma_f16_16816(sc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_hi_to_f16x2(lo),
+                            e4m3x2_hi_to_f16x2(hi), qf[2 * m], qf[2 * m + 1]);
+            }
+          } else {
+            scores4(sc, kr, qf);
           }
         }
-        if (page >= 0) load_keys(kr, head_page(page), lane);
+        if (page >= 0) fetch_keys(page);
         if (here) {
           const int g = lane >> 2;
-          const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 0xff) - 127);
+          const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 0xff) - 127);  // 4 bits: 0
           const float f0 = fac[0] * ks, f1 = fac[1] * ks;
           float s0 = fmaf(sc[0], f0, lv), s1 = fmaf(sc[1], f1, lv);
           float s2 = fmaf(sc[2], f0, lv), s3 = fmaf(sc[3], f1, lv);
@@ -371,10 +463,15 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
             if (g + 8 >= valid) s2 = s3 = neg_inf();
             // what lies behind the last token may be NaN: zero times it is not zero
             const int t = (lane & 3) * 2;
-            if (t >= valid) vr.v[0] = make_uint4(0u, 0u, 0u, 0u);
-            if (t + 1 >= valid) vr.v[1] = make_uint4(0u, 0u, 0u, 0u);
-            if (t + 8 >= valid) vr.v[2] = make_uint4(0u, 0u, 0u, 0u);
-            if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (kBits == 8) {
+              if (t >= valid) vr.v[0] = make_uint4(0u, 0u, 0u, 0u);
+              if (t + 1 >= valid) vr.v[1] = make_uint4(0u, 0u, 0u, 0u);
+              if (t + 8 >= valid) vr.v[2] = make_uint4(0u, 0u, 0u, 0u);
+              if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
+            } else {  // codes are finite, scales may not be
+              vr.scale[0] &= t >= valid ? 0u : t + 1 >= valid ? 0xffu : 0xffffu;
+              vr.scale[1] &= t + 8 >= valid ? 0u : t + 9 >= valid ? 0xffu : 0xffffu;
+            }
           }
           float m0 = fmaxf(fmaxf(s0, s2), kLowest), m1 = fmaxf(fmaxf(s1, s3), kLowest);
           if (__any_sync(0xffffffffu, m0 > st.top[0] + kMostBits || m1 > st.top[1] + kMostBits)) {
@@ -403,6 +500,8 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
           st.sum[0] = fmaf(w0 + w2, iv, st.sum[0]);
           st.sum[1] = fmaf(w1 + w3, iv, st.sum[1]);
           const uint32_t b0 = transpose_8x8(pack_f16x2(w0, w1)), b1 = transpose_8x8(pack_f16x2(w2, w3));
+          if constexpr (kBits == 4) outputs4(st.acc, vr, b0, b1);
+          else
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const uint32_t t0 = word(vr.v[0], m), t1 = word(vr.v[1], m), t8 = word(vr.v[2], m), t9 = word(vr.v[3], m);
@@ -414,7 +513,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
                           e4m3x2_hi_to_f16x2(p3), b0, b1);
           }
         }
-        if (page >= 0) load_values(vr, head_page(page), lane);
+        if (page >= 0) fetch_values(page);
       }
 
       // ---- the pair's piece: the output if it is all of it, else a slot
@@ -595,10 +694,14 @@ size_t paged_attn_workspace_bytes(const PagedShape& s) {
   return n * 2 * s.G() * kRowFloats * sizeof(float) + n * sizeof(int2);
 }
 
-cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint8_t* pages,
-                                     const float* scales, const int* table, const int* ctx, const int* sel,
-                                     const int* nsel, int sel_max, float scale, void* ws, uint16_t* out,
-                                     unsigned* err, cudaStream_t stream) {
+namespace {
+
+std::mutex both_launches[kMaxDevicesCached];
+
+template <int kBits>
+cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint8_t* pages, const void* scales,
+                          const int* table, const int* ctx, const int* sel, const int* nsel, int sel_max, float scale,
+                          void* ws, uint16_t* out, unsigned* err, cudaStream_t stream) {
   const int most = most_blocks();
   const long long pages_max = (long long)s.B * s.Hkv * (sel ? sel_max : s.nb_max);
   const long long blocks = (pages_max + kMinPages - 1) / kMinPages;
@@ -620,21 +723,36 @@ cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, siz
   if (pairs * a.team <= most && pair_max <= team_pages * a.team) {
     const size_t with_piece = smem + (size_t)s.G() * kRowFloats * sizeof(float);
     static int attr_cache[kMaxDevicesCached] = {};
-    cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<true>, with_piece, attr_cache);
+    cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<true, kBits>, with_piece, attr_cache);
     if (e != cudaSuccess) return e;
-    return launch_chained(paged_decode_attn_kernel<true>, dim3((unsigned)(pairs * a.team)), dim3(kThreads), with_piece, stream,
+    return launch_chained(paged_decode_attn_kernel<true, kBits>, dim3((unsigned)(pairs * a.team)), dim3(kThreads), with_piece, stream,
                           a.team, s, a);
   }
   static int attr_cache[kMaxDevicesCached] = {};
-  cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<false>, smem, attr_cache);
+  cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<false, kBits>, smem, attr_cache);
   if (e != cudaSuccess) return e;
   // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
-  static std::mutex both[kMaxDevicesCached];
-  std::lock_guard<std::mutex> lock(both[current_device()]);
-  e = launch_chained(paged_decode_attn_kernel<false>, dim3(grid), dim3(kThreads), smem, stream, 1, s, a);
+  std::lock_guard<std::mutex> lock(both_launches[current_device()]);
+  e = launch_chained(paged_decode_attn_kernel<false, kBits>, dim3(grid), dim3(kThreads), smem, stream, 1, s, a);
   if (e != cudaSuccess || grid == 1) return e;
   return launch_chained(paged_decode_join_kernel, dim3(grid, s.G()), dim3(kJoinWarps * 32), 0, stream, 1, s, parts, a.tails,
                         out);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint8_t* pages,
+                                     const float* scales, const int* table, const int* ctx, const int* sel,
+                                     const int* nsel, int sel_max, float scale, void* ws, uint16_t* out,
+                                     unsigned* err, cudaStream_t stream) {
+  return launch_decode<8>(s, q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, scale, ws, out, err, stream);
+}
+
+cudaError_t launch_paged_decode_attn_q4(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint8_t* pages,
+                                        const uint8_t* scales, const int* table, const int* ctx, const int* sel,
+                                        const int* nsel, int sel_max, float scale, void* ws, uint16_t* out,
+                                        unsigned* err, cudaStream_t stream) {
+  return launch_decode<4>(s, q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, scale, ws, out, err, stream);
 }
 
 }  // namespace oasis

@@ -1,0 +1,120 @@
+// New K/V rows quantised into 4-bit pages (oasis_store_kv_q4).
+//
+// Mathematics: for 16 dimensions of one token of one head, s = the least scale (5 exponent, 3 fraction
+// bits) of at least amax / 6 (6: the largest e2m1), y = e2m1(x / s), ties to the even code.  Every
+// token has its own scales, so a page's earlier tokens stay as they are, whatever comes later.
+// The quotient is formed as x * (1 / s) in fp32 and rounded to a multiple of 2^-16 by adding and
+// taking away 192; that has one right answer: with 8 bits in x and 4 in s a quotient is a tie of the
+// codes (a multiple of 1/4) exactly or is 2^-11 away from each, and the product is off by less than
+// 2^-20, so ties come out as ties and everything else stays on its side.
+//
+// Two rows of one head to a warp's instruction: 16 lanes of 16 bytes cover a row, a pair of lanes a
+// group.  Rows are independent, so there is no order to keep and nothing is read but the rows.
+#include <cuda_fp16.h>
+
+#include "paged.cuh"
+
+namespace oasis {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kRows = 16;  // rows of a warp in long calls
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The byte of the least scale of at least amax / 6, at most the largest one in use.
+__device__ __forceinline__ int scale_byte(float amax) {
+  const float r = __fdiv_rn(amax, 6.0f);
+  if (r < 6.103515625e-5f) return (int)ceilf(r * 131072.0f);  // below 2^-14: multiples of 2^-17
+  return (int)min((__float_as_uint(r) + 0xfffffu) >> 20, (uint32_t)(kScaleByteHigh + 896)) - 896;  // 896: exponents' bias
+}
+
+// Eight quotients -> codes, the lowest dimension in the lowest bits; a zero has no sign.
+__device__ __forceinline__ uint32_t codes8(const float* y) {
+  uint32_t w;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  const uint32_t some = (w | w >> 1 | w >> 2) & 0x11111111u;
+  return w & (0x77777777u | some << 3);
+}
+
+// grid: x = groups of kWarps * per rows, y = heads * 2 (K, V); per: rows of a warp, 2 or kRows.
+template <int kPer>
+__global__ void __launch_bounds__(kWarps * 32)
+store_kv_q4_kernel(PagedShape s, const uint16_t* k, size_t k_stride, const uint16_t* v, size_t v_stride,
+                   const int* slot_map, int n_rows, uint8_t* pages, uint8_t* scales, unsigned* err) {
+  wait_for_predecessor();
+  const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
+  const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
+  const uint16_t* src = (which ? v : k) + (size_t)h * kD + col * 8;
+  const size_t stride = which ? v_stride : k_stride;
+  const long long r0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kPer;
+  const int n_slots = s.n_pages * kBS;
+  unsigned bits = 0;
+  if (r0 >= n_rows) return;
+  uint4 x[kPer / 2];
+  int slot[kPer / 2];
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i) {
+    const long long r = r0 + 2 * i + half;
+    slot[i] = r < n_rows ? slot_map[r] : -1;
+    x[i] = r < n_rows ? load16_stream(src + (size_t)r * stride) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                           max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the group's other lane
+    const bool nan = m > 0x7f80u;
+    const int b = scale_byte(__uint_as_float(m << 16));
+    const float inv = b ? __fdiv_rn(1.0f, __half2float(__ushort_as_half((unsigned short)(b << 7)))) : 0.f;
+    float y[8];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      y[2 * d] = fmaf(bf_lo(w[d]), inv, 192.0f) - 192.0f;
+      y[2 * d + 1] = fmaf(bf_hi(w[d]), inv, 192.0f) - 192.0f;
+    }
+    const uint32_t code = nan ? 0u : codes8(y);
+    if (slot[i] < 0 || slot[i] >= n_slots) {
+      if (slot[i] != -1) bits |= OASIS_EW_BAD_SLOT;
+      continue;  // no shuffle follows in this turn
+    }
+    const int pos = slot[i] % kBS;
+    const long long head_page = (long long)(slot[i] / kBS) * s.Hkv + h;
+    uint8_t* dst = pages + head_page * kHeadPageBytes4 + which * (kBS * kD / 2) + pos * (kD / 2);
+    *reinterpret_cast<uint32_t*>(dst + col * 4) = code;
+    if ((col & 1) == 0) {
+      uint8_t* to = scales + head_page * kHeadScaleBytes4 + which * (kBS * kGroups);
+      to[which ? (col >> 1) * kBS + pos : pos * kGroups + (col >> 1)] = (uint8_t)(nan ? kScaleByteNaN : b);
+    }
+  }
+  if (blockIdx.y == 0) set_err(err, bits);
+}
+
+}  // namespace
+
+cudaError_t launch_store_kv_q4(const PagedShape& s, const uint16_t* k, size_t k_stride, const uint16_t* v, size_t v_stride,
+                               const int* slot_map, int n_rows, uint8_t* pages, uint8_t* scales, unsigned* err,
+                               cudaStream_t stream) {
+  if (n_rows == 0) return cudaSuccess;
+  // Two rows to a warp while all those warps are resident at once; long calls take 16 for the loads in flight.
+  const long long resident = (long long)sm_count() * 64;
+  const bool few = ((long long)n_rows + 1) / 2 * s.Hkv * 2 <= resident;
+  const int per = few ? 2 : kRows;
+  const dim3 grid((unsigned)(((long long)n_rows + kWarps * per - 1) / (kWarps * per)), (unsigned)(2 * s.Hkv));
+  if (few)
+    return launch_chained(store_kv_q4_kernel<2>, grid, dim3(kWarps * 32), 0, stream, 1, s, k, k_stride, v, v_stride, slot_map,
+                          n_rows, pages, scales, err);
+  return launch_chained(store_kv_q4_kernel<kRows>, grid, dim3(kWarps * 32), 0, stream, 1, s, k, k_stride, v, v_stride,
+                        slot_map, n_rows, pages, scales, err);
+}
+
+}  // namespace oasis

@@ -53,6 +53,8 @@
 // against 53, the others the same, for 80 lines of accounting).
 // Every wait is bounded: on expiry the block raises OASIS_EW_TIMEOUT, waits (bounded)
 // for its own copies and MMAs, frees TMEM and returns.
+#include <type_traits>
+
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -85,6 +87,40 @@ struct Item {
   int h;      // KV head
 };
 
+// An item of a call with keys before the new rows, or a part of one: K/V tiles j0 .. j1 - 1 of the sequence.
+struct Piece : Item {
+  int kv0;     // first K/V row of the sequence
+  int past;    // keys before its first query row
+  int j0, j1;
+  bool whole;  // all tiles of the item
+};
+
+__device__ __forceinline__ int past_of(const Item&) { return 0; }
+__device__ __forceinline__ int past_of(const Piece& it) { return it.past; }
+__device__ __forceinline__ int kv_row(const Item& it) { return it.row0; }
+__device__ __forceinline__ int kv_row(const Piece& it) { return it.kv0; }
+__device__ __forceinline__ int first_tile(const Item&) { return 0; }
+__device__ __forceinline__ int first_tile(const Piece& it) { return it.j0; }
+
+// What the parts of items that cross thread blocks leave for the join.  A block has two places: 0 for a part of an item
+// that began in a block before it, 1 for the first part of one that goes on in the next.
+struct Tail {
+  int row0, len, tok0, h, past;
+  int last;    // the block with the item's last tiles, -1: no item goes on from here
+  int2 tiles[2];  // j0, j1 of the parts in this block's places, (0, 0): none
+};
+struct Parts {
+  const int* kv_start;
+  int n_kv_rows;
+  float* o;       // [blocks][2][2 * kTile][kD], not divided
+  float2* stats;  // [blocks][2][2 * kTile]: reference and sum of a row
+  Tail* tails;    // [blocks]
+  __device__ __forceinline__ size_t row(int block, int place, int r) const {
+    return ((size_t)block * 2 + place) * (2 * kTile) + r;
+  }
+};
+
+template <class It>
 struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kRing], kv_empty[kRing];
@@ -92,15 +128,16 @@ struct Bars {
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t raw_full[kRing];  // V tiles that the scheduler warp has to look over first
   uint64_t done[2];
-  Item items[kItems];
+  It items[kItems];
   uint32_t tmem_base;
   int abort_flag;
   int token;  // 1: a row tile's products are being issued
   int cleaned;  // 1: infinities or NaN of V were taken out of a tile
 };
 
-constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a thread block");
+template <class It>
+constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kTileBytes + kRing * (size_t)kTileBytes + sizeof(Bars<It>);
+static_assert(kSmemBytes<Piece> <= 227 * 1024, "shared memory of a thread block");
 
 // Shared-memory operand descriptors, low word: address and leading offset, high word: the rest.
 // Q, K: K-major 128-byte rows, 8-row groups 1,024 B apart.  V: rows are tokens (the contraction),
@@ -223,13 +260,21 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   return w;
 }
 
-// The first K/V tile of an item with tokens after the item's first one.
-__device__ __forceinline__ int first_masked(const Item& it) { return (it.tok0 + 1) / kTile; }
+// The first K/V tile of an item's sequence with tokens after the item's first one.
+template <class It>
+__device__ __forceinline__ int first_masked(const It& it) {
+  return (past_of(it) + it.tok0 + 1) / kTile;
+}
 
 // K/V tiles that query tile i of an item reads (0: the tile has no token).
-__device__ __forceinline__ int kv_tiles(const Item& it, int i, int per) {
+template <class It>
+__device__ __forceinline__ int tiles_of(const It& it, int i, int per) {
   const int t0 = it.tok0 + i * per;
-  return t0 < it.len ? (min(it.len, t0 + per) + kTile - 1) / kTile : 0;
+  return t0 < it.len ? (past_of(it) + min(it.len, t0 + per) + kTile - 1) / kTile : 0;
+}
+__device__ __forceinline__ int kv_tiles(const Item& it, int i, int per) { return tiles_of(it, i, per); }
+__device__ __forceinline__ int kv_tiles(const Piece& it, int i, int per) {  // those of this part
+  return max(min(tiles_of(it, i, per), it.j1) - it.j0, 0);
 }
 
 // Work items: two query tiles of one sequence and KV head.  Up to 320 sequences are kept in one
@@ -350,26 +395,197 @@ struct Schedule {
   }
 };
 
+// The items of a call with keys before its new rows, cut into equal ranges of cost for the thread blocks: cost in keys,
+// past + the keys of the item's last row (whole tiles of rows) + kItemCost for its ends.  A sequence's items follow
+// each other head by head; an item that crosses a range's border is cut at a tile there (not one tile from its ends).
+struct Ranges {
+  static constexpr long long kItemCost = 192, kLeast = 512;  // least cost of a block's range
+  const int *q_start, *kv_start;
+  int B, n_rows, n_kv_rows, pair, per, heads, lane;
+  unsigned bits;
+  long long lo, hi;        // this block's range
+  long long share, extra;  // all ranges: `extra` of them are one longer than `share`
+  // the sequence at hand
+  int b, a, len, kv0, past;
+  long long start, of_head;  // where it begins, a head's cost
+  int h, place;              // the next item
+  long long at;              // where it begins
+
+  __device__ bool sequence(int s, int& qa, int& n, int& ka, int& before) {
+    qa = q_start[s];
+    n = q_start[s + 1] - qa;
+    ka = kv_start[s];
+    const int m = kv_start[s + 1] - ka;
+    before = m - n;
+    const bool good = qa >= 0 && n >= 0 && q_start[s + 1] <= n_rows && ka >= 0 && m >= n && kv_start[s + 1] <= n_kv_rows;
+    if (!good) {
+      bits |= OASIS_EW_BAD_COUNT;
+      n = 0;
+    }
+    return n > 0;
+  }
+  __device__ long long before_place(int p, int keys) const {  // cost of a head's items before place p
+    return (long long)p * (keys + kItemCost) + (long long)pair * ((long long)p * (p + 1) / 2);
+  }
+  __device__ long long head_cost(int n, int keys) const { return before_place((n + pair - 1) / pair, keys); }
+
+  // gives the number of blocks that have a range
+  __device__ int init(const int* qs, const Parts& parts, int b_, int rows, int tokens, int hkv, int ln) {
+    q_start = qs;
+    kv_start = parts.kv_start;
+    B = b_;
+    n_rows = rows;
+    n_kv_rows = parts.n_kv_rows;
+    per = tokens;
+    pair = 2 * tokens;
+    heads = hkv;
+    lane = ln;
+    bits = 0;
+    long long total = 0;
+    for (int s = lane; s < B; s += 32) {
+      int qa, n, ka, before;
+      if (sequence(s, qa, n, ka, before)) total += heads * head_cost(n, before);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const long long most = (total + kLeast - 1) / kLeast;
+    const int blocks = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
+    lo = hi = at = 0;
+    len = 0;
+    if ((int)blockIdx.x >= blocks) return blocks;
+    share = total / blocks;
+    extra = total % blocks;
+    lo = begin_of(blockIdx.x);
+    hi = begin_of(blockIdx.x + 1);
+    // the sequence that holds cost lo
+    start = 0;
+    for (int w = 0;; w += 32) {
+      const int s = w + lane;
+      int qa, n, ka, before;
+      const unsigned keep = bits;  // reported by the pass above
+      long long c = s < B && sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0, x = c;
+      bits = keep;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, start + x > lo);
+      if (over) {
+        const int src = __ffs(over) - 1;
+        start += __shfl_sync(0xffffffffu, x - c, src);
+        take_sequence(w + src);
+        break;
+      }
+      start += __shfl_sync(0xffffffffu, x, 31);
+    }
+    h = (int)((lo - start) / of_head);
+    const long long rest = lo - start - h * of_head;
+    int p0 = 0, p1 = (len + pair - 1) / pair - 1;  // the last place that begins at or before it
+    while (p0 < p1) {
+      const int m = (p0 + p1 + 1) >> 1;
+      if (before_place(m, past) <= rest) p0 = m; else p1 = m - 1;
+    }
+    place = p0;
+    at = start + h * of_head + before_place(place, past);
+    return blocks;
+  }
+  __device__ long long begin_of(int block) const { return block * share + min((long long)block, extra); }
+  __device__ int block_of(long long cost) const {
+    const long long longer = extra * (share + 1);
+    return (int)(cost < longer ? cost / (share + 1) : extra + (cost - longer) / share);
+  }
+  __device__ void take_sequence(int s) {
+    b = s;
+    const unsigned keep = bits;
+    sequence(s, a, len, kv0, past);
+    bits = keep;
+    of_head = len > 0 ? head_cost(len, past) : 0;
+    h = place = 0;
+  }
+  // The tile at which a border inside an item cuts it, `cost` behind its beginning.
+  __device__ int cut(long long cost, int tiles) const {
+    const int j = (int)min(max(cost - kItemCost, 0ll) / kTile, (long long)tiles);
+    return j < 2 ? 0 : tiles - j < 2 ? tiles : j;
+  }
+  // This block's next part (row0 -1: there are no more).  tail: of an item that goes on behind this block's range.
+  __device__ Piece next(int* last) {
+    *last = -1;
+    while (at < hi) {
+      Piece it;
+      it.row0 = a;
+      it.len = len;
+      it.tok0 = place * pair;
+      it.h = h;
+      it.kv0 = kv0;
+      it.past = past;
+      const int tiles = max(tiles_of(it, 0, per), tiles_of(it, 1, per));
+      const long long from = at, to = start + h * of_head + before_place(place + 1, past);
+      at = to;
+      if (++place * (long long)pair >= len) {
+        place = 0;
+        if (++h == heads) {
+          h = 0;
+          start = to;
+          len = 0;
+          while (len == 0 && at < hi) take_sequence(b + 1);  // below hi there is another one
+        }
+      }
+      it.j0 = from < lo ? cut(lo - from, tiles) : 0;
+      it.j1 = to > hi ? cut(hi - from, tiles) : tiles;
+      it.whole = it.j0 == 0 && it.j1 == tiles;
+      if (it.j0 >= it.j1) continue;
+      if (it.j0 == 0 && !it.whole) *last = block_of(to - 1);
+      return it;
+    }
+    Piece none = {};
+    none.row0 = -1;
+    return none;
+  }
+};
+
 // Adds to a block's output rows what was taken out of V: infinities and NaN of the tokens from an item's second to each
 // row's own.  An item to a warp of the first eight, four dimensions to a lane; rare, so out of the kernel's own code.
+template <class It>
 __device__ __noinline__ void give_back(int sequences, int heads, int G, const int* row_start, int n_rows, const uint16_t* v,
-                                       size_t v_stride, uint16_t* out, size_t out_stride) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tokens = 2 * (kTile / G);
-  Schedule sch;
-  sch.init(row_start, sequences, n_rows, tokens, lane);
+                                       size_t v_stride, uint16_t* out, size_t out_stride, Parts parts) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = kTile / G, tokens = 2 * per;
+  std::conditional_t<std::is_same_v<It, Item>, Schedule, Ranges> sch;
+  if constexpr (std::is_same_v<It, Item>) sch.init(row_start, sequences, n_rows, tokens, lane);
+  else sch.init(row_start, parts, sequences, n_rows, per, heads, lane);
   for (int k = 0;; ++k) {
-    const Item it = sch.item(k, heads);
+    It it;
+    if constexpr (std::is_same_v<It, Item>) {
+      it = sch.item(k, heads);
+    } else {
+      int last;
+      it = sch.next(&last);
+    }
     if (it.row0 < 0) return;
     if (k % 8 != warp) continue;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t = it.tok0 + 1; t < min(it.len, it.tok0 + tokens); ++t) {
-      const uint2 x = *reinterpret_cast<const uint2*>(v + (size_t)(it.row0 + t) * v_stride + (size_t)it.h * kD + lane * 4);
-      const uint32_t w[4] = {x.x << 16, x.x & 0xffff0000u, x.y << 16, x.y & 0xffff0000u};
+      bool here = true;  // the token's key and value are in this part's tiles
+      if constexpr (!std::is_same_v<It, Item>) here = it.past + t >= it.j0 * kTile && it.past + t < it.j1 * kTile;
+      if (here) {
+        const uint2 x = *reinterpret_cast<const uint2*>(v + (size_t)(kv_row(it) + past_of(it) + t) * v_stride +
+                                                        (size_t)it.h * kD + lane * 4);
+        const uint32_t w[4] = {x.x << 16, x.x & 0xffff0000u, x.y << 16, x.y & 0xffff0000u};
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
-        if ((w[d] & 0x7f800000u) == 0x7f800000u) sum[d] += __uint_as_float(w[d]);
+        for (int d = 0; d < 4; ++d)
+          if ((w[d] & 0x7f800000u) == 0x7f800000u) sum[d] += __uint_as_float(w[d]);
+      }
       if (sum[0] == 0.f && sum[1] == 0.f && sum[2] == 0.f && sum[3] == 0.f) continue;
       for (int g = 0; g < G; ++g) {
+        if constexpr (!std::is_same_v<It, Item>) {
+          if (!it.whole) {
+            const int i = (t - it.tok0) / per, r = i * kTile + (t - it.tok0 - i * per) * G + g;
+            float4* dst = reinterpret_cast<float4*>(parts.o + parts.row(blockIdx.x, it.j0 == 0, r) * kD) + lane;
+            const float4 o = *dst;
+            *dst = make_float4(o.x + sum[0], o.y + sum[1], o.z + sum[2], o.w + sum[3]);
+            continue;
+          }
+        }
         uint2* dst = reinterpret_cast<uint2*>(out + (size_t)(it.row0 + t) * out_stride + (size_t)(it.h * G + g) * kD + lane * 4);
         const uint2 o = *dst;
         *dst = make_uint2(pack_bf16x2(bf_lo(o.x) + sum[0], bf_hi(o.x) + sum[1]),
@@ -382,27 +598,31 @@ __device__ __noinline__ void give_back(int sequences, int heads, int G, const in
 // The scheduler warp: hands out the block's items, and looks over the V tiles with tokens that not all rows of an item
 // attend.  False: a wait gave up.  Out of the kernel's own code (56 registers of the warp's 88): inlined, it crowded
 // the other roles, and the whole kernel took 4 to 5% longer.
-__device__ __noinline__ bool schedule(Bars* bars, uint8_t* ring, int sequences, int heads, int per, const int* row_start,
-                                      int n_rows, unsigned* err) {
+template <class It>
+__device__ __noinline__ bool schedule(Bars<It>* bars, uint8_t* ring, int sequences, int heads, int per, const int* row_start,
+                                      int n_rows, Parts parts, unsigned* err) {
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
   };
   bool ok = true;
-  Schedule sch;
-  sch.init(row_start, sequences, n_rows, 2 * per, lane);
+  std::conditional_t<std::is_same_v<It, Item>, Schedule, Ranges> sch;
+  Tail tail = {};
+  tail.last = -1;
+  if constexpr (std::is_same_v<It, Item>) sch.init(row_start, sequences, n_rows, 2 * per, lane);
+  else sch.init(row_start, parts, sequences, n_rows, per, heads, lane);
   unsigned slot = 0, raw_uses = 0;  // ring places of the items before, uses of raw_full (odd: 1)
   // Rows behind the sequence's last token become zeros, infinities and NaN after the item's first token too.
-  auto look_over = [&](const Item& it) {
-    const int n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
-    for (int j = first_masked(it); j < n; ++j) {
-      const unsigned place = (slot + 2 * (unsigned)j + 1) % kRing;
+  auto look_over = [&](const It& it) {
+    const int n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per)), j0 = first_tile(it), keys = past_of(it) + it.len;
+    for (int j = max(first_masked(it), j0); j < j0 + n; ++j) {
+      const unsigned place = (slot + 2 * (unsigned)(j - j0) + 1) % kRing;
       if (!wait_all(&bars->raw_full[place], raw_uses >> place & 1)) return false;
       raw_uses ^= 1u << place;
       uint8_t* buf = ring + (size_t)place * kTileBytes;
-      const int held = min(kTile, it.len - j * kTile);                    // rows of the sequence
-      const int c0 = max(0, it.tok0 + 1 - j * kTile) * 8, c1 = held * 8;  // in pieces of 16 bytes
+      const int held = min(kTile, keys - j * kTile);                                     // rows of the sequence
+      const int c0 = max(0, past_of(it) + it.tok0 + 1 - j * kTile) * 8, c1 = held * 8;  // in pieces of 16 bytes
       const bool clean = all_finite(smem_u32(buf), c0, c1, lane);
       if (!clean) {
         for (int c = c0 + lane; c < c1; c += 32)
@@ -426,7 +646,24 @@ __device__ __noinline__ bool schedule(Bars* bars, uint8_t* ring, int sequences, 
   };
   // An item's tiles are looked over when the next item is out, so that the producer need not wait for it.
   for (int k = 0;; ++k) {
-    const Item it = sch.item(k, heads);
+    It it;
+    if constexpr (std::is_same_v<It, Item>) {
+      it = sch.item(k, heads);
+    } else {
+      int last;
+      it = sch.next(&last);
+      if (it.row0 >= 0 && !it.whole) {
+        tail.tiles[it.j0 == 0] = make_int2(it.j0, it.j1);
+        if (last >= 0) {
+          tail.row0 = it.row0;
+          tail.len = it.len;
+          tail.tok0 = it.tok0;
+          tail.h = it.h;
+          tail.past = it.past;
+          tail.last = last;
+        }
+      }
+    }
     const int st = k % kItems;
     if (!wait_all(&bars->item_empty[st], ((k / kItems) & 1) ^ 1)) {
       ok = false;
@@ -443,19 +680,26 @@ __device__ __noinline__ bool schedule(Bars* bars, uint8_t* ring, int sequences, 
     }
     if (it.row0 < 0) break;
   }
-  set_err(err, sch.bits);
+  if constexpr (std::is_same_v<It, Item>) {
+    set_err(err, sch.bits);
+  } else {
+    if (blockIdx.x == 0) set_err(err, sch.bits);
+    if (lane == 0) parts.tails[blockIdx.x] = tail;
+  }
   return ok;
 }
 
+// It: Item, or Piece where keys lie before the new rows (row_start: of the query rows, parts: the rest).
+template <class It>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, PagedShape s, const uint16_t* v, size_t v_stride,
                    const int* row_start, int n_rows, float scale_log2, uint16_t* out, size_t out_stride,
-                   unsigned* err) {
+                   Parts parts, unsigned* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * kTileBytes;
-  Bars* bars = reinterpret_cast<Bars*>(ring + kRing * (size_t)kTileBytes);
+  Bars<It>* bars = reinterpret_cast<Bars<It>*>(ring + kRing * (size_t)kTileBytes);
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = s.Hq / s.Hkv, per = kTile / G;  // per: tokens of a query tile
@@ -498,7 +742,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   bool timed_out = false;
 
   // Item k of this block, for the warps that consume items: false at the end or on a time-out.
-  auto take = [&](int k, Item& it) {
+  auto take = [&](int k, It& it) {
     const int st = k % kItems;
     const bool ok = mbar_wait(&bars->item_full[st], (k / kItems) & 1, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) {
@@ -526,11 +770,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int g = row % G, tok_in = row / G;
     const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
     unsigned turn = 0, outputs = 0;
-    Item it;
+    It it;
     for (int k = 0; take(k, it); ++k) {
       const int n = kv_tiles(it, i, per);
       if (n == 0) continue;
       const int t0 = it.tok0 + i * per, tok = t0 + tok_in;
+      const int past = past_of(it) - first_tile(it) * kTile;  // keys before the first query row, from this part's first one
       float ref = 0.f;
       uint64_t sum_a = 0, sum_b = 0;
       for (int j = 0; j < n; ++j, ++turn) {
@@ -545,8 +790,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tmem_ld32(s_addr + 64, x + 64);
         tmem_ld32(s_addr + 96, x + 96);
         tmem_wait_ld();
-        if (j * kTile + kTile - 1 > t0 || (j + 1) * kTile > it.len) {  // keys in the future or behind the sequence
-          const int last = min(tok, it.len - 1) - j * kTile;
+        if (j * kTile + kTile - 1 > past + t0 || (j + 1) * kTile > past + it.len) {  // in the future or behind the sequence
+          const int last = past + min(tok, it.len - 1) - j * kTile;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > last) x[c] = 0xff800000u;
@@ -616,6 +861,25 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       unpack2(sum_a, a, b);
       unpack2(sum_b, d, e);
       const float total = (a + b) + (d + e);
+      if constexpr (std::is_same_v<It, Piece>) {
+        if (!it.whole) {
+          const size_t at = parts.row(blockIdx.x, it.j0 == 0, i * kTile + row);
+          const bool mine = row < per * G && tok < it.len;
+          if (mine) parts.stats[at] = make_float2(ref, total);
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+            if (mine) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) store32(parts.o + at * kD + c + q, o + q);
+            }
+          }
+          tc_fence_before();
+          continue;
+        }
+      }
       const float inv = 1.0f / total;  // every row has a key; no finite score at all gives NaN
       const bool live = row < per * G && tok < it.len;
       uint16_t* dst = out + (size_t)(it.row0 + (live ? tok : 0)) * out_stride + (size_t)(it.h * G + g) * kD;
@@ -690,7 +954,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       for (int k = 0;; ++k) {
         const int st = k % kItems;
         if (!ready(&bars->item_full[st], (k / kItems) & 1)) break;
-        const Item it = bars->items[st];
+        const It it = bars->items[st];
         mbar_arrive(&bars->item_empty[st]);
         if (it.row0 < 0) break;
         const int ni = kv_tiles(it, i, per), n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
@@ -751,13 +1015,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
     }
     const uint32_t q_bytes = 2u * 128u * (uint32_t)(per * G);
-    Item it;
+    It it;
     for (int k = 0; take(k, it) && !timed_out; ++k) {
+      const int j0 = first_tile(it);
       const int n = max(kv_tiles(it, 0, per), kv_tiles(it, 1, per));
       for (int j = 0; j < n && !timed_out; ++j) {
         for (int part = 0; part < 2 && !timed_out; ++part, ++slot) {  // K_j, V_j
           const bool q_here = j == 0 && kv_tiles(it, part, per) > 0;   // Q_0 before K_0, Q_1 before V_0
-          const bool raw = part == 1 && j >= first_masked(it);         // to be looked over before it is full
+          const bool raw = part == 1 && j0 + j >= first_masked(it);         // to be looked over before it is full
           const unsigned place = slot % kRing;
           uint8_t* buf = ring + (size_t)place * kTileBytes;
           bool ok = true;
@@ -776,8 +1041,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
               uint64_t* bar = raw ? &bars->raw_full[place] : &bars->kv_full[place];
               const CUtensorMap* map = part ? &map_v : &map_k;
               mbar_expect_tx(bar, kTileBytes);
-              tma_load_3d(buf, map, 0, it.h, it.row0 + j * kTile, bar);
-              tma_load_3d(buf + kHalf, map, 64, it.h, it.row0 + j * kTile, bar);
+              tma_load_3d(buf, map, 0, it.h, kv_row(it) + (j0 + j) * kTile, bar);
+              tma_load_3d(buf + kHalf, map, 64, it.h, kv_row(it) + (j0 + j) * kTile, bar);
             }
           }
           if (q_here) ++q_uses[part];
@@ -800,7 +1065,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     }
     __syncwarp();
   } else if (warp == 10) {
-    timed_out = !schedule(bars, ring, s.B, s.Hkv, per, row_start, n_rows, err);
+    timed_out = !schedule<It>(bars, ring, s.B, s.Hkv, per, row_start, n_rows, parts, err);
   }
 
   if (timed_out) {
@@ -811,8 +1076,46 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   __syncthreads();
   tc_fence_after();
   if (warp < 8 && bars->cleaned)  // the block's outputs are written
-    give_back(s.B, s.Hkv, G, row_start, n_rows, v, v_stride, out, out_stride);
+    give_back<It>(s.B, s.Hkv, G, row_start, n_rows, v, v_stride, out, out_stride, parts);
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+constexpr int kJoinWarps = 8, kJoinBlocks = 8;
+
+// Joins the parts of the item that goes on behind block blockIdx.x: a row to a warp, four dimensions to a lane.
+__global__ void __launch_bounds__(kJoinWarps * 32)
+prompt_join_kernel(PagedShape s, Parts parts, uint16_t* out, size_t out_stride) {
+  wait_for_predecessor();  // the parts are written
+  const Tail tail = parts.tails[blockIdx.x];
+  if (tail.last < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x;
+  const int G = s.Hq / s.Hkv, per = kTile / G, blocks = min(tail.last, (int)gridDim.x - 1) - first + 1;
+  for (int r = blockIdx.y * kJoinWarps + warp; r < 2 * kTile; r += kJoinBlocks * kJoinWarps) {
+    const int i = r / kTile, in = r % kTile, tok = tail.tok0 + i * per + in / G;
+    if (in >= per * G || tok >= tail.len) continue;
+    const Item it{tail.row0, tail.len, tail.tok0, tail.h};
+    Piece whole = {};
+    static_cast<Item&>(whole) = it;
+    whole.past = tail.past;
+    const int tiles = tiles_of(whole, i, per);
+    float top = neg_inf(), sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = 0; c < blocks; ++c) {
+      const int2 part = parts.tails[first + c].tiles[c == 0];
+      if (min(part.y, tiles) <= part.x) continue;  // none of this row's
+      const size_t at = parts.row(first + c, c == 0, r);
+      const float2 st = parts.stats[at];
+      const float4 x = reinterpret_cast<const float4*>(parts.o + at * kD)[lane];
+      const float next = fmaxf(top, st.x), f0 = ex2(top - next), f1 = ex2(st.x - next);
+      o = make_float4(fmaf(o.x, f0, x.x * f1), fmaf(o.y, f0, x.y * f1), fmaf(o.z, f0, x.z * f1), fmaf(o.w, f0, x.w * f1));
+      sum = fmaf(sum, f0, st.y * f1);
+      top = next;
+    }
+    const float inv = 1.0f / sum;
+    *reinterpret_cast<uint2*>(out + (size_t)(tail.row0 + tok) * out_stride + (size_t)(tail.h * G + in % G) * kD + lane * 4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
 }
 
 bool rows_map(CUtensorMap* m, const uint16_t* p, int heads, int n_rows, size_t stride, int box_heads, int box_rows) {
@@ -827,35 +1130,84 @@ bool rows_map(CUtensorMap* m, const uint16_t* p, int heads, int n_rows, size_t s
 
 }  // namespace
 
-cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint16_t* k,
-                               size_t k_stride, const uint16_t* v, size_t v_stride, const int* row_start, int n_rows,
-                               float scale, uint16_t* out, size_t out_stride, unsigned* err, cudaStream_t stream) {
-  if (n_rows == 0) return cudaSuccess;
-  if (!encode_fn()) return cudaErrorNotSupported;
+namespace {
+
+template <class It>
+cudaError_t launch_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint16_t* k, size_t k_stride,
+                        const uint16_t* v, size_t v_stride, const int* row_start, int n_rows, int n_kv_rows, float scale,
+                        uint16_t* out, size_t out_stride, const Parts& parts, int grid, unsigned* err, cudaStream_t stream) {
   const int G = s.G(), per = kTile / G;
   CUtensorMap mq, mk, mv;
-  if (!rows_map(&mq, q, s.Hq, n_rows, q_stride, G, per) || !rows_map(&mk, k, s.Hkv, n_rows, k_stride, 1, kTile) ||
-      !rows_map(&mv, v, s.Hkv, n_rows, v_stride, 1, kTile))
+  if (!rows_map(&mq, q, s.Hq, n_rows, q_stride, G, per) || !rows_map(&mk, k, s.Hkv, n_kv_rows, k_stride, 1, kTile) ||
+      !rows_map(&mv, v, s.Hkv, n_kv_rows, v_stride, 1, kTile))
     return cudaErrorInvalidValue;
-  // items of all sequences: at most one partly filled one for each
-  const long long items = ((long long)n_rows / (2 * per) + (s.B < n_rows ? s.B : n_rows)) * s.Hkv;
-  const int sms = sm_count();
-  const int grid = items < sms ? (int)items : sms;
   static int attr_cache[kMaxDevicesCached] = {};
-  cudaError_t e = ensure_dyn_smem((const void*)prompt_attn_kernel, kSmemBytes, attr_cache);
+  cudaError_t e = ensure_dyn_smem((const void*)prompt_attn_kernel<It>, kSmemBytes<It>, attr_cache);
   if (e != cudaSuccess) return e;
   // the roles' register split draws on what the kernel is launched with: a build with fewer would wait for ever
   static int launch_regs[kMaxDevicesCached] = {};
   int& regs = launch_regs[current_device()];
   if (!regs) {
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, prompt_attn_kernel);
+    e = cudaFuncGetAttributes(&fa, prompt_attn_kernel<It>);
     if (e != cudaSuccess) return e;
     regs = fa.numRegs;
   }
   if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_chained(prompt_attn_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, 1, mq, mk, mv, s, v, v_stride,
-                        row_start, n_rows, scale * 1.4426950408889634f, out, out_stride, err);
+  return launch_chained(prompt_attn_kernel<It>, dim3(grid), dim3(kThreads), kSmemBytes<It>, stream, 1, mq, mk, mv, s, v,
+                        v_stride, row_start, n_rows, scale * 1.4426950408889634f, out, out_stride, parts, err);
+}
+
+Parts parts_of(void* ws, const int* kv_start, int n_kv_rows) {
+  const size_t rows = (size_t)sm_count() * 2 * (2 * kTile);
+  Parts p;
+  p.kv_start = kv_start;
+  p.n_kv_rows = n_kv_rows;
+  p.o = static_cast<float*>(ws);
+  p.stats = reinterpret_cast<float2*>(p.o + rows * kD);
+  p.tails = reinterpret_cast<Tail*>(p.stats + rows);
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint16_t* k,
+                               size_t k_stride, const uint16_t* v, size_t v_stride, const int* row_start, int n_rows,
+                               float scale, uint16_t* out, size_t out_stride, unsigned* err, cudaStream_t stream) {
+  if (n_rows == 0) return cudaSuccess;
+  if (!encode_fn()) return cudaErrorNotSupported;
+  // items of all sequences: at most one partly filled one for each
+  const long long items = ((long long)n_rows / (2 * (kTile / s.G())) + (s.B < n_rows ? s.B : n_rows)) * s.Hkv;
+  const int sms = sm_count();
+  return launch_attn<Item>(s, q, q_stride, k, k_stride, v, v_stride, row_start, n_rows, n_rows, scale, out, out_stride, Parts{},
+                           items < sms ? (int)items : sms, err, stream);
+}
+
+size_t resume_workspace_bytes() {
+  const size_t blocks = (size_t)sm_count();
+  return blocks * (2 * (2 * kTile) * (kD * sizeof(float) + sizeof(float2)) + sizeof(Tail));
+}
+
+cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint16_t* k, size_t k_stride,
+                               const uint16_t* v, size_t v_stride, const int* q_start, int n_rows, const int* kv_start,
+                               int n_kv_rows, float scale, void* ws, uint16_t* out, size_t out_stride, unsigned* err,
+                               cudaStream_t stream) {
+  if (n_rows == 0 || n_kv_rows == 0) return cudaSuccess;
+  if (!encode_fn()) return cudaErrorNotSupported;
+  // blocks that the largest cost of these sizes can use: every item with all keys
+  const int pair = 2 * (kTile / s.G());
+  const long long items = ((long long)n_rows / pair + (s.B < n_rows ? s.B : n_rows)) * s.Hkv;
+  const long long most = (items * (Ranges::kItemCost + (long long)n_kv_rows + pair) + Ranges::kLeast - 1) / Ranges::kLeast;
+  const int sms = sm_count(), grid = most < sms ? (int)most : sms;
+  const Parts parts = parts_of(ws, kv_start, n_kv_rows);
+  // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
+  static std::mutex both[kMaxDevicesCached];
+  std::lock_guard<std::mutex> lock(both[current_device()]);
+  cudaError_t e = launch_attn<Piece>(s, q, q_stride, k, k_stride, v, v_stride, q_start, n_rows, n_kv_rows, scale, out, out_stride,
+                                     parts, grid, err, stream);
+  if (e != cudaSuccess || grid == 1) return e;
+  return launch_chained(prompt_join_kernel, dim3(grid, kJoinBlocks), dim3(kJoinWarps * 32), 0, stream, 1, s, parts, out,
+                        out_stride);
 }
 
 }  // namespace oasis

@@ -1,4 +1,4 @@
-"""A KV cache in 8-bit pages: tables, store, decode attention, and the prompt's attention.
+"""A KV cache in 8-bit or 4-bit pages: tables, store, decode attention, read-back, and the prompts' attention.
 
 PyTorch owns the memory and the streams; every step runs in liboasis.so through
 :mod:`binding`.  One :class:`PagedKV` serves a model of several layers whose requests
@@ -6,6 +6,9 @@ share the tables:
 
   kv     uint8   [layers][n_pages][Hkv][2][16][128]   e4m3 keys, values
   scale  float32 [layers][n_pages][Hkv][2]            powers of two
+  with bits=4:
+  kv     uint8   [layers][n_pages][Hkv][2][16][64]    e2m1 keys, values, two to a byte
+  scale  uint8   [layers][n_pages][Hkv][2][128]       for 16 dimensions of a token
   table  int32   [batch][nb_max]                      page of each request's blocks
   free   int32   [n_pages]                            free pages, the first n_free of them
   lens   int32   [batch]                              tokens that each request holds
@@ -24,9 +27,16 @@ A prompt's pass, layer by layer, and a decode step::
     out = cache.decode(q, plan.lens, layer)            # sel, nsel: only the selected blocks
     cache.commit(plan)
 
+A prompt that continues a context attends what its request holds as well as itself::
+
+    plan = cache.extend(cache.lens + more, n_rows)     # held: at least the tokens held in all
+    out = cache.resume(q, k, v, plan, held, layer)     # before commit
+    cache.store(k, v, plan.slot_map, layer)
+    cache.commit(plan)
+
 Calls run on the current stream of the tensors' device and can be captured into a CUDA
 graph; nothing is kept between calls but the tensors above and decode's scratch, one for
-each stream (calls on one stream follow each other, those of several host threads as well:
+each stream (resume takes its own from PyTorch's memory at each call; calls on one stream follow each other, those of several host threads as well:
 the library keeps a call's launches together).  A captured call takes scratch of its
 own from the graph's memory pool, so graphs, and calls on other streams, never share it.
 
@@ -48,6 +58,14 @@ D = 128
 BS = 16
 _SCALE = 1.0 / math.sqrt(D)
 _BF16, _INT32 = torch.bfloat16, torch.int32
+
+
+class Rows(NamedTuple):
+    """What :meth:`PagedKV.read` gives: request b's tokens are rows row_start[b] .. row_start[b+1] - 1."""
+
+    k: torch.Tensor          # bfloat16 [n_rows][Hkv][128]
+    v: torch.Tensor
+    row_start: torch.Tensor  # int32 [batch + 1]
 
 
 class Plan(NamedTuple):
@@ -94,6 +112,14 @@ def _prompt_shape(sequences: int, hq: int, hkv: int):
     return ctypes.byref(B.PagedShape(sequences, hq, hkv, D, BS, 1, 1))
 
 
+@functools.lru_cache(maxsize=256)
+def _resume_bytes(sequences: int, hq: int, hkv: int, index: int) -> int:
+    n = (B._lib or B.load()).oasis_resume_attn_workspace_bytes(_prompt_shape(sequences, hq, hkv))
+    if not n:
+        raise B.OasisError("oasis_resume_attn_workspace_bytes", 1, B.oasis_last_error())
+    return n
+
+
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                 err: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -127,9 +153,49 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: to
     return out
 
 
+def resume_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, kv_start: torch.Tensor,
+                scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                err: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of new rows that continue a context: q [rows, Hq, 128] in rows q_start[b] ..
+    q_start[b+1] - 1 for sequence b, k and v [kv_rows, Hkv, 128] in rows kv_start[b] .. kv_start[b+1] - 1, its
+    earlier tokens first and then one for each of its query rows (bf16; slices of one buffer as well).
+    Rows of no sequence are left as they are in out (zero where out is allocated here).
+
+    Errors (bad starts, fewer rows of keys than of queries, a wait inside the kernel that gave up) go
+    to err and nowhere else; :meth:`PagedKV.resume` passes the cache's."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [rows, heads, 128]")
+    n, hq, m, hkv, device = q.shape[0], q.shape[1], k.shape[0], k.shape[1], q.device
+    index = _cuda(device)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return resume_attn(q, k, v, q_start, kv_start, scale, out, err)
+    qs, ks, vs = _rows("q", q, hq, n, device), _rows("k", k, hkv, m, device), _rows("v", v, hkv, m, device)
+    sequences = q_start.numel() - 1
+    if sequences < 1:
+        raise ValueError("q_start must be int32 [sequences + 1]")
+    _ints("q_start", q_start, (sequences + 1,), device)
+    _ints("kv_start", kv_start, (sequences + 1,), device)
+    if out is None:
+        out = torch.zeros((n, hq, D), dtype=_BF16, device=device)
+    shape = _prompt_shape(sequences, hq, hkv)
+    ws_bytes = _resume_bytes(sequences, hq, hkv, index)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    st = (B._lib or B.load()).oasis_resume_attn(
+        shape, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, q_start.data_ptr(), n, kv_start.data_ptr(), m,
+        _SCALE if scale is None else scale, ws.data_ptr(), ws_bytes, out.data_ptr(), _rows("out", out, hq, n, device),
+        None if err is None else _ints("err", err, (1,), device).data_ptr(), _current_stream(index))
+    if st:
+        B._check("oasis_resume_attn", st)
+    return out
+
+
 class PagedKV:
     def __init__(self, n_pages: int, batch: int, nb_max: int, n_q_heads: int, n_kv_heads: int, layers: int = 1,
-                 device="cuda"):
+                 device="cuda", bits: int = 8):
+        if bits not in (4, 8):
+            raise ValueError(f"pages hold 4 or 8 bits, not {bits}")
+        self.bits = bits
         self.shape = B.PagedShape.of(batch, n_q_heads, n_kv_heads, nb_max, n_pages)
         self.ws_bytes = B.oasis_paged_attn_workspace_bytes(self.shape)  # also checks the shape
         if not self.ws_bytes:
@@ -138,8 +204,11 @@ class PagedKV:
             raise ValueError("layers must be >= 1")
         self.batch, self.n_q_heads, self.n_kv_heads, self.layers = batch, n_q_heads, n_kv_heads, layers
         # not initialised: positions that were never stored are never read
-        self.kv = torch.empty((layers, n_pages, n_kv_heads, 2, BS, D), dtype=torch.uint8, device=device)
-        self.scale = torch.ones((layers, n_pages, n_kv_heads, 2), dtype=torch.float32, device=device)
+        self.kv = torch.empty((layers, n_pages, n_kv_heads, 2, BS, D * bits // 8), dtype=torch.uint8, device=device)
+        if bits == 8:
+            self.scale = torch.ones((layers, n_pages, n_kv_heads, 2), dtype=torch.float32, device=device)
+        else:
+            self.scale = torch.zeros((layers, n_pages, n_kv_heads, 2, BS * D // 16), dtype=torch.uint8, device=device)
         self.table = torch.full((batch, nb_max), -1, dtype=torch.int32, device=device)
         self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 is taken first
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)
@@ -148,7 +217,7 @@ class PagedKV:
         self.device = self.kv.device
         self._index = _cuda(self.device)
         self._shape = ctypes.byref(self.shape)
-        self._kv_bytes, self._scale_bytes = self.kv.stride(0), 4 * self.scale.stride(0)  # of a layer
+        self._kv_bytes, self._scale_bytes = self.kv.stride(0), self.scale.element_size() * self.scale.stride(0)  # of a layer
         self._scratch = {}  # decode's, by stream
 
     def adopt(self, **tensors: torch.Tensor) -> None:
@@ -207,7 +276,8 @@ class PagedKV:
     def prompt(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Plan, scale: Optional[float] = None,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """:func:`prompt_attn` over a plan's rows; :meth:`check` raises its errors.  For plans whose
-        new rows are all of requests that held nothing before: earlier tokens are not attended."""
+        new rows are all of requests that held nothing before: earlier tokens are not attended (:meth:`resume`
+        attends them)."""
         if q.dim() != 3 or q.shape[1] != self.n_q_heads or k.dim() != 3 or k.shape[1] != self.n_kv_heads:
             raise ValueError(f"q must be [rows, {self.n_q_heads}, 128], k and v [rows, {self.n_kv_heads}, 128]")
         return prompt_attn(q, k, v, plan.row_start, scale, out, self.err)
@@ -222,12 +292,13 @@ class PagedKV:
         _ints("slot_map", slot_map, (n,), device)
         if not 0 <= layer < self.layers:
             raise ValueError(f"layer {layer} of {self.layers}")
-        st = (B._lib or B.load()).oasis_store_kv_q8(
+        lib = B._lib or B.load()
+        st = (lib.oasis_store_kv_q8 if self.bits == 8 else lib.oasis_store_kv_q4)(
             self._shape, k.data_ptr(), ks, v.data_ptr(), vs, slot_map.data_ptr(), n,
             self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
             self.err.data_ptr(), _current_stream(self._index))
         if st:
-            B._check("oasis_store_kv_q8", st)
+            B._check(f"oasis_store_kv_q{self.bits}", st)
 
     def decode(self, q: torch.Tensor, ctx_len: Optional[torch.Tensor] = None, layer: int = 0,
                sel: Optional[torch.Tensor] = None, nsel: Optional[torch.Tensor] = None,
@@ -260,14 +331,75 @@ class PagedKV:
             ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
             if not capturing:
                 self._scratch[stream] = ws
-        st = (B._lib or B.load()).oasis_paged_decode_attn_q8(
+        lib = B._lib or B.load()
+        st = (lib.oasis_paged_decode_attn_q8 if self.bits == 8 else lib.oasis_paged_decode_attn_q4)(
             self._shape, q.data_ptr(), stride, self.kv.data_ptr() + layer * self._kv_bytes,
             self.scale.data_ptr() + layer * self._scale_bytes, self.table.data_ptr(), ctx_len.data_ptr(), sel_at, nsel_at,
             most, _SCALE if scale is None else scale, ws.data_ptr(), self.ws_bytes, out.data_ptr(), self.err.data_ptr(),
             stream)
         if st:
-            B._check("oasis_paged_decode_attn_q8", st)
+            B._check(f"oasis_paged_decode_attn_q{self.bits}", st)
         return out
+
+    def read(self, n_rows: int, ctx_len: Optional[torch.Tensor] = None, layer: int = 0, new=None, out=None) -> Rows:
+        """The first ctx_len tokens of every request (lens by default) as packed bf16 rows, at most n_rows
+        of them; stored values are bf16 exactly.  new = (k, v, row_start) puts the rows row_start[b] ..
+        row_start[b+1] - 1 of k and v [rows, Hkv, 128] behind request b's.  out = (k, v): contiguous bf16
+        [n_rows, Hkv, 128] to write to; rows behind the last request's are left as they are."""
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.read(n_rows, ctx_len, layer, new, out)
+        b, h, device = self.batch, self.n_kv_heads, self.device
+        ctx_len = _ints("ctx_len", self.lens if ctx_len is None else ctx_len, (b,), device)
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of {self.layers}")
+        if n_rows < 0:
+            raise ValueError("n_rows must be >= 0")
+        k_at = v_at = ks = vs = n_new = 0
+        start_at = None
+        if new is not None:
+            k, v, row_start = new
+            if k.dim() != 3:
+                raise ValueError("new rows must be [rows, heads, 128]")
+            n_new = k.shape[0]
+            ks, vs = _rows("k", k, h, n_new, device), _rows("v", v, h, n_new, device)
+            k_at, v_at = k.data_ptr(), v.data_ptr()
+            start_at = _ints("row_start", row_start, (b + 1,), device).data_ptr()
+        if out is None:
+            out = (torch.empty((n_rows, h, D), dtype=_BF16, device=device), torch.empty((n_rows, h, D), dtype=_BF16, device=device))
+        else:
+            for t in out:
+                if t.dtype is not _BF16 or t.shape != (n_rows, h, D) or t.device != device or not t.is_contiguous():
+                    raise ValueError(f"out must be two contiguous bfloat16 [{n_rows}, {h}, {D}] on {device}")
+        kv_start = torch.empty(b + 1, dtype=_INT32, device=device)
+        lib = B._lib or B.load()
+        st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
+            self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
+            self.table.data_ptr(), ctx_len.data_ptr(), k_at, ks, v_at, vs, start_at, n_new, kv_start.data_ptr(),
+            out[0].data_ptr(), out[1].data_ptr(), n_rows, self.err.data_ptr(), _current_stream(self._index))
+        if st:
+            B._check(f"oasis_read_kv_q{self.bits}", st)
+        return Rows(out[0], out[1], kv_start)
+
+    def resume(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: Plan, n_held: int, layer: int = 0,
+               scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Causal attention of a plan's rows over what their requests hold (lens, before the plan's commit) and
+        over each other: q [rows, Hq, 128], k and v [rows, Hkv, 128] in bf16.  n_held: at least the tokens
+        that the requests hold in all, which sizes the scratch (a request that does not fit is reported to
+        :meth:`check` and its rows stay as they are).  Rows of no request stay as they are in out (zero where
+        out is allocated here).  The held tokens are read back from the pages (:meth:`read`), the new ones
+        are taken as given; whether they are stored before or after makes no difference."""
+        if _current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.resume(q, k, v, plan, n_held, layer, scale, out)
+        if q.dim() != 3 or q.shape[1] != self.n_q_heads or k.dim() != 3 or k.shape[1] != self.n_kv_heads:
+            raise ValueError(f"q must be [rows, {self.n_q_heads}, 128], k and v [rows, {self.n_kv_heads}, 128]")
+        if q.shape[0] != k.shape[0]:
+            raise ValueError("q, k and v must have the same rows")
+        if n_held < 0:
+            raise ValueError("n_held must be >= 0")
+        rows = self.read(n_held + k.shape[0], None, layer, (k, v, plan.row_start))
+        return resume_attn(q, rows.k, rows.v, plan.row_start, rows.row_start, scale, out, self.err)
 
     def check(self) -> None:
         """Waits for the device (every stream) and raises if a kernel reported an error; clears the word."""

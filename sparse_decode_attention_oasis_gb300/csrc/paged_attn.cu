@@ -54,6 +54,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPages = 8;  // pages a thread block gets at least, when there are so few
+constexpr int kPairGap = 2;   // 4 bits: what a pair costs a warp beside its pages, in pages
 constexpr int kJoinWarps = 4;
 constexpr int kMaxG = 8;
 constexpr int kRowFloats = kD + 2;
@@ -155,43 +156,52 @@ __device__ __forceinline__ void load_values(Rows& v, const uint8_t* page, int la
   v.v[3] = load16_stream(p + 9 * kD);
 }
 
-// The same in 4 bits, with their scales.  A lane's 16 dimensions of a value row are one group, its 32 of a key row two.
-struct Keys4 {  // rows lane / 4 and + 8, dimensions 32 (lane % 4) ..
-  uint4 v[2];
-  uint32_t scale[2];
-  __device__ __forceinline__ void load(const uint8_t* page, const uint8_t* scales, int lane) {
-    const uint8_t* p = page + (lane >> 2) * (kD / 2) + (lane & 3) * 16;
-    v[0] = load16_stream(p);
-    v[1] = load16_stream(p + 8 * (kD / 2));
-    const uint8_t* s = scales + (lane >> 2) * kGroups + (lane & 3) * 2;
-    scale[0] = load2_stream(s);
-    scale[1] = load2_stream(s + 8 * kGroups);
-  }
-};
-struct Values4 {  // tokens 2 (lane % 4), + 1, + 8, + 9, dimensions 16 (lane / 4) ..
-  uint2 v[4];
-  uint32_t scale[2];
-  __device__ __forceinline__ void load(const uint8_t* page, const uint8_t* scales, int lane) {
-    const uint8_t* p = page + kBS * (kD / 2) + (lane & 3) * kD + (lane >> 2) * 8;
-    v[0] = load8_stream(p);
-    v[1] = load8_stream(p + kD / 2);
-    v[2] = load8_stream(p + 8 * (kD / 2));
-    v[3] = load8_stream(p + 9 * (kD / 2));
-    const uint8_t* s = scales + kBS * kGroups + (lane >> 2) * kBS + (lane & 3) * 2;
-    scale[0] = load2_stream(s);
-    scale[1] = load2_stream(s + 8);
-  }
-};
+// Pages in 4 bits pass through a ring of kStages places in shared memory for each warp: codes of keys, of values, scales.
+// A place's value rows are kept in lines of two tokens whose 16-byte pieces are exchanged (xor 2 (line & 3)), so that
+// the lanes' 8-byte reads of four lines at a time meet in no bank.
+constexpr int kStages = 4;
+constexpr int kStageBytes = (int)(kHeadPageBytes4 + kHeadScaleBytes4);
 
-// S^T += K Q^T of a page in 4 bits: a step of the product takes 4 of the lane's 32 dimensions (step m: 4m ..).
-__device__ __forceinline__ void scores4(float* sc, const Keys4& k, const uint32_t* qf) {
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
+  if constexpr (kBytes == 16)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+  else if constexpr (kBytes == 8)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else
+    asm volatile("{\n .reg .u16 h;\n ld.shared.u16 h, [%1];\n cvt.u32.u16 %0, h;\n}" : "=r"(w[0]) : "r"(at));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {  // results below 2^-126 become zero
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// S^T += K Q^T of a page in 4 bits.  A lane has keys lane / 4 and + 8, dimensions 32 (lane % 4) .., two groups of each;
+// a step of the product takes 4 of them (step m: 4m ..).
+__device__ __forceinline__ void scores4(float* sc, uint32_t place, int lane, const uint32_t* qf) {
+  uint32_t k0[4], k1[4], s0, s1;
+  lds<16>(place + lane * 16, k0);
+  lds<16>(place + lane * 16 + 8 * (kD / 2), k1);
+  const uint32_t s = place + (uint32_t)kHeadPageBytes4 + lane * 2;
+  lds<2>(s, &s0);
+  lds<2>(s + 8 * kGroups, &s1);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {  // a group of 16 dimensions
-    const uint32_t f0 = half ? scale_twice<1>(k.scale[0]) : scale_twice<0>(k.scale[0]);
-    const uint32_t f1 = half ? scale_twice<1>(k.scale[1]) : scale_twice<0>(k.scale[1]);
+    const uint32_t f0 = half ? scale_twice<1>(s0) : scale_twice<0>(s0);
+    const uint32_t f1 = half ? scale_twice<1>(s1) : scale_twice<0>(s1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = word(k.v[0], 2 * half + i), hi = word(k.v[1], 2 * half + i);
+      const uint32_t lo = k0[2 * half + i], hi = k1[2 * half + i];
       const int m = 4 * half + 2 * i;
       mma_f16_16816(sc, mul_f16x2(e2m1x2_to_f16x2<0>(lo), f0), mul_f16x2(e2m1x2_to_f16x2<0>(hi), f1),
                     mul_f16x2(e2m1x2_to_f16x2<1>(lo), f0), mul_f16x2(e2m1x2_to_f16x2<1>(hi), f1), qf[2 * m], qf[2 * m + 1]);
@@ -202,16 +212,33 @@ __device__ __forceinline__ void scores4(float* sc, const Keys4& k, const uint32_
   }
 }
 
-// O^T += V^T W^T of a page in 4 bits: bytes of a token's row hold two dimensions, the product takes pairs of tokens, so
-// the codes of two rows are exchanged (lo: the even dimensions of both, hi: the odd ones) before they become halves.
-__device__ __forceinline__ void outputs4(float (*acc)[4], const Values4& v, uint32_t b0, uint32_t b1) {
-  const uint32_t f0 = scale_pair(v.scale[0]), f1 = scale_pair(v.scale[1]);
+// O^T += V^T W^T of a page in 4 bits.  A lane has tokens 2 (lane % 4), + 1, + 8, + 9, dimensions 16 (lane / 4) .., a group.
+// Bytes of a token's row hold two dimensions, the product takes pairs of tokens, so the codes of two rows are exchanged
+// (lo: the even dimensions of both, hi: the odd ones) before they become halves.  valid: tokens of the page; what lies
+// behind them may be NaN, and zero times that is not zero: codes are finite, so it is their scales that become zero.
+__device__ __forceinline__ void outputs4(float (*acc)[4], uint32_t place, int lane, int valid, uint32_t b0, uint32_t b1) {
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t line = place + kBS * (kD / 2) + c * kD + ((g * 8) ^ (c * 32));
+  uint32_t t0[2], t1[2], t8[2], t9[2], s0, s1;
+  lds<8>(line, t0);
+  lds<8>(place + kBS * (kD / 2) + c * kD + ((kD / 2 + g * 8) ^ (c * 32)), t1);
+  lds<8>(line + 4 * kD, t8);
+  lds<8>(place + kBS * (kD / 2) + c * kD + ((kD / 2 + g * 8) ^ (c * 32)) + 4 * kD, t9);
+  const uint32_t s = place + (uint32_t)kHeadPageBytes4 + kBS * kGroups + g * kBS + c * 2;
+  lds<2>(s, &s0);
+  lds<2>(s + 8, &s1);
+  if (valid < kBS) {
+    const int t = c * 2;
+    s0 &= t >= valid ? 0u : t + 1 >= valid ? 0xffu : 0xffffu;
+    s1 &= t + 8 >= valid ? 0u : t + 9 >= valid ? 0xffu : 0xffffu;
+  }
+  const uint32_t f0 = scale_pair(s0), f1 = scale_pair(s1);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t t0 = i ? v.v[0].y : v.v[0].x, t1 = i ? v.v[1].y : v.v[1].x;
-    const uint32_t t8 = i ? v.v[2].y : v.v[2].x, t9 = i ? v.v[3].y : v.v[3].x;
-    const uint32_t lo0 = (t0 & 0x0f0f0f0fu) | (t1 << 4 & 0xf0f0f0f0u), hi0 = (t0 >> 4 & 0x0f0f0f0fu) | (t1 & 0xf0f0f0f0u);
-    const uint32_t lo1 = (t8 & 0x0f0f0f0fu) | (t9 << 4 & 0xf0f0f0f0u), hi1 = (t8 >> 4 & 0x0f0f0f0fu) | (t9 & 0xf0f0f0f0u);
+    const uint32_t lo0 = (t0[i] & 0x0f0f0f0fu) | (t1[i] << 4 & 0xf0f0f0f0u);
+    const uint32_t hi0 = (t0[i] >> 4 & 0x0f0f0f0fu) | (t1[i] & 0xf0f0f0f0u);
+    const uint32_t lo1 = (t8[i] & 0x0f0f0f0fu) | (t9[i] << 4 & 0xf0f0f0f0u);
+    const uint32_t hi1 = (t8[i] >> 4 & 0x0f0f0f0fu) | (t9[i] & 0xf0f0f0f0u);
     mma_f16_16816(acc[4 * i], mul_f16x2(e2m1x2_to_f16x2<0>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<0>(hi0), f0),
                   mul_f16x2(e2m1x2_to_f16x2<0>(lo1), f1), mul_f16x2(e2m1x2_to_f16x2<0>(hi1), f1), b0, b1);
     mma_f16_16816(acc[4 * i + 1], mul_f16x2(e2m1x2_to_f16x2<1>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<1>(hi0), f0),
@@ -221,6 +248,57 @@ __device__ __forceinline__ void outputs4(float (*acc)[4], const Values4& v, uint
     mma_f16_16816(acc[4 * i + 3], mul_f16x2(e2m1x2_to_f16x2<3>(lo0), f0), mul_f16x2(e2m1x2_to_f16x2<3>(hi0), f0),
                   mul_f16x2(e2m1x2_to_f16x2<3>(lo1), f1), mul_f16x2(e2m1x2_to_f16x2<3>(hi1), f1), b0, b1);
   }
+}
+
+// Scores of tokens behind a page's last one.
+__device__ __forceinline__ void mask4(float* sc, int valid, int lane) {
+  const int g = lane >> 2;
+  if (g >= valid) sc[0] = sc[1] = neg_inf();
+  if (g + 8 >= valid) sc[2] = sc[3] = neg_inf();
+}
+
+// Two pages in 4 bits into the running state (two chains of products, one look at the maxima).  v0, v1: their tokens, 0
+// where there is no page: what its place holds then weighs nothing.  top: M, kLowest before the first page (scores
+// of -inf alone leave it there).
+__device__ __forceinline__ void attend4(uint32_t place, int v0, int v1, const uint32_t* qf, const float* f, int lane, State& st,
+                                        float* top) {
+  float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+  scores4(a, place, lane, qf);
+  scores4(b, place + kStageBytes, lane, qf);
+  if (v0 + v1 < 2 * kBS) {
+    mask4(a, v0, lane);
+    mask4(b, v1, lane);
+  }
+  float m0 = fmaxf(fmaxf(a[0], a[2]), fmaxf(b[0], b[2])) * f[0], m1 = fmaxf(fmaxf(a[1], a[3]), fmaxf(b[1], b[3])) * f[1];
+  if (__any_sync(0xffffffffu, m0 > top[0] + kMostBits || m1 > top[1] + kMostBits)) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+      m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    }
+    const float n0 = fmaxf(top[0], m0 - kLift), n1 = fmaxf(top[1], m1 - kLift);
+    const float c0 = exp2_fast(top[0] - n0), c1 = exp2_fast(top[1] - n1);  // 0 for the first page
+    top[0] = n0;
+    top[1] = n1;
+    st.sum[0] *= c0;
+    st.sum[1] *= c1;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      st.acc[m][0] *= c0;
+      st.acc[m][1] *= c1;
+      st.acc[m][2] *= c0;
+      st.acc[m][3] *= c1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = exp2_fast(fmaf(a[i], f[i & 1], -top[i & 1]));
+    b[i] = exp2_fast(fmaf(b[i], f[i & 1], -top[i & 1]));
+  }
+  st.sum[0] += (a[0] + a[2]) + (b[0] + b[2]);
+  st.sum[1] += (a[1] + a[3]) + (b[1] + b[3]);
+  outputs4(st.acc, place, lane, v0, transpose_8x8(pack_f16x2(a[0], a[1])), transpose_8x8(pack_f16x2(a[2], a[3])));
+  outputs4(st.acc, place + kStageBytes, lane, v1, transpose_8x8(pack_f16x2(b[0], b[1])), transpose_8x8(pack_f16x2(b[2], b[3])));
 }
 
 struct Shared {
@@ -246,17 +324,27 @@ __device__ __forceinline__ float2 load_remote(const float* mine, unsigned rank) 
 template <bool kClustered, int kBits>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_decode_attn_kernel(PagedShape s, Args a) {
-  extern __shared__ __align__(16) float slot_rows[];  // [2 * kWarps][G][kD], then (kClustered) [G][kRowFloats]
+  // 8 bits: rows of slots [2 * kWarps][G][kD], then (kClustered) of the block's piece [G][kRowFloats].
+  // 4 bits: rows of every second slot [kWarps][G][kD], then each warp's ring; the other slot of a warp is written when its
+  // ring is done with and takes its beginning, the block's piece the end of the first one.
+  extern __shared__ __align__(16) float slot_rows[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = s.Hq / s.Hkv;
+  auto ring_of = [&](int w) { return reinterpret_cast<uint8_t*>(slot_rows + (size_t)kWarps * G * kD) + w * kStages * kStageBytes; };
+  auto slot_at = [&](int slot) {
+    if constexpr (kBits == 8) return slot_rows + (size_t)slot * G * kD;
+    return slot & 1 ? reinterpret_cast<float*>(ring_of(slot >> 1)) : slot_rows + (size_t)(slot >> 1) * G * kD;
+  };
   wait_for_predecessor();
   const int pairs = s.B * s.Hkv;
   const int per = (pairs + kThreads - 1) / kThreads;
   const int team = a.team, rank = blockIdx.x % team;  // kClustered: blocks to a pair, this one's place
   unsigned bits = 0;
   int blocks = 1;
-  long long total = 0, c_lo, c_hi;  // pages of all pairs (of this one), this block's range
+  // Before each pair's pages lies a gap: a warp with many short pairs spends its time on their tables and first pages.
+  constexpr int kGap = kBits == 4 && !kClustered ? kPairGap : 0;
+  long long total = 0, c_lo, c_hi;  // pages (and gaps) of all pairs (of this one), this block's range
 
   if constexpr (kClustered) {
     const int e = blockIdx.x / team;
@@ -277,7 +365,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     long long n = 0;
     for (int e = min(tid * per, pairs); e < min((tid + 1) * per, pairs); ++e) {
       const int c = pair_pages(s, a, e, &bits);
-      n += c;
+      n += c > 0 ? c + kGap : 0;
       if (c == 0 && e % (int)gridDim.x == (int)blockIdx.x)
         for (int i = 0; i < G * kD / 8; ++i)
           reinterpret_cast<uint4*>(a.out + (long long)e * G * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -324,236 +412,273 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     // with one pair to a chunk the prefix holds its pages
     auto pages_of = [&](int pair) {
       if (kClustered) return (int)total;
-      return per == 1 ? (int)(sh.chunk_start[pair + 1] - sh.chunk_start[pair]) : pair_pages(s, a, pair, &bits);
+      return per == 1 ? max((int)(sh.chunk_start[pair + 1] - sh.chunk_start[pair]) - kGap, 0) : pair_pages(s, a, pair, &bits);
     };
+    auto span = [&](int pages) { return pages > 0 ? pages + kGap : 0; };
     int count = pages_of(e);
-    while (e_lo + count <= w_lo) {
-      e_lo += count;
+    while (e_lo + span(count) <= w_lo) {
+      e_lo += span(count);
       count = pages_of(++e);
     }
-    long long p = w_lo;
     while (true) {
-      const int b = e / s.Hkv, h = e - b * s.Hkv;
-      const int ctx = (int)min((long long)max(a.ctx_len[b], 0), (long long)s.nb_max * kBS);
-      const int nb = (ctx + kBS - 1) / kBS;
-      const int first = (int)(p - e_lo), last = (int)min((long long)count, w_hi - e_lo);  // pages of the pair
+      const long long p_lo = e_lo + kGap;  // the pair's first page
+      const int first = (int)max(w_lo - p_lo, 0ll), last = (int)min((long long)count, w_hi - p_lo);  // pages of the pair
+      if (first < last) {
+        const int b = e / s.Hkv, h = e - b * s.Hkv;
+        const int ctx = (int)min((long long)max(a.ctx_len[b], 0), (long long)s.nb_max * kBS);
+        const int nb = (ctx + kBS - 1) / kBS;
 
-      // ---- the query row lane / 4, dimensions as for the keys
-      uint32_t qf[16];
-      float fac[2];
-      {
-        uint4 w[4];
+        // ---- the query row lane / 4, dimensions as for the keys
+        uint32_t qf[16];
+        float fac[2];
+        {
+          uint4 w[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
-        if ((lane >> 2) < G) {
-          constexpr int kPiece = kBits == 8 ? 16 : 32, kNext = kBits == 8 ? 64 : 16;
-          const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * kPiece;
-          w[0] = load16(src);
-          w[1] = load16(src + 8);
-          w[2] = load16(src + kNext);
-          w[3] = load16(src + kNext + 8);
-        }
-        uint32_t m = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t v = word(w[c], d) & 0x7fff7fffu;
-            m = max(m, max(v & 0xffffu, v >> 16));
+          for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
+          if ((lane >> 2) < G) {
+            constexpr int kPiece = kBits == 8 ? 16 : 32, kNext = kBits == 8 ? 64 : 16;
+            const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * kPiece;
+            w[0] = load16(src);
+            w[1] = load16(src + 8);
+            w[2] = load16(src + kNext);
+            w[3] = load16(src + kNext + 8);
           }
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int ex = max((int)(m >> 7) - 127, -112);  // exponent of the row's largest value
-        const float f = pow2f(14 - ex);
+          uint32_t m = 0;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t v = word(w[c >> 2], c & 3);
-          qf[c] = pack_f16x2(bf_lo(v) * f, bf_hi(v) * f);
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t v = word(w[c], d) & 0x7fff7fffu;
+              m = max(m, max(v & 0xffffu, v >> 16));
+            }
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          const int ex = max((int)(m >> 7) - 127, -112);  // exponent of the row's largest value
+          const float f = pow2f(14 - ex);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t v = word(w[c >> 2], c & 3);
+            qf[c] = pack_f16x2(bf_lo(v) * f, bf_hi(v) * f);
+          }
+          const float mine = a.scale_log2 * pow2f(ex - 14);
+          fac[0] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8);
+          fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
         }
-        const float mine = a.scale_log2 * pow2f(ex - 14);
-        fac[0] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8);
-        fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
-      }
 
-      std::conditional_t<kBits == 8, Rows, Keys4> kr;
-      std::conditional_t<kBits == 8, Rows, Values4> vr;
-      int my_page = -1, my_valid = 0;  // of page (group of 32) + lane
-      float2 my_scale = make_float2(1.f, 1.f);
-      const long long head_stride = kBits == 8 ? kHeadPageBytes : kHeadPageBytes4;
-      auto lookup = [&](int at) {  // tables of pages at .. at + 31
-        my_page = -1;
-        my_valid = 0;
-        const int idx = at + lane;
-        if (idx < last) {
-          int blk = idx;
-          if (a.sel != nullptr) {
-            blk = a.sel[(long long)e * a.sel_max + idx];
-            if (blk < 0 || blk >= nb) {
-              blk = -1;
-              bits |= OASIS_EW_BAD_BLOCK;
+        int my_page = -1, my_valid = 0;  // of page (group of 32) + lane
+        float2 my_scale = make_float2(1.f, 1.f);
+        auto lookup = [&](int at) {  // tables of pages at .. at + 31
+          my_page = -1;
+          my_valid = 0;
+          const int idx = at + lane;
+          if (idx < last) {
+            int blk = idx;
+            if (a.sel != nullptr) {
+              blk = a.sel[(long long)e * a.sel_max + idx];
+              if (blk < 0 || blk >= nb) {
+                blk = -1;
+                bits |= OASIS_EW_BAD_BLOCK;
+              }
+            }
+            if (blk >= 0) {
+              const int pg = a.table[(long long)b * s.nb_max + blk];
+              if (pg >= 0 && pg < s.n_pages) {
+                my_page = pg;
+                my_valid = min(kBS, ctx - blk * kBS);
+                if constexpr (kBits == 8)
+                  my_scale = *reinterpret_cast<const float2*>(static_cast<const float*>(a.scales) + ((long long)pg * s.Hkv + h) * 2);
+              } else {
+                bits |= OASIS_EW_BAD_SLOT;
+              }
             }
           }
-          if (blk >= 0) {
-            const int pg = a.table[(long long)b * s.nb_max + blk];
-            if (pg >= 0 && pg < s.n_pages) {
-              my_page = pg;
-              my_valid = min(kBS, ctx - blk * kBS);
-              if constexpr (kBits == 8)
-                my_scale = *reinterpret_cast<const float2*>(static_cast<const float*>(a.scales) + ((long long)pg * s.Hkv + h) * 2);
-            } else {
-              bits |= OASIS_EW_BAD_SLOT;
-            }
-          }
-        }
-      };
-      auto head_page = [&](int page) { return a.pages + ((long long)page * s.Hkv + h) * head_stride; };
-      auto head_scales = [&](int page) {
-        return static_cast<const uint8_t*>(a.scales) + ((long long)page * s.Hkv + h) * kHeadScaleBytes4;
-      };
-      auto fetch_keys = [&](int page) {
-        if constexpr (kBits == 8) load_keys(kr, head_page(page), lane);
-        else kr.load(head_page(page), head_scales(page), lane);
-      };
-      auto fetch_values = [&](int page) {
-        if constexpr (kBits == 8) load_values(vr, head_page(page), lane);
-        else vr.load(head_page(page), head_scales(page), lane);
-      };
-
-      lookup(first);
-      int page = __shfl_sync(0xffffffffu, my_page, 0);
-      if (page >= 0) {
-        fetch_keys(page);
-        fetch_values(page);
-      }
-      State st;
-      st.clear();
-      for (int at = first; at < last; ++at) {
-        const int in = (at - first) & 31;
-        const int valid = __shfl_sync(0xffffffffu, my_valid, in);
-        float ks = 1.f, vs = 1.f;
+        };
+        State st;
+        st.clear();
         if constexpr (kBits == 8) {
-          ks = __shfl_sync(0xffffffffu, my_scale.x, in);
-          vs = __shfl_sync(0xffffffffu, my_scale.y, in);
-        }
-        const bool here = page >= 0;
-        if (in == 31) lookup(at + 1);
-        page = at + 1 < last ? __shfl_sync(0xffffffffu, my_page, (at + 1 - first) & 31) : -1;
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
-        if (here) {
-          if constexpr (kBits == 8) {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              const uint32_t lo = word(kr.v[m >> 2], m & 3), hi = word(kr.v[2 + (m >> 2)], m & 3);
-              mma_f16_16816(sc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_hi_to_f16x2(lo),
-                            e4m3x2_hi_to_f16x2(hi), qf[2 * m], qf[2 * m + 1]);
-            }
-          } else {
-            scores4(sc, kr, qf);
+          Rows kr, vr;
+          const long long head_stride = kHeadPageBytes;
+          auto head_page = [&](int page) { return a.pages + ((long long)page * s.Hkv + h) * head_stride; };
+          lookup(first);
+          int page = __shfl_sync(0xffffffffu, my_page, 0);
+          if (page >= 0) {
+            load_keys(kr, head_page(page), lane);
+            load_values(vr, head_page(page), lane);
           }
-        }
-        if (page >= 0) fetch_keys(page);
-        if (here) {
-          const int g = lane >> 2;
-          const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 0xff) - 127);  // 4 bits: 0
-          const float f0 = fac[0] * ks, f1 = fac[1] * ks;
-          float s0 = fmaf(sc[0], f0, lv), s1 = fmaf(sc[1], f1, lv);
-          float s2 = fmaf(sc[2], f0, lv), s3 = fmaf(sc[3], f1, lv);
-          if (valid < kBS) {
-            if (g >= valid) s0 = s1 = neg_inf();
-            if (g + 8 >= valid) s2 = s3 = neg_inf();
-            // what lies behind the last token may be NaN: zero times it is not zero
-            const int t = (lane & 3) * 2;
-            if constexpr (kBits == 8) {
-              if (t >= valid) vr.v[0] = make_uint4(0u, 0u, 0u, 0u);
-              if (t + 1 >= valid) vr.v[1] = make_uint4(0u, 0u, 0u, 0u);
-              if (t + 8 >= valid) vr.v[2] = make_uint4(0u, 0u, 0u, 0u);
-              if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
-            } else {  // codes are finite, scales may not be
-              vr.scale[0] &= t >= valid ? 0u : t + 1 >= valid ? 0xffu : 0xffffu;
-              vr.scale[1] &= t + 8 >= valid ? 0u : t + 9 >= valid ? 0xffu : 0xffffu;
+          for (int at = first; at < last; ++at) {
+            const int in = (at - first) & 31;
+            const int valid = __shfl_sync(0xffffffffu, my_valid, in);
+            const float ks = __shfl_sync(0xffffffffu, my_scale.x, in), vs = __shfl_sync(0xffffffffu, my_scale.y, in);
+            const bool here = page >= 0;
+            if (in == 31) lookup(at + 1);
+            page = at + 1 < last ? __shfl_sync(0xffffffffu, my_page, (at + 1 - first) & 31) : -1;
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            if (here) {
+#pragma unroll
+              for (int m = 0; m < 8; ++m) {
+                const uint32_t lo = word(kr.v[m >> 2], m & 3), hi = word(kr.v[2 + (m >> 2)], m & 3);
+                mma_f16_16816(sc, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi), e4m3x2_hi_to_f16x2(lo),
+                              e4m3x2_hi_to_f16x2(hi), qf[2 * m], qf[2 * m + 1]);
+              }
             }
-          }
-          float m0 = fmaxf(fmaxf(s0, s2), kLowest), m1 = fmaxf(fmaxf(s1, s3), kLowest);
-          if (__any_sync(0xffffffffu, m0 > st.top[0] + kMostBits || m1 > st.top[1] + kMostBits)) {
+            if (page >= 0) load_keys(kr, head_page(page), lane);
+            if (here) {
+              const int g = lane >> 2;
+              const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 0xff) - 127);
+              const float f0 = fac[0] * ks, f1 = fac[1] * ks;
+              float s0 = fmaf(sc[0], f0, lv), s1 = fmaf(sc[1], f1, lv);
+              float s2 = fmaf(sc[2], f0, lv), s3 = fmaf(sc[3], f1, lv);
+              if (valid < kBS) {
+                if (g >= valid) s0 = s1 = neg_inf();
+                if (g + 8 >= valid) s2 = s3 = neg_inf();
+                // what lies behind the last token may be NaN: zero times it is not zero
+                const int t = (lane & 3) * 2;
+                if (t >= valid) vr.v[0] = make_uint4(0u, 0u, 0u, 0u);
+                if (t + 1 >= valid) vr.v[1] = make_uint4(0u, 0u, 0u, 0u);
+                if (t + 8 >= valid) vr.v[2] = make_uint4(0u, 0u, 0u, 0u);
+                if (t + 9 >= valid) vr.v[3] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              float m0 = fmaxf(fmaxf(s0, s2), kLowest), m1 = fmaxf(fmaxf(s1, s3), kLowest);
+              if (__any_sync(0xffffffffu, m0 > st.top[0] + kMostBits || m1 > st.top[1] + kMostBits)) {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-              m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                for (int o = 4; o < 32; o <<= 1) {
+                  m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                  m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                }
+                const float n0 = fmaxf(st.top[0], m0 - kLift), n1 = fmaxf(st.top[1], m1 - kLift);
+                const float c0 = exp2f(st.top[0] - n0), c1 = exp2f(st.top[1] - n1);  // 0 for the first page
+                st.top[0] = n0;
+                st.top[1] = n1;
+                st.sum[0] *= c0;
+                st.sum[1] *= c1;
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                  st.acc[m][0] *= c0;
+                  st.acc[m][1] *= c1;
+                  st.acc[m][2] *= c0;
+                  st.acc[m][3] *= c1;
+                }
+              }
+              const float w0 = exp2f(s0 - st.top[0]), w1 = exp2f(s1 - st.top[1]);
+              const float w2 = exp2f(s2 - st.top[0]), w3 = exp2f(s3 - st.top[1]);
+              const float iv = pow2f(-(int)lv);
+              st.sum[0] = fmaf(w0 + w2, iv, st.sum[0]);
+              st.sum[1] = fmaf(w1 + w3, iv, st.sum[1]);
+              const uint32_t b0 = transpose_8x8(pack_f16x2(w0, w1)), b1 = transpose_8x8(pack_f16x2(w2, w3));
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const uint32_t t0 = word(vr.v[0], m), t1 = word(vr.v[1], m), t8 = word(vr.v[2], m), t9 = word(vr.v[3], m);
+                const uint32_t p0 = __byte_perm(t0, t1, 0x5140), p1 = __byte_perm(t8, t9, 0x5140);
+                const uint32_t p2 = __byte_perm(t0, t1, 0x7362), p3 = __byte_perm(t8, t9, 0x7362);
+                mma_f16_16816(st.acc[2 * m], e4m3x2_to_f16x2(p0), e4m3x2_hi_to_f16x2(p0), e4m3x2_to_f16x2(p1),
+                              e4m3x2_hi_to_f16x2(p1), b0, b1);
+                mma_f16_16816(st.acc[2 * m + 1], e4m3x2_to_f16x2(p2), e4m3x2_hi_to_f16x2(p2), e4m3x2_to_f16x2(p3),
+                              e4m3x2_hi_to_f16x2(p3), b0, b1);
+              }
             }
-            const float n0 = fmaxf(st.top[0], m0 - kLift), n1 = fmaxf(st.top[1], m1 - kLift);
-            const float c0 = exp2f(st.top[0] - n0), c1 = exp2f(st.top[1] - n1);  // 0 for the first page
-            st.top[0] = n0;
-            st.top[1] = n1;
-            st.sum[0] *= c0;
-            st.sum[1] *= c1;
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              st.acc[m][0] *= c0;
-              st.acc[m][1] *= c1;
-              st.acc[m][2] *= c0;
-              st.acc[m][3] *= c1;
-            }
+            if (page >= 0) load_values(vr, head_page(page), lane);
           }
-          const float w0 = exp2f(s0 - st.top[0]), w1 = exp2f(s1 - st.top[1]);
-          const float w2 = exp2f(s2 - st.top[0]), w3 = exp2f(s3 - st.top[1]);
-          const float iv = pow2f(-(int)lv);
-          st.sum[0] = fmaf(w0 + w2, iv, st.sum[0]);
-          st.sum[1] = fmaf(w1 + w3, iv, st.sum[1]);
-          const uint32_t b0 = transpose_8x8(pack_f16x2(w0, w1)), b1 = transpose_8x8(pack_f16x2(w2, w3));
-          if constexpr (kBits == 4) outputs4(st.acc, vr, b0, b1);
-          else
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t t0 = word(vr.v[0], m), t1 = word(vr.v[1], m), t8 = word(vr.v[2], m), t9 = word(vr.v[3], m);
-            const uint32_t p0 = __byte_perm(t0, t1, 0x5140), p1 = __byte_perm(t8, t9, 0x5140);
-            const uint32_t p2 = __byte_perm(t0, t1, 0x7362), p3 = __byte_perm(t8, t9, 0x7362);
-            mma_f16_16816(st.acc[2 * m], e4m3x2_to_f16x2(p0), e4m3x2_hi_to_f16x2(p0), e4m3x2_to_f16x2(p1),
-                          e4m3x2_hi_to_f16x2(p1), b0, b1);
-            mma_f16_16816(st.acc[2 * m + 1], e4m3x2_to_f16x2(p2), e4m3x2_hi_to_f16x2(p2), e4m3x2_to_f16x2(p3),
-                          e4m3x2_hi_to_f16x2(p3), b0, b1);
-          }
-        }
-        if (page >= 0) fetch_values(page);
-      }
-
-      // ---- the pair's piece: the output if it is all of it, else a slot
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        st.sum[0] += __shfl_xor_sync(0xffffffffu, st.sum[0], o);
-        st.sum[1] += __shfl_xor_sync(0xffffffffu, st.sum[1], o);
-      }
-      const bool whole = first == 0 && last == count && !(kClustered && team > 1);
-      const int which = first == 0 ? 1 : 0, slot = warp * 2 + which;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = (lane & 3) * 2 + i;
-        if (r >= G) continue;
-        if (whole) {
-          const float inv = inverse(st.top[i], st.sum[i]);
-          uint32_t w[8];
-#pragma unroll
-          for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(st.acc[m][i] * inv, st.acc[m][2 + i] * inv);
-          uint4* dst = reinterpret_cast<uint4*>(a.out + ((long long)e * G + r) * kD + (lane >> 2) * 16);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-          float* row = slot_rows + ((size_t)slot * G + r) * kD + (lane >> 2) * 16;
+          // Two pages at a time, the next two on their way: half as many bytes each as in 8 bits.
+          const uint8_t* const codes = a.pages + (long long)h * kHeadPageBytes4 + lane * 16;
+          const uint8_t* const scales = static_cast<const uint8_t*>(a.scales) + (long long)h * kHeadScaleBytes4 + (lane & 15) * 16;
+          const long long page_bytes = s.Hkv * kHeadPageBytes4, scale_bytes = s.Hkv * kHeadScaleBytes4;
+          const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_of(warp));
+          const uint32_t value_at = kBS * (kD / 2) + (lane >> 3) * kD + ((lane & 7) ^ (lane >> 3) << 1) * 16;
+          // a page and its tokens in one word (page * 32 + tokens, -32: none): of page (group of 32) + lane
+          int ahead = -32;
+          auto fetch = [&](int at, uint32_t place) {  // pages at and at + 1: their tokens, 16 bits each
+            int tokens = 0;
+            if (at < last) {
+              const int in = (at - first) & 31;
+              if (in == 0) {
+                lookup(at);
+                ahead = my_page * 32 + my_valid;
+              }
+              const int w0 = __shfl_sync(0xffffffffu, ahead, in), w1 = __shfl_sync(0xffffffffu, ahead, in + 1);
+              if (w0 >= 0) {
+                const uint8_t* from = codes + (w0 >> 5) * page_bytes;
+                copy16(place + lane * 16, from);
+                copy16(place + lane * 16 + 512, from + 512);
+                copy16(place + value_at, from + 1024);
+                copy16(place + value_at + 512, from + 1536);
+              }
+              if (w1 >= 0) {
+                const uint8_t* from = codes + (w1 >> 5) * page_bytes;
+                copy16(place + kStageBytes + lane * 16, from);
+                copy16(place + kStageBytes + lane * 16 + 512, from + 512);
+                copy16(place + kStageBytes + value_at, from + 1024);
+                copy16(place + kStageBytes + value_at + 512, from + 1536);
+              }
+              const int mine = lane < 16 ? w0 : w1;  // the first 16 lanes copy the first one's scales
+              if (mine >= 0)
+                copy16(place + (lane < 16 ? 0 : kStageBytes) + (uint32_t)kHeadPageBytes4 + (lane & 15) * 16,
+                       scales + (mine >> 5) * scale_bytes);
+              tokens = (w0 & 31) | (w1 & 31) << 16;
+            }
+            copy_commit();
+            return tokens;
+          };
+          // a score's factor stays normal, so that it leaves an infinity one
+          const float f[2] = {fmaxf(fac[0], 1.1754944e-38f), fmaxf(fac[1], 1.1754944e-38f)};
+          float top[2] = {kLowest, kLowest};
+          int seen = 0, tokens = fetch(first, ring), next = fetch(first + 2, ring + 2 * kStageBytes);
+          uint32_t place = ring;
+          for (int at = first; at < last; at += 2) {
+            copy_wait<1>();
+            __syncwarp();  // the pages have landed for all lanes
+            seen |= tokens;
+            attend4(place, tokens & 31, tokens >> 16, qf, f, lane, st, top);
+            __syncwarp();  // all lanes are done with them
+            tokens = next;
+            next = fetch(at + 4, place);
+            place = place == ring ? ring + 2 * kStageBytes : ring;
+          }
+          copy_wait<0>();
+          if (seen) {
+            st.top[0] = top[0];
+            st.top[1] = top[1];
+          }
+        }
+
+        // ---- the pair's piece: the output if it is all of it, else a slot
 #pragma unroll
-          for (int m = 0; m < 8; m += 2)
-            *reinterpret_cast<float4*>(row + 2 * m) =
-                make_float4(st.acc[m][i], st.acc[m][2 + i], st.acc[m + 1][i], st.acc[m + 1][2 + i]);
-          if (lane < 4) sh.top_sum[slot][r] = make_float2(st.top[i], st.sum[i]);
+        for (int o = 4; o < 32; o <<= 1) {
+          st.sum[0] += __shfl_xor_sync(0xffffffffu, st.sum[0], o);
+          st.sum[1] += __shfl_xor_sync(0xffffffffu, st.sum[1], o);
+        }
+        const bool whole = first == 0 && last == count && !(kClustered && team > 1);
+        const int which = first == 0 ? 1 : 0, slot = warp * 2 + which;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = (lane & 3) * 2 + i;
+          if (r >= G) continue;
+          if (whole) {
+            const float inv = inverse(st.top[i], st.sum[i]);
+            uint32_t w[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) w[m] = pack_bf16x2(st.acc[m][i] * inv, st.acc[m][2 + i] * inv);
+            uint4* dst = reinterpret_cast<uint4*>(a.out + ((long long)e * G + r) * kD + (lane >> 2) * 16);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else {
+            float* row = slot_at(slot) + (size_t)r * kD + (lane >> 2) * 16;
+#pragma unroll
+            for (int m = 0; m < 8; m += 2)
+              *reinterpret_cast<float4*>(row + 2 * m) =
+                  make_float4(st.acc[m][i], st.acc[m][2 + i], st.acc[m + 1][i], st.acc[m + 1][2 + i]);
+            if (lane < 4) sh.top_sum[slot][r] = make_float2(st.top[i], st.sum[i]);
+          }
+        }
+        if (!whole && lane == 0) {
+          sh.slot_pair[slot] = e;
+          sh.slot_lo[slot] = p_lo;
+          sh.slot_hi[slot] = p_lo + count;
         }
       }
-      if (!whole && lane == 0) {
-        sh.slot_pair[slot] = e;
-        sh.slot_lo[slot] = e_lo;
-        sh.slot_hi[slot] = e_lo + count;
-      }
-      p = e_lo + last;
-      if (p >= w_hi) break;
+      if (p_lo + count >= w_hi) break;
       do {
-        e_lo += count;
+        e_lo += span(count);
         count = pages_of(++e);
       } while (count == 0);
     }
@@ -575,7 +700,9 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
       tail = make_int2(sh.slot_pair[lead], (int)((e_hi * blocks + total - 1) / total - 1));
   }
   if (!kClustered && tid == 0) a.tails[blockIdx.x] = tail;
-  float* piece = slot_rows + (size_t)2 * kWarps * G * kD;  // kClustered: this block's rows
+  // kClustered: this block's rows
+  float* piece = kBits == 8 ? slot_rows + (size_t)2 * kWarps * G * kD
+                            : reinterpret_cast<float*>(ring_of(0)) + (size_t)kMaxG * kD;
   for (int u = warp; u < units; u += kWarps) {
     const int lead = __fns(leads, 0, u / G + 1), r = u % G;
     const unsigned mask = __shfl_sync(0xffffffffu, same, lead);
@@ -587,7 +714,7 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     for (unsigned left = mask; left; left &= left - 1) {
       const int j = __ffs(left) - 1;
       const float fj = __shfl_sync(0xffffffffu, f, j);
-      const float4 v = reinterpret_cast<const float4*>(slot_rows + ((size_t)j * G + r) * kD)[lane];
+      const float4 v = reinterpret_cast<const float4*>(slot_at(j) + (size_t)r * kD)[lane];
       o.x = fmaf(fj, v.x, o.x);
       o.y = fmaf(fj, v.y, o.y);
       o.z = fmaf(fj, v.z, o.z);
@@ -709,7 +836,9 @@ cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_strid
   float* parts = static_cast<float*>(ws);
   Args a{q, q_stride, pages, scales, table, ctx, sel, nsel, sel_max, 1, scale * 1.4426950408889634f, parts,
          reinterpret_cast<int2*>(parts + (size_t)most * 2 * s.G() * kRowFloats), out, err};
-  const size_t smem = (size_t)2 * kWarps * s.G() * kD * sizeof(float);
+  static_assert(kMaxG * (kD + kRowFloats) * sizeof(float) <= kStages * kStageBytes, "a slot and the piece fit in a ring");
+  const size_t slots = (size_t)kWarps * s.G() * kD * sizeof(float);
+  const size_t smem = kBits == 8 ? 2 * slots : slots + (size_t)kWarps * kStages * kStageBytes;
   const long long pairs = (long long)s.B * s.Hkv;
   const int pair_max = sel ? sel_max : s.nb_max;
   // A cluster for each pair needs no prefix over the pairs, no workspace and no second kernel, but leaves blocks
@@ -721,7 +850,7 @@ cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_strid
   while (a.team < 8 && pairs * a.team * 2 <= most && pair_max > kMinPages * a.team) a.team *= 2;
   const int team_pages = pairs * a.team * 3 >= most * 2LL ? 128 : 56;  // two thirds of the GPU's places filled, or fewer
   if (pairs * a.team <= most && pair_max <= team_pages * a.team) {
-    const size_t with_piece = smem + (size_t)s.G() * kRowFloats * sizeof(float);
+    const size_t with_piece = kBits == 8 ? smem + (size_t)s.G() * kRowFloats * sizeof(float) : smem;
     static int attr_cache[kMaxDevicesCached] = {};
     cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<true, kBits>, with_piece, attr_cache);
     if (e != cudaSuccess) return e;

@@ -399,7 +399,7 @@ struct Schedule {
 // past + the keys of the item's last row (whole tiles of rows) + kItemCost for its ends.  A sequence's items follow
 // each other head by head; an item that crosses a range's border is cut at a tile there (not one tile from its ends).
 struct Ranges {
-  static constexpr long long kItemCost = 192, kLeast = 512;  // least cost of a block's range
+  static constexpr long long kItemCost = 336, kLeast = 512;  // least cost of a block's range
   const int *q_start, *kv_start;
   int B, n_rows, n_kv_rows, pair, per, heads, lane;
   unsigned bits;
@@ -441,10 +441,12 @@ struct Ranges {
     heads = hkv;
     lane = ln;
     bits = 0;
-    long long total = 0;
+    long long total = 0, of_first = 0;  // of_first: sequence `lane`
     for (int s = lane; s < B; s += 32) {
       int qa, n, ka, before;
-      if (sequence(s, qa, n, ka, before)) total += heads * head_cost(n, before);
+      const long long c = sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0;
+      total += c;
+      if (s == lane) of_first = c;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -461,10 +463,14 @@ struct Ranges {
     start = 0;
     for (int w = 0;; w += 32) {
       const int s = w + lane;
-      int qa, n, ka, before;
-      const unsigned keep = bits;  // reported by the pass above
-      long long c = s < B && sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0, x = c;
-      bits = keep;
+      long long c = of_first;
+      if (w > 0) {
+        int qa, n, ka, before;
+        const unsigned keep = bits;  // reported by the pass above
+        c = s < B && sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0;
+        bits = keep;
+      }
+      long long x = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -1080,41 +1086,126 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
-constexpr int kJoinWarps = 8, kJoinBlocks = 8;
+constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinPerSm = 3;
+constexpr int kMostBlocks = kJoinThreads;  // thread blocks whose parts a join can take
 
-// Joins the parts of the item that goes on behind block blockIdx.x: a row to a warp, four dimensions to a lane.
-__global__ void __launch_bounds__(kJoinWarps * 32)
-prompt_join_kernel(PagedShape s, Parts parts, uint16_t* out, size_t out_stride) {
-  wait_for_predecessor();  // the parts are written
-  const Tail tail = parts.tails[blockIdx.x];
-  if (tail.last < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x;
-  const int G = s.Hq / s.Hkv, per = kTile / G, blocks = min(tail.last, (int)gridDim.x - 1) - first + 1;
-  for (int r = blockIdx.y * kJoinWarps + warp; r < 2 * kTile; r += kJoinBlocks * kJoinWarps) {
-    const int i = r / kTile, in = r % kTile, tok = tail.tok0 + i * per + in / G;
-    if (in >= per * G || tok >= tail.len) continue;
-    const Item it{tail.row0, tail.len, tail.tok0, tail.h};
-    Piece whole = {};
-    static_cast<Item&>(whole) = it;
-    whole.past = tail.past;
-    const int tiles = tiles_of(whole, i, per);
-    float top = neg_inf(), sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = 0; c < blocks; ++c) {
-      const int2 part = parts.tails[first + c].tiles[c == 0];
-      if (min(part.y, tiles) <= part.x) continue;  // none of this row's
-      const size_t at = parts.row(first + c, c == 0, r);
-      const float2 st = parts.stats[at];
-      const float4 x = reinterpret_cast<const float4*>(parts.o + at * kD)[lane];
-      const float next = fmaxf(top, st.x), f0 = ex2(top - next), f1 = ex2(st.x - next);
-      o = make_float4(fmaf(o.x, f0, x.x * f1), fmaf(o.y, f0, x.y * f1), fmaf(o.z, f0, x.z * f1), fmaf(o.w, f0, x.w * f1));
-      sum = fmaf(sum, f0, st.y * f1);
-      top = next;
+__device__ __forceinline__ float2 load8(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load16f(const float* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// kRows rows of an item to a warp, from `row` on, `step` apart: a lane has four dimensions.  tails: from the item's first block.
+template <int kRows>
+__device__ __forceinline__ void join_rows(const Parts& parts, const Tail* tails, int first, int row, int step, int rows, int count,
+                                          int per, int G, uint16_t* out, size_t out_stride) {
+  const int lane = threadIdx.x & 31;
+  const Tail& tail = tails[0];
+  float top[kRows], sum[kRows];
+  float4 o[kRows];
+  int r[kRows], tiles[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int at = min(row + k * step, rows - 1), i = at / G / per;  // behind the last row: that again
+    Piece item = {};
+    item.len = tail.len;
+    item.tok0 = tail.tok0;
+    item.past = tail.past;
+    r[k] = at + i * (kTile - per * G);
+    tiles[k] = tiles_of(item, i, per);
+    top[k] = neg_inf();
+    sum[k] = 0.f;
+    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  constexpr int kAtOnce = 8 / kRows;  // parts whose loads are in flight together
+  for (int c0 = 0; c0 < count; c0 += kAtOnce) {
+    float2 st[kAtOnce][kRows];
+    float4 x[kAtOnce][kRows];
+#pragma unroll
+    for (int d = 0; d < kAtOnce; ++d) {
+      const int c = min(c0 + d, count - 1);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const size_t at = parts.row(first + c, c == 0, r[k]);
+        st[d][k] = load8(parts.stats + at);
+        x[d][k] = load16f(parts.o + at * kD + lane * 4);
+      }
     }
-    const float inv = 1.0f / sum;
-    *reinterpret_cast<uint2*>(out + (size_t)(tail.row0 + tok) * out_stride + (size_t)(tail.h * G + in % G) * kD + lane * 4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+#pragma unroll
+    for (int d = 0; d < kAtOnce; ++d) {
+      const int c = min(c0 + d, count - 1);
+      const int2 part = tails[c].tiles[c == 0];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (c0 + d >= count || min(part.y, tiles[k]) <= part.x) continue;  // no part, or one without tiles of this row
+        const float next = fmaxf(top[k], st[d][k].x), f0 = ex2(top[k] - next), f1 = ex2(st[d][k].x - next);
+        o[k] = make_float4(fmaf(o[k].x, f0, x[d][k].x * f1), fmaf(o[k].y, f0, x[d][k].y * f1),
+                           fmaf(o[k].z, f0, x[d][k].z * f1), fmaf(o[k].w, f0, x[d][k].w * f1));
+        sum[k] = fmaf(sum[k], f0, st[d][k].y * f1);
+        top[k] = next;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int at = row + k * step;
+    if (at >= rows) continue;
+    const float inv = 1.0f / sum[k];
+    *reinterpret_cast<uint2*>(out + (size_t)(tail.row0 + tail.tok0 + at / G) * out_stride +
+                              (size_t)(tail.h * G + at % G) * kD + lane * 4) =
+        make_uint2(pack_bf16x2(o[k].x * inv, o[k].y * inv), pack_bf16x2(o[k].z * inv, o[k].w * inv));
+  }
+}
+
+// Joins the parts of items that go on in a later block.  Every thread block lists the items (a tail to a thread); their rows
+// are dealt out in units of kJoinWarps rows, or four times as many where there are enough of them to go round.
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm)
+prompt_join_kernel(PagedShape s, Parts parts, int blocks, uint16_t* out, size_t out_stride) {
+  __shared__ Tail tails[kMostBlocks];
+  __shared__ int unit_end[kMostBlocks], warp_units[kJoinWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = s.Hq / s.Hkv, per = kTile / G;
+  wait_for_predecessor();  // the parts are written
+  auto rows_of = [&](const Tail& t) { return min(t.len - t.tok0, 2 * per) * G; };
+  int rows = 0;
+  if (tid < blocks) {
+    tails[tid] = parts.tails[tid];
+    if (tails[tid].last >= 0) rows = rows_of(tails[tid]);
+  }
+  const int items = __syncthreads_count(rows > 0);
+  const int turns = items * 2 * kTile >= (int)gridDim.x * 2 * kJoinWarps ? 4 : 1;  // rows of a warp
+  int n = (rows + kJoinWarps * turns - 1) / (kJoinWarps * turns);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += y;
+  }
+  if (lane == 31) warp_units[warp] = n;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    n += w < warp ? warp_units[w] : 0;
+    total += warp_units[w];
+  }
+  unit_end[tid] = n;
+  __syncthreads();
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int first = 0, hi = kMostBlocks - 1;  // the first block whose units end behind u
+    while (first < hi) {
+      const int m = (first + hi) >> 1;
+      if (unit_end[m] > u) hi = m; else first = m + 1;
+    }
+    const int row = (u - (first ? unit_end[first - 1] : 0)) * kJoinWarps * turns + warp;
+    const int all = rows_of(tails[first]), count = min(tails[first].last, blocks - 1) - first + 1;
+    if (row >= all) continue;
+    if (turns == 4) join_rows<4>(parts, tails + first, first, row, kJoinWarps, all, count, per, G, out, out_stride);
+    else join_rows<1>(parts, tails + first, first, row, kJoinWarps, all, count, per, G, out, out_stride);
   }
 }
 
@@ -1198,7 +1289,7 @@ cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_
   const int pair = 2 * (kTile / s.G());
   const long long items = ((long long)n_rows / pair + (s.B < n_rows ? s.B : n_rows)) * s.Hkv;
   const long long most = (items * (Ranges::kItemCost + (long long)n_kv_rows + pair) + Ranges::kLeast - 1) / Ranges::kLeast;
-  const int sms = sm_count(), grid = most < sms ? (int)most : sms;
+  const int sms = sm_count() < kMostBlocks ? sm_count() : kMostBlocks, grid = most < sms ? (int)most : sms;
   const Parts parts = parts_of(ws, kv_start, n_kv_rows);
   // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
   static std::mutex both[kMaxDevicesCached];
@@ -1206,7 +1297,7 @@ cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_
   cudaError_t e = launch_attn<Piece>(s, q, q_stride, k, k_stride, v, v_stride, q_start, n_rows, n_kv_rows, scale, out, out_stride,
                                      parts, grid, err, stream);
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_chained(prompt_join_kernel, dim3(grid, kJoinBlocks), dim3(kJoinWarps * 32), 0, stream, 1, s, parts, out,
+  return launch_chained(prompt_join_kernel, dim3(kJoinPerSm * sm_count()), dim3(kJoinThreads), 0, stream, 1, s, parts, grid, out,
                         out_stride);
 }
 

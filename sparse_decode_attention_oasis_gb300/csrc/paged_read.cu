@@ -17,6 +17,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 3;
+constexpr int kUnits = 2;  // of a warp in long calls
 
 struct Args {
   const uint8_t* pages;
@@ -159,16 +160,18 @@ read_kv_kernel(PagedShape s, Args a) {
   const int b0 = min(tid * per, s.B), b1 = min(b0 + per, s.B);
   unsigned bits = 0;
   long long rows = 0, units = 0, all;
+  Request mine = {};  // the chunk's only request
   for (int b = b0; b < b1; ++b) {
-    const Request r = request(s, a, b, &bits);
-    rows += (long long)r.held + r.fresh;
+    mine = request(s, a, b, &bits);
+    rows += (long long)mine.held + mine.fresh;
   }
+  auto again = [&](int b) { return per == 1 ? mine : request(s, a, b, &bits); };
   const long long row0 = block_prefix(rows, warp_sums, &all);
   // the first request whose rows do not fit, and all behind it, get none
   int end_fits = 0;
   long long at = row0;
   for (int b = b0; b < b1; ++b) {
-    const Request r = request(s, a, b, &bits);
+    const Request r = again(b);
     at += (long long)r.held + r.fresh;
     if (at > a.n_rows) {
       bits |= OASIS_EW_BAD_COUNT;
@@ -186,7 +189,7 @@ read_kv_kernel(PagedShape s, Args a) {
     at = row0;
     if (tid == 0) a.kv_start[0] = 0;
     for (int b = b0; b < b1; ++b) {
-      const Request r = request(s, a, b, &bits);
+      const Request r = again(b);
       at += (long long)r.held + r.fresh;
       a.kv_start[b + 1] = at > a.n_rows ? last_end : (int)at;
     }
@@ -268,9 +271,9 @@ template <int kBits>
 static cudaError_t launch(const PagedShape& s, const Args& a, cudaStream_t stream) {
   // every request may end in a partly filled unit
   const long long units = ((long long)a.n_rows / kBS + (s.B < a.n_rows ? s.B : a.n_rows)) * s.Hkv;
-  const long long wanted = (units + kWarps - 1) / kWarps, most = (long long)kCtasPerSm * sm_count();
-  const int grid = wanted < 1 ? 1 : wanted < most ? (int)wanted : (int)most;
-  return launch_chained(read_kv_kernel<kBits>, dim3(grid), dim3(kThreads), 0, stream, 1, s, a);
+  const long long one = (units + kWarps - 1) / kWarps, most = (long long)kCtasPerSm * sm_count();
+  const long long grid = one < 1 ? 1 : one <= most ? one : (one + kUnits - 1) / kUnits > most ? (one + kUnits - 1) / kUnits : most;
+  return launch_chained(read_kv_kernel<kBits>, dim3((unsigned)grid), dim3(kThreads), 0, stream, 1, s, a);
 }
 
 cudaError_t launch_read_kv(int bits, const PagedShape& s, const uint8_t* pages, const void* scales, const int* table,

@@ -3,10 +3,12 @@
 // Mathematics: for 16 dimensions of one token of one head, s = the least scale (5 exponent, 3 fraction
 // bits) of at least amax / 6 (6: the largest e2m1), y = e2m1(x / s), ties to the even code.  Every
 // token has its own scales, so a page's earlier tokens stay as they are, whatever comes later.
-// The quotient is formed as x * (1 / s) in fp32 and rounded to a multiple of 2^-16 by adding and
-// taking away 192; that has one right answer: with 8 bits in x and 4 in s a quotient is a tie of the
-// codes (a multiple of 1/4) exactly or is 2^-11 away from each, and the product is off by less than
-// 2^-20, so ties come out as ties and everything else stays on its side.
+// The quotient is formed as x * (1 / s) in fp32, from an approximate reciprocal (2^-22 off at most),
+// and rounded to a multiple of 2^-16 by adding and taking away 192; that has one right answer: with 8
+// bits in x and 4 in s a quotient is a tie of the codes (a multiple of 1/4) exactly or is 2^-11 away
+// from each, and the product is off by less than 2^-19, so ties come out as ties and everything else
+// stays on its side.  Likewise amax * fl(1/6) is s where amax is 6 s (fl(1/6) is 2^-25 too large, less
+// than half a step at the 4 bits of s), and 2^-8 away from it elsewhere.
 //
 // Two rows of one head to a warp's instruction: 16 lanes of 16 bytes cover a row, a pair of lanes a
 // group.  Rows are independent, so there is no order to keep and nothing is read but the rows.
@@ -28,9 +30,20 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 
 // The byte of the least scale of at least amax / 6, at most the largest one in use.
 __device__ __forceinline__ int scale_byte(float amax) {
-  const float r = __fdiv_rn(amax, 6.0f);
+  const float r = __fmul_rn(amax, 1.0f / 6.0f);
   if (r < 6.103515625e-5f) return (int)ceilf(r * 131072.0f);  // below 2^-14: multiples of 2^-17
   return (int)min((__float_as_uint(r) + 0xfffffu) >> 20, (uint32_t)(kScaleByteHigh + 896)) - 896;  // 896: exponents' bias
+}
+
+// a * inv rounded to a multiple of 2^-16, both halves of a pair.
+__device__ __forceinline__ void quotients(uint32_t w, uint64_t inv, float& lo, float& hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(w << 16), "r"(w & 0xffff0000u));
+  asm("{\n .reg .b64 c, d;\n mov.b64 c, {%3, %3};\n mov.b64 d, {%4, %4};\n fma.rn.f32x2 %0, %1, %2, c;\n"
+      " add.rn.f32x2 %0, %0, d;\n}"
+      : "=l"(x)
+      : "l"(x), "l"(inv), "f"(192.0f), "f"(-192.0f));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
 }
 
 // Eight quotients -> codes, the lowest dimension in the lowest bits; a zero has no sign.
@@ -75,13 +88,13 @@ store_kv_q4_kernel(PagedShape s, const uint16_t* k, size_t k_stride, const uint1
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the group's other lane
     const bool nan = m > 0x7f80u;
     const int b = scale_byte(__uint_as_float(m << 16));
-    const float inv = b ? __fdiv_rn(1.0f, __half2float(__ushort_as_half((unsigned short)(b << 7)))) : 0.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__half2float(__ushort_as_half((unsigned short)max(b << 7, 128)))));
+    uint64_t inv2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
     float y[8];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      y[2 * d] = fmaf(bf_lo(w[d]), inv, 192.0f) - 192.0f;
-      y[2 * d + 1] = fmaf(bf_hi(w[d]), inv, 192.0f) - 192.0f;
-    }
+    for (int d = 0; d < 4; ++d) quotients(w[d], inv2, y[2 * d], y[2 * d + 1]);  // all zeros where b is 0
     const uint32_t code = nan ? 0u : codes8(y);
     if (slot[i] < 0 || slot[i] >= n_slots) {
       if (slot[i] != -1) bits |= OASIS_EW_BAD_SLOT;

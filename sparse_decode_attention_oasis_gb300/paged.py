@@ -219,6 +219,7 @@ class PagedKV:
         self._shape = ctypes.byref(self.shape)
         self._kv_bytes, self._scale_bytes = self.kv.stride(0), self.scale.element_size() * self.scale.stride(0)  # of a layer
         self._scratch = {}  # decode's, by stream
+        self._resume_bytes = -(-B.oasis_resume_attn_workspace_bytes(self.shape) // 256) * 256
 
     def adopt(self, **tensors: torch.Tensor) -> None:
         """Use the caller's tensors in place of kv, scale, table, free, n_free or lens (same
@@ -392,14 +393,39 @@ class PagedKV:
         if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.resume(q, k, v, plan, n_held, layer, scale, out)
-        if q.dim() != 3 or q.shape[1] != self.n_q_heads or k.dim() != 3 or k.shape[1] != self.n_kv_heads:
-            raise ValueError(f"q must be [rows, {self.n_q_heads}, 128], k and v [rows, {self.n_kv_heads}, 128]")
-        if q.shape[0] != k.shape[0]:
-            raise ValueError("q, k and v must have the same rows")
+        if q.dim() != 3:
+            raise ValueError("q, k and v must be [rows, heads, 128]")
+        n, b, hq, hkv, device = q.shape[0], self.batch, self.n_q_heads, self.n_kv_heads, self.device
+        qs, ks, vs = _rows("q", q, hq, n, device), _rows("k", k, hkv, n, device), _rows("v", v, hkv, n, device)
+        row_start = _ints("plan.row_start", plan.row_start, (b + 1,), device).data_ptr()
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of {self.layers}")
         if n_held < 0:
             raise ValueError("n_held must be >= 0")
-        rows = self.read(n_held + k.shape[0], None, layer, (k, v, plan.row_start))
-        return resume_attn(q, rows.k, rows.v, plan.row_start, rows.row_start, scale, out, self.err)
+        if out is None:
+            out = torch.zeros((n, hq, D), dtype=_BF16, device=device)
+        out_stride = _rows("out", out, hq, n, device)
+        if n == 0:
+            return out
+        # one piece of scratch: keys, values, the workspace, kv_start, each a multiple of 256 bytes
+        m = n_held + n
+        kv_bytes, ws_bytes = m * hkv * D * 2, self._resume_bytes
+        scratch = torch.empty(2 * kv_bytes + ws_bytes + 4 * (b + 1), dtype=torch.uint8, device=device)
+        k_at = scratch.data_ptr()
+        v_at, ws_at, start_at = k_at + kv_bytes, k_at + 2 * kv_bytes, k_at + 2 * kv_bytes + ws_bytes
+        lib, stream, err = B._lib or B.load(), _current_stream(self._index), self.err.data_ptr()
+        st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
+            self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
+            self.table.data_ptr(), self.lens.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, row_start, n, start_at, k_at, v_at,
+            m, err, stream)
+        if st:
+            B._check(f"oasis_read_kv_q{self.bits}", st)
+        st = lib.oasis_resume_attn(
+            self._shape, q.data_ptr(), qs, k_at, hkv * D, v_at, hkv * D, row_start, n, start_at, m,
+            _SCALE if scale is None else scale, ws_at, ws_bytes, out.data_ptr(), out_stride, err, stream)
+        if st:
+            B._check("oasis_resume_attn", st)
+        return out
 
     def check(self) -> None:
         """Waits for the device (every stream) and raises if a kernel reported an error; clears the word."""

@@ -42,17 +42,29 @@ def test_codes_are_the_nearest_ties_to_even():
 
 def test_the_quotient_formed_by_a_reciprocal_has_the_right_code():
     """x * (1 / s) in fp32, rounded to a multiple of 2^-16: the same code as the exact quotient's, for every
-    significand of x and of s and every exponent between them that matters (both are scaled by powers of two)."""
+    significand of x and of s and every exponent between them that matters (both are scaled by powers of two),
+    with a reciprocal that is off by up to 2^-22."""
     x = np.arange(1, 256)
     for s in range(1, 16):  # subnormal scales have fewer bits
-        inv = np.float32(1.0) / np.float32(s)
-        for e in range(-12, 8):
-            xs = x * 2.0 ** e
-            keep = xs / s <= 6
-            product = (xs[keep].astype(np.float32).astype(np.float64) * np.float64(inv))  # exact: 8 + 24 bits
-            y = (product + 192.0).astype(np.float32) - np.float32(192.0)  # one rounding, as a fused multiply-add's
-            exact = np.array([float(Fraction(v) / s) for v in xs[keep].tolist()])
-            np.testing.assert_array_equal(ref.e2m1_codes(y.astype(np.float64)), ref.e2m1_codes(exact))
+        for off in (-2.0 ** -22, 0.0, 2.0 ** -22):
+            inv = np.float32(1.0 / s * (1 + off))
+            for e in range(-12, 8):
+                xs = x * 2.0 ** e
+                keep = xs / s <= 6
+                product = xs[keep].astype(np.float32).astype(np.float64) * np.float64(inv)  # exact: 8 + 24 bits
+                y = (product + 192.0).astype(np.float32) - np.float32(192.0)  # one rounding, as a fused multiply-add's
+                exact = np.array([float(Fraction(v) / s) for v in xs[keep].tolist()])
+                np.testing.assert_array_equal(ref.e2m1_codes(y.astype(np.float64)), ref.e2m1_codes(exact))
+
+
+def test_the_scale_formed_by_a_product_is_the_least_one():
+    """amax * fl(1/6) in fp32 for every bf16 amax, then the next scale at or above it."""
+    a = (np.arange(0x7f80) << 16).astype(np.uint32).view(np.float32)
+    r = a * np.float32(1 / 6)
+    low = np.ceil(r.astype(np.float64) * 2.0 ** 17)
+    normal = ((r.view(np.uint32).astype(np.int64) + 0xfffff) >> 20) - 896
+    got = np.where(r < 2.0 ** -14, low, np.minimum(normal, ref.S_HIGH))
+    np.testing.assert_array_equal(got, ref.scale_byte(a.astype(np.float64)))
 
 
 def test_values_follow_the_layout():

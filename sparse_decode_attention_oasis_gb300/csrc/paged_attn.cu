@@ -812,6 +812,102 @@ paged_decode_join_kernel(PagedShape s, const float* parts, const int2* tails,
   *reinterpret_cast<uint32_t*>(out + ((long long)t.x * G + r) * kD + 2 * d) = pack_bf16x2(o0 * inv, o1 * inv);
 }
 
+// The same for pages in 4 bits, with no more thread blocks than there can be pairs that go on in a later block.  kSpread: a
+// block for each of a pair's rows, its pieces spread over the warps (few pairs in many pieces); else one for the
+// pair, a row to a warp (many pairs in two pieces).
+constexpr int kJoinWarps4 = 8, kJoinThreads4 = kJoinWarps4 * 32;
+template <bool kSpread>
+__global__ void __launch_bounds__(kJoinThreads4)
+paged_decode_join4_kernel(PagedShape s, const float* parts, const int2* tails, int blocks, uint16_t* out) {
+  __shared__ float rows[kJoinWarps4][kRowFloats];
+  __shared__ int warp_tails[kJoinWarps4], found[3];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = s.Hq / s.Hkv;
+  const int wanted = kSpread ? blockIdx.x / G : blockIdx.x;
+  wait_for_predecessor();  // the pieces are written
+  if (tid == 0) found[0] = -1;
+  int before = 0;  // tails of the blocks looked at
+  for (int b0 = 0; b0 < blocks; b0 += kJoinThreads4) {
+    const int b = b0 + tid;
+    const int2 t = b < blocks ? tails[b] : make_int2(-1, 0);
+    const unsigned has = __ballot_sync(0xffffffffu, t.x >= 0);
+    if (lane == 0) warp_tails[warp] = __popc(has);
+    __syncthreads();
+    int rank = before + __popc(has & ((1u << lane) - 1));
+#pragma unroll
+    for (int w = 0; w < kJoinWarps4; ++w) {
+      rank += w < warp ? warp_tails[w] : 0;
+      before += warp_tails[w];
+    }
+    if (t.x >= 0 && rank == wanted) {
+      found[0] = t.x;
+      found[1] = b;
+      found[2] = t.y;
+    }
+    __syncthreads();
+  }
+  if (found[0] < 0) return;
+  const int first = found[1], n = found[2] - first + 1;
+  const int r = kSpread ? blockIdx.x % G : warp, c_first = kSpread ? warp : 0;
+  constexpr int kStep = kSpread ? kJoinWarps4 : 1, kAtOnce = 5;
+  float top = neg_inf(), sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (r < G) {
+    for (int c0 = c_first; c0 < n; c0 += kStep * kAtOnce) {
+      float4 x[kAtOnce];
+      float2 ml[kAtOnce];
+#pragma unroll
+      for (int d = 0; d < kAtOnce; ++d) {
+        const int c = min(c0 + d * kStep, n - 1);
+        const float* row = parts + ((((long long)first + c) * 2 + (c == 0 ? 1 : 0)) * G + r) * kRowFloats;
+        ml[d] = *reinterpret_cast<const float2*>(row + kD);
+        const float2 u = *reinterpret_cast<const float2*>(row + lane * 4), v = *reinterpret_cast<const float2*>(row + lane * 4 + 2);
+        x[d] = make_float4(u.x, u.y, v.x, v.y);
+      }
+#pragma unroll
+      for (int d = 0; d < kAtOnce; ++d) {
+        if (c0 + d * kStep >= n) continue;
+        const float next = fmaxf(top, ml[d].x);
+        const float f0 = top == neg_inf() ? 0.f : exp2f(top - next), f1 = ml[d].x == neg_inf() ? 0.f : exp2f(ml[d].x - next);
+        o[0] = fmaf(o[0], f0, x[d].x * f1);
+        o[1] = fmaf(o[1], f0, x[d].y * f1);
+        o[2] = fmaf(o[2], f0, x[d].z * f1);
+        o[3] = fmaf(o[3], f0, x[d].w * f1);
+        sum = fmaf(sum, f0, ml[d].y * f1);
+        top = next;
+      }
+    }
+  }
+  uint16_t* const dst = out + ((long long)found[0] * G + r) * kD;
+  if constexpr (!kSpread) {
+    if (r >= G) return;
+    const float inv = inverse(top, sum);
+    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rows[warp][lane * 4 + i] = o[i];
+    if (lane == 0) {
+      rows[warp][kD] = top;
+      rows[warp][kD + 1] = sum;
+    }
+    __syncthreads();
+    if (tid >= kD / 2) return;
+    float m = neg_inf();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps4; ++w) m = fmaxf(m, rows[w][kD]);
+    float l = 0.f, o0 = 0.f, o1 = 0.f;
+    if (m != neg_inf()) {
+#pragma unroll
+      for (int w = 0; w < kJoinWarps4; ++w) {
+        const float f = exp2f(rows[w][kD] - m);
+        l = fmaf(f, rows[w][kD + 1], l);
+        o0 = fmaf(f, rows[w][2 * tid], o0);
+        o1 = fmaf(f, rows[w][2 * tid + 1], o1);
+      }
+    }
+    const float inv = inverse(m, l);
+    *reinterpret_cast<uint32_t*>(dst + 2 * tid) = pack_bf16x2(o0 * inv, o1 * inv);
+  }
+}
+
 int most_blocks() { return kCtasPerSm * sm_count(); }
 
 }  // namespace
@@ -848,7 +944,10 @@ cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_strid
   // 1,000 16.7 against 19.7.  With more of the places filled the gain lasts longer: of 304, 208 pairs of 96 pages 21.3 against
   // 22.3 and of 128 26.4 against 25.9, 256 pairs of 128 27.8 against 30.3, of 192 38.6 against 40.3, of 256 49.1 against 50.0.
   while (a.team < 8 && pairs * a.team * 2 <= most && pair_max > kMinPages * a.team) a.team *= 2;
-  const int team_pages = pairs * a.team * 3 >= most * 2LL ? 128 : 56;  // two thirds of the GPU's places filled, or fewer
+  // 4 bits: 8 pairs of 512 pages by teams of 8 11.1 against 11.5, of 1,024 15.7 against 13.4; 256 pairs of 128 22.0 against
+  // 25.2, of 188 28.4 against 28.9, of 256 35.2 against 36.7.
+  const bool filled = pairs * a.team * 3 >= most * 2LL;  // two thirds of the GPU's places, or fewer
+  const int team_pages = kBits == 8 ? (filled ? 128 : 56) : filled ? 256 : 72;
   if (pairs * a.team <= most && pair_max <= team_pages * a.team) {
     const size_t with_piece = kBits == 8 ? smem + (size_t)s.G() * kRowFloats * sizeof(float) : smem;
     static int attr_cache[kMaxDevicesCached] = {};
@@ -864,6 +963,12 @@ cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_strid
   std::lock_guard<std::mutex> lock(both_launches[current_device()]);
   e = launch_chained(paged_decode_attn_kernel<false, kBits>, dim3(grid), dim3(kThreads), smem, stream, 1, s, a);
   if (e != cudaSuccess || grid == 1) return e;
+  if constexpr (kBits == 4) {
+    const int tails = pairs < grid ? (int)pairs : grid;
+    const bool spread = tails * s.G() <= most;
+    return launch_chained(spread ? paged_decode_join4_kernel<true> : paged_decode_join4_kernel<false>,
+                          dim3(spread ? tails * s.G() : tails), dim3(kJoinThreads4), 0, stream, 1, s, parts, a.tails, grid, out);
+  }
   return launch_chained(paged_decode_join_kernel, dim3(grid, s.G()), dim3(kJoinWarps * 32), 0, stream, 1, s, parts, a.tails,
                         out);
 }

@@ -1,4 +1,4 @@
-// Decode attention over 8-bit pages (oasis_paged_decode_attn_q8).
+// Decode attention over pages in 8 bits (oasis_paged_decode_attn_q8) and in 4 (oasis_paged_decode_attn_q4).
 //
 // Mathematics: a softmax over tokens with a running reference M, one per query
 // row: w_t = 2^(c s_t + lv_t - M), o = sum w_t v8_t / sum w_t 2^-lv_t, where
@@ -43,6 +43,22 @@
 // pages ahead (177 to 197), queries loaded before the tables but converted after (205:
 // the live registers cost the loop), 4 or 16 warps to a block (no change), one join
 // block for all query rows of a pair (1 us more).
+//
+// Pages in 4 bits: the same mathematics without page scales (lk, lv = 0): a code times its group's scale has 6 significant
+// bits and is a half exactly, so keys and values are scaled before the products and the weights need no exponent of a page.
+// A lane's dimensions of a token are whole groups of 16, so it needs two scale bytes for a key and one for a value.  Pages
+// pass through shared memory by asynchronous copies, two at a time while the next two are on their way: half the bytes
+// of a page in 8 bits want twice as many in flight, more than registers hold (two pages ahead in registers: 123 against 103 us).
+// Bound: HBM, 2,304 B for a page and head, with the instructions close behind (287 for each: 64 conversions, 64
+// multiplications by scales, 16 for the exchange of codes between value rows, 16 MMAs; conversions and logic share one
+// pipe, half-precision multiplications and integer ones another, two cycles an instruction each).  32 requests of 1 to 32K
+// tokens, 32/8 heads (471 MB): 91 us, 5.2 TB/s, 0.77 of the measured copy rate; while all blocks run they read 6.5 TB/s,
+// but of an SM's two blocks one finishes 10 us before the other, whose warps alone do not keep up the rate.  One
+// request of 128K tokens, 64/8 heads (151 MB): 38 us.  128 pages for each of 256 pairs (76 MB): 22 us.  A gap before
+// each pair's pages in the equal ranges: 103 against 90 us with 17 pairs of one or two pages at the first block's warps.
+// Measured and not kept: one page at a time (105 against 103), scores of the next pages beside the products of these
+// (101 against 91: 302 instructions), copies that zero instead of branches (93), 9 warps to a block (100: spills), 16 warps
+// to one block (96; meeting every 8 to 32 pages 103), 53 to 57% of the pages for the blocks that start first (96 to 100).
 #include <type_traits>
 
 #include "paged.cuh"

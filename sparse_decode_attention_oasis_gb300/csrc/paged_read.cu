@@ -7,6 +7,10 @@
 // new rows that lie there).  The units of all requests, heads innermost, form one sequence, cut into
 // equal ranges for the thread blocks; a block's warps take its units in turn.  Each lane has 32
 // dimensions of two tokens, whole 32-byte sectors to a store.
+// Bound: HBM, 10.5 KB read and written for a unit in 4 bits, 12.3 in 8.  46,700 tokens of 8 heads in ten requests
+// (254 MB, 4 bits): 45 us, 5.7 TB/s, 0.85 of the measured copy rate; 1,000 tokens: 5.3 us, four loads that wait for one
+// another.  Blocks of 16 units, so that the ones that finish early make room: one range for each place of the GPU 49 us;
+// one unit to a warp 46; two blocks an SM 46 (1,000 tokens: 4.5), four 57.
 #include <cuda_fp16.h>
 
 #include "paged.cuh"

@@ -12,6 +12,9 @@
 //
 // Two rows of one head to a warp's instruction: 16 lanes of 16 bytes cover a row, a pair of lanes a
 // group.  Rows are independent, so there is no order to keep and nothing is read but the rows.
+// Bound: HBM, 656 B for a row, head, K and V, with the instructions close behind.  15,600 rows of 8 heads (82 MB):
+// 16.8 us, 4.9 TB/s, 0.73 of the measured copy rate (20.2 with two divisions for each group and quotients
+// one by one); 32 rows of a decode step: 1.4 us.
 #include <cuda_fp16.h>
 
 #include "paged.cuh"

@@ -1,4 +1,5 @@
-// Causal attention over packed prompts (oasis_prompt_attn): TMA -> shared memory ->
+// Causal attention over packed prompts (oasis_prompt_attn), and over keys that lie before them as well
+// (oasis_resume_attn): TMA -> shared memory ->
 // tcgen05.mma -> TMEM, one persistent thread block per SM.
 //
 // Mathematics: one pass over the keys with a running reference M and sum of a
@@ -51,6 +52,15 @@
 // (packed 210 against 175), only its products cut (within 2% either way), outputs transposed over four lanes
 // (packed 181 against 175), the output through a ring place and a tensor store (16 prompts of 512 tokens 51
 // against 53, the others the same, for 80 lines of accounting).
+//
+// Keys before the new rows (Piece for Item): few rows may read many keys, so all items' tiles form one sequence, cut into
+// ranges of equal cost (Ranges), one for each block; parts of items that cross a border leave their accumulators,
+// reference and sum in fp32, and a second kernel joins them.  Two parts at most for a block, 266 KB each, so
+// the workspace does not depend on the sizes.  32/8 heads, with the read-back from 4-bit pages: 2,048 tokens after 30,000
+// 645 to 675 us (1.04 PFLOP in all, 1.9 PFLOP/s in the kernel's 540 to 565 us; read-back 25 to 30, join 15), 45 after 6,000
+// 29 us (6, 15 and 6), eight requests of 1 to 2,000 after up to 12,000 156 us (30, 105, 10); 64/8 heads, 511 after 8,100 and
+// 900 after 700 from 8-bit pages 154 us.  Beside the tiles a block pays 5 to 7 us before its first scores and 3 to 4 at
+// an item's ends.  The join moves what the parts hold (40 MB where every block has two) at the rate of the L2 and HBM.
 // Every wait is bounded: on expiry the block raises OASIS_EW_TIMEOUT, waits (bounded)
 // for its own copies and MMAs, frees TMEM and returns.
 #include <type_traits>
@@ -396,10 +406,12 @@ struct Schedule {
 };
 
 // The items of a call with keys before its new rows, cut into equal ranges of cost for the thread blocks: cost in keys,
-// past + the keys of the item's last row (whole tiles of rows) + kItemCost for its ends.  A sequence's items follow
-// each other head by head; an item that crosses a range's border is cut at a tile there (not one tile from its ends).
+// past + the keys of the item's last row (whole tiles of rows) + kItemCost for its ends, and an eighth less for an item
+// whose second query tile has no token (measured: 1.3 us for a K/V tile and both query tiles, 1.1 for one, 2.8 to 3.9 for an
+// item's ends, 1.3 us being 128 keys).  A sequence's items follow each other head by head; an item that crosses a range's
+// border is cut at a tile there (not one tile from its ends).
 struct Ranges {
-  static constexpr long long kItemCost = 336, kLeast = 512;  // least cost of a block's range
+  static constexpr long long kItemCost = 400, kLeast = 512;  // least cost of a block's range
   const int *q_start, *kv_start;
   int B, n_rows, n_kv_rows, pair, per, heads, lane;
   unsigned bits;
@@ -427,7 +439,15 @@ struct Ranges {
   __device__ long long before_place(int p, int keys) const {  // cost of a head's items before place p
     return (long long)p * (keys + kItemCost) + (long long)pair * ((long long)p * (p + 1) / 2);
   }
-  __device__ long long head_cost(int n, int keys) const { return before_place((n + pair - 1) / pair, keys); }
+  // The item at place p of a sequence with n rows.
+  __device__ long long item_cost(int p, int n, int keys) const {
+    const long long c = keys + kItemCost + (long long)(p + 1) * pair;
+    return (long long)p * pair + per >= n ? c - c / 8 : c;
+  }
+  __device__ long long head_cost(int n, int keys) const {
+    const int last = (n - 1) / pair;
+    return before_place(last, keys) + item_cost(last, n, keys);
+  }
 
   // gives the number of blocks that have a range
   __device__ int init(const int* qs, const Parts& parts, int b_, int rows, int tokens, int hkv, int ln) {
@@ -509,9 +529,9 @@ struct Ranges {
     of_head = len > 0 ? head_cost(len, past) : 0;
     h = place = 0;
   }
-  // The tile at which a border inside an item cuts it, `cost` behind its beginning.
-  __device__ int cut(long long cost, int tiles) const {
-    const int j = (int)min(max(cost - kItemCost, 0ll) / kTile, (long long)tiles);
+  // The tile at which a border inside an item cuts it, `cost` behind its beginning; half: its second query tile is empty.
+  __device__ int cut(long long cost, int tiles, bool half) const {
+    const int j = (int)min(max((half ? cost + cost / 7 : cost) - kItemCost, 0ll) / kTile, (long long)tiles);
     return j < 2 ? 0 : tiles - j < 2 ? tiles : j;
   }
   // This block's next part (row0 -1: there are no more).  tail: of an item that goes on behind this block's range.
@@ -526,7 +546,8 @@ struct Ranges {
       it.kv0 = kv0;
       it.past = past;
       const int tiles = max(tiles_of(it, 0, per), tiles_of(it, 1, per));
-      const long long from = at, to = start + h * of_head + before_place(place + 1, past);
+      const bool half = it.tok0 + per >= len;
+      const long long from = at, to = start + h * of_head + before_place(place, past) + item_cost(place, len, past);
       at = to;
       if (++place * (long long)pair >= len) {
         place = 0;
@@ -537,8 +558,8 @@ struct Ranges {
           while (len == 0 && at < hi) take_sequence(b + 1);  // below hi there is another one
         }
       }
-      it.j0 = from < lo ? cut(lo - from, tiles) : 0;
-      it.j1 = to > hi ? cut(hi - from, tiles) : tiles;
+      it.j0 = from < lo ? cut(lo - from, tiles, half) : 0;
+      it.j1 = to > hi ? cut(hi - from, tiles, half) : tiles;
       it.whole = it.j0 == 0 && it.j1 == tiles;
       if (it.j0 >= it.j1) continue;
       if (it.j0 == 0 && !it.whole) *last = block_of(to - 1);
@@ -1087,7 +1108,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 }
 
 constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
-constexpr int kJoinPerSm = 3;
+constexpr int kJoinPerSm = 2;
 constexpr int kMostBlocks = kJoinThreads;  // thread blocks whose parts a join can take
 
 __device__ __forceinline__ float2 load8(const float2* p) {

@@ -21,7 +21,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kUnits = 2;  // of a warp in long calls
+constexpr int kUnits = 2;  // of a warp in long calls of few requests
 
 struct Args {
   const uint8_t* pages;
@@ -169,7 +169,7 @@ read_kv_kernel(PagedShape s, Args a) {
     mine = request(s, a, b, &bits);
     rows += (long long)mine.held + mine.fresh;
   }
-  auto again = [&](int b) { return per == 1 ? mine : request(s, a, b, &bits); };
+  auto again = [&](int b) { return per == 1 ? mine : request(s, a, b, &bits); };  // bits of the first pass stay
   const long long row0 = block_prefix(rows, warp_sums, &all);
   // the first request whose rows do not fit, and all behind it, get none
   int end_fits = 0;
@@ -276,7 +276,9 @@ static cudaError_t launch(const PagedShape& s, const Args& a, cudaStream_t strea
   // every request may end in a partly filled unit
   const long long units = ((long long)a.n_rows / kBS + (s.B < a.n_rows ? s.B : a.n_rows)) * s.Hkv;
   const long long one = (units + kWarps - 1) / kWarps, most = (long long)kCtasPerSm * sm_count();
-  const long long grid = one < 1 ? 1 : one <= most ? one : (one + kUnits - 1) / kUnits > most ? (one + kUnits - 1) / kUnits : most;
+  long long grid = one < 1 ? 1 : one < most ? one : most;
+  // every block goes over all requests, so where those are many there are no more blocks than places
+  if (s.B <= kThreads && (one + kUnits - 1) / kUnits > most) grid = (one + kUnits - 1) / kUnits;
   return launch_chained(read_kv_kernel<kBits>, dim3((unsigned)grid), dim3(kThreads), 0, stream, 1, s, a);
 }
 

@@ -57,7 +57,7 @@
 // ranges of equal cost (Ranges), one for each block; parts of items that cross a border leave their accumulators,
 // reference and sum in fp32, and a second kernel joins them.  Two parts at most for a block, 266 KB each, so
 // the workspace does not depend on the sizes.  32/8 heads, with the read-back from 4-bit pages: 2,048 tokens after 30,000
-// 645 to 675 us (1.04 PFLOP in all, 1.9 PFLOP/s in the kernel's 540 to 565 us; read-back 25 to 30, join 15), 45 after 6,000
+// 645 to 675 us (1.04 TFLOP, 1.9 PFLOP/s in the kernel's 540 to 565 us; read-back 25 to 30, join 15), 45 after 6,000
 // 29 us (6, 15 and 6), eight requests of 1 to 2,000 after up to 12,000 156 us (30, 105, 10); 64/8 heads, 511 after 8,100 and
 // 900 after 700 from 8-bit pages 154 us.  Beside the tiles a block pays 5 to 7 us before its first scores and 3 to 4 at
 // an item's ends.  The join moves what the parts hold (40 MB where every block has two) at the rate of the L2 and HBM.
@@ -462,6 +462,7 @@ struct Ranges {
     lane = ln;
     bits = 0;
     long long total = 0, of_first = 0;  // of_first: sequence `lane`
+#pragma unroll 4
     for (int s = lane; s < B; s += 32) {
       int qa, n, ka, before;
       const long long c = sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0;

@@ -208,7 +208,7 @@ class PagedKV:
         if bits == 8:
             self.scale = torch.ones((layers, n_pages, n_kv_heads, 2), dtype=torch.float32, device=device)
         else:
-            self.scale = torch.zeros((layers, n_pages, n_kv_heads, 2, BS * D // 16), dtype=torch.uint8, device=device)
+            self.scale = torch.empty((layers, n_pages, n_kv_heads, 2, BS * D // 16), dtype=torch.uint8, device=device)
         self.table = torch.full((batch, nb_max), -1, dtype=torch.int32, device=device)
         self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)  # page 0 is taken first
         self.n_free = torch.full((1,), n_pages, dtype=torch.int32, device=device)

@@ -234,6 +234,42 @@ def test_through_the_cache(bits):
     c.check()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_the_caches_resume_captured_and_replayed(bits):
+    """The whole call in a graph, replayed after the cache has grown, beside an eager call; against the eager call's bits."""
+    from paged_helpers import bf16, ints
+
+    from sparse_decode_attention_oasis_gb300.paged import PagedKV
+
+    rng = np.random.default_rng(20 + bits)
+    c = PagedKV(n_pages=300, batch=3, nb_max=100, n_q_heads=16, n_kv_heads=4, bits=bits)
+    q, _ = bf16(rng, (40, 16, 128))
+    k, _ = bf16(rng, (2000, 4, 128))
+    new = ints([20, 0, 20])
+
+    def grow(tokens):
+        plan = c.extend(c.lens + ints(tokens), int(sum(tokens)))
+        c.store(k[: sum(tokens)], k[-sum(tokens):], plan.slot_map)
+        c.commit(plan)
+
+    grow([700, 0, 33])
+    plan = c.extend(c.lens + new, 40)
+    c.resume(q, k[:40], k[40:80], plan, 1900)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = c.extend(c.lens + new, 40)
+        out = c.resume(q, k[:40], k[40:80], captured, 1900)
+    for tokens in ([1, 0, 0], [100, 50, 900], [0, 1, 16]):
+        grow(tokens)
+        eager = c.resume(q, k[:40], k[40:80], c.extend(c.lens + new, 40), 1900)
+        g.replay()
+        again = c.resume(q, k[:40], k[40:80], captured, 1900)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(again, eager)
+    c.check()
+
+
 def test_a_bound_that_is_too_small_is_reported():
     from paged_helpers import bf16, ints
 

@@ -49,16 +49,17 @@
 // A lane's dimensions of a token are whole groups of 16, so it needs two scale bytes for a key and one for a value.  Pages
 // pass through shared memory by asynchronous copies, two at a time while the next two are on their way: half the bytes
 // of a page in 8 bits want twice as many in flight, more than registers hold (two pages ahead in registers: 123 against 103 us).
-// Bound: HBM, 2,304 B for a page and head, with the instructions close behind (287 for each: 64 conversions, 64
-// multiplications by scales, 16 for the exchange of codes between value rows, 16 MMAs; conversions and logic share one
-// pipe, half-precision multiplications and integer ones another, two cycles an instruction each).  32 requests of 1 to 32K
-// tokens, 32/8 heads (471 MB): 91 us, 5.2 TB/s, 0.77 of the measured copy rate; while all blocks run they read 6.5 TB/s,
-// but of an SM's two blocks one finishes 10 us before the other, whose warps alone do not keep up the rate.  One
-// request of 128K tokens, 64/8 heads (151 MB): 38 us.  128 pages for each of 256 pairs (76 MB): 22 us.  A gap before
-// each pair's pages in the equal ranges: 103 against 90 us with 17 pairs of one or two pages at the first block's warps.
-// Measured and not kept: one page at a time (105 against 103), scores of the next pages beside the products of these
-// (101 against 91: 302 instructions), copies that zero instead of branches (93), 9 warps to a block (100: spills), 16 warps
-// to one block (96; meeting every 8 to 32 pages 103), 53 to 57% of the pages for the blocks that start first (96 to 100).
+// Bound: HBM, 2,304 B for a page and head.  32 requests of 1 to 32K tokens, 32/8 heads (471 MB): 88 us, 5.4 TB/s,
+// 0.80 of the measured copy rate; the same copies without any arithmetic 86.  4 us pass before the first pages are there, and
+// of an SM's two blocks the one that started first is done at 66, the other at 79 (without arithmetic 65 and 68).  One
+// request of 128K tokens, 64/8 heads (151 MB): 38 us.  128 pages for each of 256 pairs (76 MB): 22 us.  A pair costs a
+// warp 3 us beside its pages, which a gap in the equal ranges stands for: 17 pairs of one or two pages at one warp made the
+// whole call 103 us without gaps, 91 with gaps of 2 pages, 88 with 5.  287 instructions for a page and head (64 conversions, 64
+// multiplications by scales, 16 for the exchange of codes between value rows, 16 MMAs): leaving out the conversions or the
+// multiplications changes no time.  Measured and not kept (against 91): one page at a time 94, keys and values copied each as soon
+// as their places are free 92, scores of the next pages beside the products of these 101, copies that zero instead of branches 93,
+// 9 warps to a block 100 (spills), 16 warps to one block 96 (103 where they meet every 8 to 32 pages), 52 to 57% of the
+// pages for the first half of the blocks 90 to 96 (in a chain of calls a half is not what an SM got first).
 #include <type_traits>
 
 #include "paged.cuh"
@@ -70,7 +71,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinPages = 8;  // pages a thread block gets at least, when there are so few
-constexpr int kPairGap = 2;   // 4 bits: what a pair costs a warp beside its pages, in pages
+constexpr int kPairGap = 5;   // 4 bits: what a pair costs a warp beside its pages, in pages
 constexpr int kJoinWarps = 4;
 constexpr int kMaxG = 8;
 constexpr int kRowFloats = kD + 2;
@@ -428,9 +429,11 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     // with one pair to a chunk the prefix holds its pages
     auto pages_of = [&](int pair) {
       if (kClustered) return (int)total;
-      return per == 1 ? max((int)(sh.chunk_start[pair + 1] - sh.chunk_start[pair]) - kGap, 0) : pair_pages(s, a, pair, &bits);
+      if (per > 1) return pair_pages(s, a, pair, &bits);
+      const int n = (int)(sh.chunk_start[pair + 1] - sh.chunk_start[pair]);
+      return kGap ? max(n - kGap, 0) : n;
     };
-    auto span = [&](int pages) { return pages > 0 ? pages + kGap : 0; };
+    auto span = [&](int pages) { return kGap && pages > 0 ? pages + kGap : pages; };
     int count = pages_of(e);
     while (e_lo + span(count) <= w_lo) {
       e_lo += span(count);
@@ -439,47 +442,10 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
     while (true) {
       const long long p_lo = e_lo + kGap;  // the pair's first page
       const int first = (int)max(w_lo - p_lo, 0ll), last = (int)min((long long)count, w_hi - p_lo);  // pages of the pair
-      if (first < last) {
+      if (kGap == 0 || first < last) {
         const int b = e / s.Hkv, h = e - b * s.Hkv;
         const int ctx = (int)min((long long)max(a.ctx_len[b], 0), (long long)s.nb_max * kBS);
         const int nb = (ctx + kBS - 1) / kBS;
-
-        // ---- the query row lane / 4, dimensions as for the keys
-        uint32_t qf[16];
-        float fac[2];
-        {
-          uint4 w[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
-          if ((lane >> 2) < G) {
-            constexpr int kPiece = kBits == 8 ? 16 : 32, kNext = kBits == 8 ? 64 : 16;
-            const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * kPiece;
-            w[0] = load16(src);
-            w[1] = load16(src + 8);
-            w[2] = load16(src + kNext);
-            w[3] = load16(src + kNext + 8);
-          }
-          uint32_t m = 0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const uint32_t v = word(w[c], d) & 0x7fff7fffu;
-              m = max(m, max(v & 0xffffu, v >> 16));
-            }
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const int ex = max((int)(m >> 7) - 127, -112);  // exponent of the row's largest value
-          const float f = pow2f(14 - ex);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint32_t v = word(w[c >> 2], c & 3);
-            qf[c] = pack_f16x2(bf_lo(v) * f, bf_hi(v) * f);
-          }
-          const float mine = a.scale_log2 * pow2f(ex - 14);
-          fac[0] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8);
-          fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
-        }
 
         int my_page = -1, my_valid = 0;  // of page (group of 32) + lane
         float2 my_scale = make_float2(1.f, 1.f);
@@ -509,9 +475,50 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
             }
           }
         };
+        // ---- the query row lane / 4, dimensions as for the keys
+        uint32_t qf[16];
+        float fac[2];
+        auto load_query = [&](uint4 (&w)[4]) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) w[m] = make_uint4(0u, 0u, 0u, 0u);
+          if ((lane >> 2) < G) {
+            constexpr int kPiece = kBits == 8 ? 16 : 32, kNext = kBits == 8 ? 64 : 16;
+            const uint16_t* src = a.q + (size_t)b * a.q_stride + (size_t)(h * G + (lane >> 2)) * kD + (lane & 3) * kPiece;
+            w[0] = load16(src);
+            w[1] = load16(src + 8);
+            w[2] = load16(src + kNext);
+            w[3] = load16(src + kNext + 8);
+          }
+        };
+        auto convert_query = [&](const uint4 (&w)[4]) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t v = word(w[c], d) & 0x7fff7fffu;
+              m = max(m, max(v & 0xffffu, v >> 16));
+            }
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          const int ex = max((int)(m >> 7) - 127, -112);  // exponent of the row's largest value
+          const float f = pow2f(14 - ex);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t v = word(w[c >> 2], c & 3);
+            qf[c] = pack_f16x2(bf_lo(v) * f, bf_hi(v) * f);
+          }
+          const float mine = a.scale_log2 * pow2f(ex - 14);
+          fac[0] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8);
+          fac[1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
+        };
+
         State st;
-        st.clear();
+        uint4 query[4];
+        load_query(query);
         if constexpr (kBits == 8) {
+          convert_query(query);
+          st.clear();
           Rows kr, vr;
           const long long head_stride = kHeadPageBytes;
           auto head_page = [&](int page) { return a.pages + ((long long)page * s.Hkv + h) * head_stride; };
@@ -601,44 +608,48 @@ paged_decode_attn_kernel(PagedShape s, Args a) {
           const long long page_bytes = s.Hkv * kHeadPageBytes4, scale_bytes = s.Hkv * kHeadScaleBytes4;
           const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_of(warp));
           const uint32_t value_at = kBS * (kD / 2) + (lane >> 3) * kD + ((lane & 7) ^ (lane >> 3) << 1) * 16;
-          // a page and its tokens in one word (page * 32 + tokens, -32: none): of page (group of 32) + lane
-          int ahead = -32;
+          // a page and its tokens in one word (page * 32 + tokens, 0: none): of page (group of 32) + lane.  The tables of the
+          // group after that are on their way as well.
+          uint32_t ahead = 0;
+          lookup(first);
           auto fetch = [&](int at, uint32_t place) {  // pages at and at + 1: their tokens, 16 bits each
-            int tokens = 0;
+            uint32_t tokens = 0;
             if (at < last) {
               const int in = (at - first) & 31;
               if (in == 0) {
-                lookup(at);
-                ahead = my_page * 32 + my_valid;
+                ahead = my_page < 0 ? 0u : (uint32_t)my_page * 32 + (uint32_t)my_valid;
+                lookup(at + 32);
               }
-              const int w0 = __shfl_sync(0xffffffffu, ahead, in), w1 = __shfl_sync(0xffffffffu, ahead, in + 1);
-              if (w0 >= 0) {
-                const uint8_t* from = codes + (w0 >> 5) * page_bytes;
+              const uint32_t w0 = __shfl_sync(0xffffffffu, ahead, in), w1 = __shfl_sync(0xffffffffu, ahead, in + 1);
+              if (w0) {
+                const uint8_t* from = codes + (long long)(w0 >> 5) * page_bytes;
                 copy16(place + lane * 16, from);
                 copy16(place + lane * 16 + 512, from + 512);
                 copy16(place + value_at, from + 1024);
                 copy16(place + value_at + 512, from + 1536);
               }
-              if (w1 >= 0) {
-                const uint8_t* from = codes + (w1 >> 5) * page_bytes;
+              if (w1) {
+                const uint8_t* from = codes + (long long)(w1 >> 5) * page_bytes;
                 copy16(place + kStageBytes + lane * 16, from);
                 copy16(place + kStageBytes + lane * 16 + 512, from + 512);
                 copy16(place + kStageBytes + value_at, from + 1024);
                 copy16(place + kStageBytes + value_at + 512, from + 1536);
               }
-              const int mine = lane < 16 ? w0 : w1;  // the first 16 lanes copy the first one's scales
-              if (mine >= 0)
+              const uint32_t mine = lane < 16 ? w0 : w1;  // the first 16 lanes copy the first one's scales
+              if (mine)
                 copy16(place + (lane < 16 ? 0 : kStageBytes) + (uint32_t)kHeadPageBytes4 + (lane & 15) * 16,
-                       scales + (mine >> 5) * scale_bytes);
+                       scales + (long long)(mine >> 5) * scale_bytes);
               tokens = (w0 & 31) | (w1 & 31) << 16;
             }
             copy_commit();
             return tokens;
           };
+          uint32_t seen = 0, tokens = fetch(first, ring), next = fetch(first + 2, ring + 2 * kStageBytes);
+          convert_query(query);  // the tables and the first pages are on their way
+          st.clear();
           // a score's factor stays normal, so that it leaves an infinity one
           const float f[2] = {fmaxf(fac[0], 1.1754944e-38f), fmaxf(fac[1], 1.1754944e-38f)};
           float top[2] = {kLowest, kLowest};
-          int seen = 0, tokens = fetch(first, ring), next = fetch(first + 2, ring + 2 * kStageBytes);
           uint32_t place = ring;
           for (int at = first; at < last; at += 2) {
             copy_wait<1>();

@@ -896,6 +896,8 @@ OASIS_API oasis_status oasis_paged_decode_attn_q4(const oasis_paged_shape* shape
  *              oasis_extend_tables).  A request whose bounds decrease or leave
  *              [0, n_new] has no new rows, with OASIS_EW_BAD_COUNT.
  *   new_start  device int32 [B+1], or NULL: no new rows
+ *   only_new   1: a request without new rows has none at all (oasis_resume_attn has
+ *              no use for its held tokens); 0: it has its held ones
  *   kv_start   device int32 [B+1]    out
  *   k_out, v_out   device bf16 [n_rows][Hkv][d], 32-byte aligned; must not overlap
  *              k_new or v_new
@@ -906,14 +908,16 @@ OASIS_API oasis_status oasis_read_kv_q8(const oasis_paged_shape* shape, const vo
                                         const float* kv_scale, const int32_t* block_table,
                                         const int32_t* ctx_len, const void* k_new, size_t k_stride,
                                         const void* v_new, size_t v_stride, const int32_t* new_start,
-                                        int32_t n_new, int32_t* kv_start, void* k_out, void* v_out,
-                                        int32_t n_rows, uint32_t* err_word, oasis_stream_t stream);
+                                        int32_t n_new, int32_t only_new, int32_t* kv_start,
+                                        void* k_out, void* v_out, int32_t n_rows,
+                                        uint32_t* err_word, oasis_stream_t stream);
 OASIS_API oasis_status oasis_read_kv_q4(const oasis_paged_shape* shape, const void* kv_pages,
                                         const void* kv_scale, const int32_t* block_table,
                                         const int32_t* ctx_len, const void* k_new, size_t k_stride,
                                         const void* v_new, size_t v_stride, const int32_t* new_start,
-                                        int32_t n_new, int32_t* kv_start, void* k_out, void* v_out,
-                                        int32_t n_rows, uint32_t* err_word, oasis_stream_t stream);
+                                        int32_t n_new, int32_t only_new, int32_t* kv_start,
+                                        void* k_out, void* v_out, int32_t n_rows,
+                                        uint32_t* err_word, oasis_stream_t stream);
 
 /*
  * Causal attention of new rows that continue a context.  Sequence b owns query rows

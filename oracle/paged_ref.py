@@ -256,8 +256,8 @@ def store_q4(kv, scale, k, v, slots):
 
 
 # ------------------------------------------------------------------ read-back, prompts that continue a context
-def read(values, table, ctx, n_rows, new=None):
-    """values float64 [n_pages][Hkv][2][16][128], new: (k, v, row_start) or None.
+def read(values, table, ctx, n_rows, new=None, only_new=False):
+    """values float64 [n_pages][Hkv][2][16][128], new: (k, v, row_start) or None; only_new: of requests with new rows.
     (k, v, kv_start, error bits): rows that are not written are NaN."""
     B, hkv, bits = table.shape[0], values.shape[1], 0
     k, v = np.full((n_rows, hkv, D), np.nan), np.full((n_rows, hkv, D), np.nan)
@@ -269,6 +269,8 @@ def read(values, table, ctx, n_rows, new=None):
             a, z = int(new[2][b]), int(new[2][b + 1])
             if a < 0 or z < a or z > len(new[0]):
                 bits, a, z = bits | 8, 0, 0
+        if only_new and z == a:
+            n = 0
         first, end = end, end + n + z - a
         if end > n_rows:
             bits |= 8

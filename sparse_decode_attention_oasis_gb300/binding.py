@@ -117,8 +117,8 @@ _SIGS = {
                           ctypes.c_int),
     "oasis_paged_decode_attn_q4": ([_PS, _VP, ctypes.c_size_t, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int32,
                                     ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP, _VP], ctypes.c_int),
-    **{f"oasis_read_kv_{bits}": ([_PS, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP,
-                                  _VP, _VP, ctypes.c_int32, _VP, _VP], ctypes.c_int) for bits in ("q8", "q4")},
+    **{f"oasis_read_kv_{bits}": ([_PS, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32,
+                                  ctypes.c_int32, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP], ctypes.c_int) for bits in ("q8", "q4")},
     "oasis_resume_attn_workspace_bytes": ([_PS], ctypes.c_size_t),
     "oasis_resume_attn": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP,
                            ctypes.c_int32, ctypes.c_float, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, _VP], ctypes.c_int),
@@ -454,22 +454,22 @@ def oasis_paged_decode_attn_q4(shape: PagedShape, q, q_stride: int, kv_pages, kv
 
 
 def oasis_read_kv_q8(shape: PagedShape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride: int, v_new,
-                     v_stride: int, new_start, n_new: int, kv_start, k_out, v_out, n_rows: int, err_word=None,
-                     stream=None):
+                     v_stride: int, new_start, n_new: int, only_new: int, kv_start, k_out, v_out, n_rows: int,
+                     err_word=None, stream=None):
     """Held tokens of 8-bit pages as packed bf16 rows, each request's new rows behind them."""
     _check("oasis_read_kv_q8", load().oasis_read_kv_q8(
         ctypes.byref(shape), _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len), _ptr(k_new), k_stride,
-        _ptr(v_new), v_stride, _ptr(new_start), n_new, _ptr(kv_start), _ptr(k_out), _ptr(v_out), n_rows,
+        _ptr(v_new), v_stride, _ptr(new_start), n_new, only_new, _ptr(kv_start), _ptr(k_out), _ptr(v_out), n_rows,
         _ptr(err_word), _stream(stream)))
 
 
 def oasis_read_kv_q4(shape: PagedShape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride: int, v_new,
-                     v_stride: int, new_start, n_new: int, kv_start, k_out, v_out, n_rows: int, err_word=None,
-                     stream=None):
+                     v_stride: int, new_start, n_new: int, only_new: int, kv_start, k_out, v_out, n_rows: int,
+                     err_word=None, stream=None):
     """Held tokens of 4-bit pages as packed bf16 rows, each request's new rows behind them."""
     _check("oasis_read_kv_q4", load().oasis_read_kv_q4(
         ctypes.byref(shape), _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len), _ptr(k_new), k_stride,
-        _ptr(v_new), v_stride, _ptr(new_start), n_new, _ptr(kv_start), _ptr(k_out), _ptr(v_out), n_rows,
+        _ptr(v_new), v_stride, _ptr(new_start), n_new, only_new, _ptr(kv_start), _ptr(k_out), _ptr(v_out), n_rows,
         _ptr(err_word), _stream(stream)))
 
 

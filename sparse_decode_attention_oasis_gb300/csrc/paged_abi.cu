@@ -23,7 +23,8 @@ cudaError_t launch_paged_decode_attn_q4(const PagedShape&, const uint16_t*, size
                                         const int*, const int*, const int*, const int*, int, float, void*, uint16_t*,
                                         unsigned*, cudaStream_t);
 cudaError_t launch_read_kv(int, const PagedShape&, const uint8_t*, const void*, const int*, const int*, const uint16_t*, size_t,
-                           const uint16_t*, size_t, const int*, int, int*, uint16_t*, uint16_t*, int, unsigned*, cudaStream_t);
+                           const uint16_t*, size_t, const int*, int, bool, int*, uint16_t*, uint16_t*, int, unsigned*,
+                           cudaStream_t);
 size_t resume_workspace_bytes();
 cudaError_t launch_resume_attn(const PagedShape&, const uint16_t*, size_t, const uint16_t*, size_t, const uint16_t*, size_t,
                                const int*, int, const int*, int, float, void*, uint16_t*, size_t, unsigned*, cudaStream_t);
@@ -111,8 +112,8 @@ void check_decode(Call* c, const PagedShape& s, const void* q, size_t q_stride, 
 
 oasis_status read_kv(const char* fn, int bits, const oasis_paged_shape* shape, const void* kv_pages, const void* kv_scale,
                      const int32_t* block_table, const int32_t* ctx_len, const void* k_new, size_t k_stride,
-                     const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new, int32_t* kv_start,
-                     void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word, oasis_stream_t stream) {
+                     const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new, int32_t only_new,
+                     int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word, oasis_stream_t stream) {
   Call c;
   const PagedShape s = check_shape(shape, &c);
   c.refuse(n_rows < 0 || n_rows > (1 << 28) || n_new < 0 || n_new > (1 << 28), "n_rows and n_new must be in [0, 2^28]");
@@ -129,8 +130,8 @@ oasis_status read_kv(const char* fn, int bits, const oasis_paged_shape* shape, c
   cudaError_t e = cudaSuccess;
   if (c.status == OASIS_OK)
     e = oasis::launch_read_kv(bits, s, (const uint8_t*)kv_pages, kv_scale, block_table, ctx_len, (const uint16_t*)k_new, k_stride,
-                              (const uint16_t*)v_new, v_stride, new_start, n_new, kv_start, (uint16_t*)k_out,
-                              (uint16_t*)v_out, n_rows, err_word, (cudaStream_t)stream);
+                              (const uint16_t*)v_new, v_stride, new_start, n_new, only_new != 0, kv_start,
+                              (uint16_t*)k_out, (uint16_t*)v_out, n_rows, err_word, (cudaStream_t)stream);
   return finish(fn, c, e);
 }
 
@@ -272,19 +273,19 @@ oasis_status oasis_paged_decode_attn_q4(const oasis_paged_shape* shape, const vo
 oasis_status oasis_read_kv_q8(const oasis_paged_shape* shape, const void* kv_pages, const float* kv_scale,
                               const int32_t* block_table, const int32_t* ctx_len, const void* k_new, size_t k_stride,
                               const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new,
-                              int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word,
+                              int32_t only_new, int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word,
                               oasis_stream_t stream) {
   return read_kv("oasis_read_kv_q8", 8, shape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride, v_new, v_stride,
-                 new_start, n_new, kv_start, k_out, v_out, n_rows, err_word, stream);
+                 new_start, n_new, only_new, kv_start, k_out, v_out, n_rows, err_word, stream);
 }
 
 oasis_status oasis_read_kv_q4(const oasis_paged_shape* shape, const void* kv_pages, const void* kv_scale,
                               const int32_t* block_table, const int32_t* ctx_len, const void* k_new, size_t k_stride,
                               const void* v_new, size_t v_stride, const int32_t* new_start, int32_t n_new,
-                              int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word,
+                              int32_t only_new, int32_t* kv_start, void* k_out, void* v_out, int32_t n_rows, uint32_t* err_word,
                               oasis_stream_t stream) {
   return read_kv("oasis_read_kv_q4", 4, shape, kv_pages, kv_scale, block_table, ctx_len, k_new, k_stride, v_new, v_stride,
-                 new_start, n_new, kv_start, k_out, v_out, n_rows, err_word, stream);
+                 new_start, n_new, only_new, kv_start, k_out, v_out, n_rows, err_word, stream);
 }
 
 oasis_status oasis_prompt_attn(const oasis_paged_shape* shape, const void* q, size_t q_stride, const void* k,

@@ -32,6 +32,7 @@ struct Args {
   size_t k_stride, v_stride;
   const int* new_start;  // NULL: no new rows
   int n_new;
+  bool only_new;  // requests without new rows have no rows at all
   int* kv_start;
   uint16_t *k_out, *v_out;
   int n_rows;
@@ -56,6 +57,7 @@ __device__ __forceinline__ Request request(const PagedShape& s, const Args& a, i
       r.fresh = to - from;
     }
   }
+  if (a.only_new && r.fresh == 0) r.held = 0;
   return r;
 }
 
@@ -284,9 +286,10 @@ static cudaError_t launch(const PagedShape& s, const Args& a, cudaStream_t strea
 
 cudaError_t launch_read_kv(int bits, const PagedShape& s, const uint8_t* pages, const void* scales, const int* table,
                            const int* ctx, const uint16_t* k_new, size_t k_stride, const uint16_t* v_new, size_t v_stride,
-                           const int* new_start, int n_new, int* kv_start, uint16_t* k_out, uint16_t* v_out, int n_rows,
+                           const int* new_start, int n_new, bool only_new, int* kv_start, uint16_t* k_out, uint16_t* v_out, int n_rows,
                            unsigned* err, cudaStream_t stream) {
-  const Args a{pages, scales, table, ctx, k_new, v_new, k_stride, v_stride, new_start, n_new, kv_start, k_out, v_out, n_rows, err};
+  const Args a{pages, scales, table, ctx, k_new, v_new, k_stride, v_stride, new_start, n_new,
+               only_new, kv_start, k_out, v_out, n_rows, err};
   return bits == 8 ? launch<8>(s, a, stream) : launch<4>(s, a, stream);
 }
 

@@ -29,7 +29,7 @@ A prompt's pass, layer by layer, and a decode step::
 
 A prompt that continues a context attends what its request holds as well as itself::
 
-    plan = cache.extend(cache.lens + more, n_rows)     # held: at least the tokens held in all
+    plan = cache.extend(cache.lens + more, n_rows)     # held: at least the tokens that these requests hold in all
     out = cache.resume(q, k, v, plan, held, layer)     # before commit
     cache.store(k, v, plan.slot_map, layer)
     cache.commit(plan)
@@ -91,8 +91,10 @@ def _rows(name: str, t: torch.Tensor, heads: int, n: int, device) -> int:
     if t.dtype is not _BF16 or t.shape != (n, heads, D) or t.device != device:
         raise ValueError(f"{name} must be bfloat16 [{n}, {heads}, {D}] on {device}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
+    if n == 0:
+        return heads * D
     stride, inner, one = t.stride()
-    if n <= 1:
+    if n == 1:
         stride = heads * D
     if one != 1 or (inner != D and heads > 1) or stride < heads * D or stride % 8:
         raise ValueError(f"{name}: a row's heads and dimensions must be contiguous, rows a multiple of 8 elements "
@@ -342,14 +344,16 @@ class PagedKV:
             B._check(f"oasis_paged_decode_attn_q{self.bits}", st)
         return out
 
-    def read(self, n_rows: int, ctx_len: Optional[torch.Tensor] = None, layer: int = 0, new=None, out=None) -> Rows:
+    def read(self, n_rows: int, ctx_len: Optional[torch.Tensor] = None, layer: int = 0, new=None, out=None,
+             only_new: bool = False) -> Rows:
         """The first ctx_len tokens of every request (lens by default) as packed bf16 rows, at most n_rows
         of them; stored values are bf16 exactly.  new = (k, v, row_start) puts the rows row_start[b] ..
-        row_start[b+1] - 1 of k and v [rows, Hkv, 128] behind request b's.  out = (k, v): contiguous bf16
+        row_start[b+1] - 1 of k and v [rows, Hkv, 128] behind request b's; with only_new requests without new
+        rows have no rows at all.  out = (k, v): contiguous bf16
         [n_rows, Hkv, 128] to write to; rows behind the last request's are left as they are."""
         if _current_device() != self._index:
             with torch.cuda.device(self._index):
-                return self.read(n_rows, ctx_len, layer, new, out)
+                return self.read(n_rows, ctx_len, layer, new, out, only_new)
         b, h, device = self.batch, self.n_kv_heads, self.device
         ctx_len = _ints("ctx_len", self.lens if ctx_len is None else ctx_len, (b,), device)
         if not 0 <= layer < self.layers:
@@ -376,7 +380,7 @@ class PagedKV:
         lib = B._lib or B.load()
         st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
             self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
-            self.table.data_ptr(), ctx_len.data_ptr(), k_at, ks, v_at, vs, start_at, n_new, kv_start.data_ptr(),
+            self.table.data_ptr(), ctx_len.data_ptr(), k_at, ks, v_at, vs, start_at, n_new, only_new, kv_start.data_ptr(),
             out[0].data_ptr(), out[1].data_ptr(), n_rows, self.err.data_ptr(), _current_stream(self._index))
         if st:
             B._check(f"oasis_read_kv_q{self.bits}", st)
@@ -386,10 +390,11 @@ class PagedKV:
                scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Causal attention of a plan's rows over what their requests hold (lens, before the plan's commit) and
         over each other: q [rows, Hq, 128], k and v [rows, Hkv, 128] in bf16.  n_held: at least the tokens
-        that the requests hold in all, which sizes the scratch (a request that does not fit is reported to
-        :meth:`check` and its rows stay as they are).  Rows of no request stay as they are in out (zero where
-        out is allocated here).  The held tokens are read back from the pages (:meth:`read`), the new ones
-        are taken as given; whether they are stored before or after makes no difference."""
+        that the requests with new rows hold in all, which sizes the scratch (a request that does not fit is
+        reported to :meth:`check`; its rows and those of requests behind it stay as they are).  Rows of no
+        request stay as they are in out (zero where out is allocated here).  The held tokens are read back from
+        the pages (:meth:`read`), the new ones are taken as given: call it before :meth:`store`, which in 8
+        bits may round a page's earlier tokens again, and before :meth:`commit`."""
         if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.resume(q, k, v, plan, n_held, layer, scale, out)
@@ -416,8 +421,8 @@ class PagedKV:
         lib, stream, err = B._lib or B.load(), _current_stream(self._index), self.err.data_ptr()
         st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
             self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
-            self.table.data_ptr(), self.lens.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, row_start, n, start_at, k_at, v_at,
-            m, err, stream)
+            self.table.data_ptr(), self.lens.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, row_start, n, 1, start_at, k_at,
+            v_at, m, err, stream)
         if st:
             B._check(f"oasis_read_kv_q{self.bits}", st)
         st = lib.oasis_resume_attn(

@@ -29,7 +29,7 @@ def _compare(rows, want, guard=None):
             assert (got[n:] == guard).all()
 
 
-def _run(bits, ctx, new=None, hkv=2, pad=0, n_rows=None, seed=0, table=None):
+def _run(bits, ctx, new=None, hkv=2, pad=0, n_rows=None, seed=0, table=None, only_new=False):
     from paged_helpers import bf16, ints, shuffled_table
     from q4_helpers import pages_and_cache
 
@@ -47,8 +47,8 @@ def _run(bits, ctx, new=None, hkv=2, pad=0, n_rows=None, seed=0, table=None):
         total += int(start[-1])
     n_rows = total + 3 if n_rows is None else n_rows
     out = tuple(torch.full((n_rows, hkv, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    rows = c.read(n_rows, ints(ctx), new=fresh, out=out)
-    want = ref.read(values, table, ctx, n_rows, fresh64)
+    rows = c.read(n_rows, ints(ctx), new=fresh, out=out, only_new=only_new)
+    want = ref.read(values, table, ctx, n_rows, fresh64, only_new)
     _compare(rows, want, 7.0)
     assert rows.k is out[0] and int(c.err) == want[3]
     return c
@@ -78,6 +78,14 @@ def test_a_long_read(bits):
 @pytest.mark.parametrize("n_rows", [0, 1, 39, 40, 41, 59, 60, 89])
 def test_requests_that_do_not_fit_get_nothing(n_rows):
     _run(4, [30, 10, 5, 0], [10, 10, 20, 5], n_rows=n_rows)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_only_requests_with_new_rows(bits):
+    _run(bits, [300, 20, 0, 17, 5], [0, 3, 0, 1, 0], only_new=True)
+    _run(bits, [300, 20], [0, 0], only_new=True, n_rows=4)
+    _run(bits, [300, 20], only_new=True, n_rows=1)
+    _run(bits, list(range(600)), [i % 7 // 6 for i in range(600)], hkv=1, only_new=True)
 
 
 def test_bad_pages_and_lengths():

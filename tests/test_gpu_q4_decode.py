@@ -234,6 +234,32 @@ def test_a_long_cache_past_32_bit_offsets():
     assert (rows.k.double().cpu().numpy() == want[0]).all() and (rows.v.double().cpu().numpy() == want[1]).all()
 
 
+def test_pages_past_2_to_the_26():
+    """A pool of 67 million pages of one head (155 GB): written, attended and read back at its end."""
+    from paged_helpers import F16_HALF_STEP, bf16, check_attention, ints
+    from sparse_decode_attention_oasis_gb300.paged import PagedKV
+
+    n_pages = 2 ** 26 + 40
+    if torch.cuda.mem_get_info()[0] < 170e9:
+        pytest.skip("less than 170 GB free")
+    rng = np.random.default_rng(19)
+    c = PagedKV(n_pages=n_pages, batch=1, nb_max=6, n_q_heads=2, n_kv_heads=1, bits=4)
+    pages = [n_pages - 1, 2 ** 26, 2 ** 25 + 3, n_pages - 2, 5, 2 ** 26 - 1]
+    c.table.copy_(ints([pages]))
+    k, k64 = bf16(rng, (90, 1, 128))
+    v, v64 = bf16(rng, (90, 1, 128))
+    c.store(k, v, ints([pages[t // 16] * 16 + t % 16 for t in range(90)]))
+    kv, scale, _ = ref.store_q4(np.zeros((6, 1, 2, 16, 64), np.uint8), np.zeros((6, 1, 2, 128), np.uint8), k64, v64, range(90))
+    q, q64 = bf16(rng, (1, 2, 128))
+    want = ref.decode_q4(q64, kv, scale, np.arange(6)[None], [90], SCALE)
+    check_attention(c.decode(q, ints([90])).double().cpu().numpy(), want[0], want[1], want[2], F16_HALF_STEP, want[3])
+    rows = c.read(90, ints([90]))
+    assert (rows.k.double().cpu().numpy() == ref.read(ref.values_q4(kv, scale), np.arange(6)[None], [90], 90)[0]).all()
+    c.check()
+    del c
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("wide", [False, True])
 def test_two_captured_graphs_replayed_with_other_lengths(wide):
     from paged_helpers import F16_HALF_STEP, check_attention, ints

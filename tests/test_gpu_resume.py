@@ -220,6 +220,8 @@ def test_through_the_cache(bits):
             got = out.double().cpu().numpy()
             check_attention(got[mine], want[mine], mass[mine], size[mine], BF16_HALF_STEP)
             assert (got[~mine] == 0).all()
+            few = c.resume(q, k, v, plan, int(lens[np.asarray(grow) > 0].sum()), layer)  # the others' tokens need no room
+            assert torch.equal(few, out)
             c.store(k, v, plan.slot_map, layer)
             d, d64 = bf16(rng, (3, hkv * G, 128))
             step = c.decode(d, plan.lens, layer).double().cpu().numpy()

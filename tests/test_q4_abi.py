@@ -28,10 +28,10 @@ def _decode(lib, s, q=16, qs=4096, kv=16, sc=16, table=16, ctx=16, sel=None, nse
                                           out, err, None)
 
 
-def _read(lib, s, kv=16, sc=16, table=16, ctx=16, k=16, ks=1024, v=16, vs=1024, new=16, n_new=3, start=16, ko=32, vo=32, n=5,
-          err=None, bits=4):
+def _read(lib, s, kv=16, sc=16, table=16, ctx=16, k=16, ks=1024, v=16, vs=1024, new=16, n_new=3, only=0, start=16, ko=32, vo=32,
+          n=5, err=None, bits=4):
     call = lib.oasis_read_kv_q4 if bits == 4 else lib.oasis_read_kv_q8
-    return call(ctypes.byref(s), kv, sc, table, ctx, k, ks, v, vs, new, n_new, start, ko, vo, n, err, None)
+    return call(ctypes.byref(s), kv, sc, table, ctx, k, ks, v, vs, new, n_new, only, start, ko, vo, n, err, None)
 
 
 def _resume(lib, s, q=16, qs=4096, k=16, ks=1024, v=16, vs=1024, start=16, n=5, kstart=16, m=9, scale=0.1, ws=32, nb=1 << 30,

@@ -122,11 +122,14 @@ struct Tail {
 struct Parts {
   const int* kv_start;
   int n_kv_rows;
-  float* o;       // [blocks][2][2 * kTile][kD], not divided
+  float* o;       // [blocks][2][kD / 8][2 * kTile][8], not divided: what a warp's 32 rows store at once lies together
   float2* stats;  // [blocks][2][2 * kTile]: reference and sum of a row
   Tail* tails;    // [blocks]
   __device__ __forceinline__ size_t row(int block, int place, int r) const {
     return ((size_t)block * 2 + place) * (2 * kTile) + r;
+  }
+  __device__ __forceinline__ float* o_at(int block, int place, int r, int c) const {  // dimensions c .. of 8 * (c / 8) + 7
+    return o + ((((size_t)block * 2 + place) * (kD / 8) + c / 8) * (2 * kTile) + r) * 8 + c % 8;
   }
 };
 
@@ -292,6 +295,7 @@ __device__ __forceinline__ int kv_tiles(const Piece& it, int i, int per) {  // t
 // (the ones with the most keys) first, so that every block gets an equal share; more sequences are
 // walked in their order, 32 at a time.
 struct Schedule {
+  using Cost = int;  // none
   static constexpr int kKept = 10;  // sequences to a lane
   const int* row_start;
   int B, n_rows, pair;              // pair: tokens of an item
@@ -405,24 +409,27 @@ struct Schedule {
   }
 };
 
-// The items of a call with keys before its new rows, cut into equal ranges of cost for the thread blocks: cost in keys,
-// past + the keys of the item's last row (whole tiles of rows) + kItemCost for its ends, and an eighth less for an item
-// whose second query tile has no token (measured: 1.3 us for a K/V tile and both query tiles, 1.1 for one, 2.8 to 3.9 for an
-// item's ends, 1.3 us being 128 keys).  A sequence's items follow each other head by head; an item that crosses a range's
-// border is cut at a tile there (not one tile from its ends).
-struct Ranges {
-  static constexpr long long kItemCost = 400, kLeast = 512;  // least cost of a block's range
+// A call with keys before its new rows: its sequences, and what their items cost in keys: past + the keys of the item's last
+// row (whole tiles of rows) + kItemCost for its ends, and an eighth less for an item whose second query tile has no token
+// (measured: 1.3 us for a K/V tile and both query tiles, 1.1 for one, 2.8 to 3.9 for an item's ends, 1.3 us being 128 keys).
+struct Sequences {
+  static constexpr int kItemCost = 400;
   const int *q_start, *kv_start;
   int B, n_rows, n_kv_rows, pair, per, heads, lane;
   unsigned bits;
-  long long lo, hi;        // this block's range
-  long long share, extra;  // all ranges: `extra` of them are one longer than `share`
-  // the sequence at hand
-  int b, a, len, kv0, past;
-  long long start, of_head;  // where it begins, a head's cost
-  int h, place;              // the next item
-  long long at;              // where it begins
 
+  __device__ void set(const int* qs, const Parts& parts, int b, int rows, int tokens, int hkv, int ln) {
+    q_start = qs;
+    kv_start = parts.kv_start;
+    B = b;
+    n_rows = rows;
+    n_kv_rows = parts.n_kv_rows;
+    per = tokens;
+    pair = 2 * tokens;
+    heads = hkv;
+    lane = ln;
+    bits = 0;
+  }
   __device__ bool sequence(int s, int& qa, int& n, int& ka, int& before) {
     qa = q_start[s];
     n = q_start[s + 1] - qa;
@@ -436,65 +443,87 @@ struct Ranges {
     }
     return n > 0;
   }
-  __device__ long long before_place(int p, int keys) const {  // cost of a head's items before place p
-    return (long long)p * (keys + kItemCost) + (long long)pair * ((long long)p * (p + 1) / 2);
+  template <class C>
+  __device__ C before_place(int p, int keys) const {  // cost of a head's items before place p
+    return (C)p * (C)(keys + kItemCost) + (C)pair * ((C)p * (C)(p + 1) / 2);
   }
   // The item at place p of a sequence with n rows.
-  __device__ long long item_cost(int p, int n, int keys) const {
-    const long long c = keys + kItemCost + (long long)(p + 1) * pair;
-    return (long long)p * pair + per >= n ? c - c / 8 : c;
+  template <class C>
+  __device__ C item_cost(int p, int n, int keys) const {
+    const C c = (C)(keys + kItemCost) + (C)(p + 1) * (C)pair;
+    return p * pair + per >= n ? c - c / 8 : c;
   }
-  __device__ long long head_cost(int n, int keys) const {
+  template <class C>
+  __device__ C head_cost(int n, int keys) const {
     const int last = (n - 1) / pair;
-    return before_place(last, keys) + item_cost(last, n, keys);
+    return before_place<C>(last, keys) + item_cost<C>(last, n, keys);
   }
-
-  // gives the number of blocks that have a range
-  __device__ int init(const int* qs, const Parts& parts, int b_, int rows, int tokens, int hkv, int ln) {
-    q_start = qs;
-    kv_start = parts.kv_start;
-    B = b_;
-    n_rows = rows;
-    n_kv_rows = parts.n_kv_rows;
-    per = tokens;
-    pair = 2 * tokens;
-    heads = hkv;
-    lane = ln;
-    bits = 0;
-    long long total = 0, of_first = 0;  // of_first: sequence `lane`
+  // The cost of all items; of_lane: of sequence `lane`; items: how many there are, at most 2^25.
+  __device__ long long cost(long long* of_lane, unsigned* items) {
+    long long total = 0;
+    unsigned many = 0;
+    *of_lane = 0;
 #pragma unroll 4
     for (int s = lane; s < B; s += 32) {
       int qa, n, ka, before;
-      const long long c = sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0;
+      const long long c = sequence(s, qa, n, ka, before) ? heads * head_cost<long long>(n, before) : 0;
       total += c;
-      if (s == lane) of_first = c;
+      many = min(many + (unsigned)(heads * ((n + pair - 1) / pair)), 1u << 20);
+      if (s == lane) *of_lane = c;
     }
+    *items = __reduce_add_sync(0xffffffffu, many);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const long long most = (total + kLeast - 1) / kLeast;
-    const int blocks = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
+    return total;
+  }
+};
+
+// The items cut into equal ranges of cost for the thread blocks.  A sequence's items follow each other head by head; an item
+// that crosses a range's border is cut at a tile there (not one tile from its ends).  There are as many ranges as pieces of
+// kLeast keys fit, or as items if they are more (items of short requests then have an SM each: 13.0 -> 11.3 us), at most one
+// to an SM.  kLeast 256, 448 and 768 take 30.5, 29.7 and 29.4 us for 45 rows after 6,000 tokens, 512 28.2.
+// C: unsigned where the cost of all items is below 2^31, else long long.  This arithmetic lies before a block's first load:
+// with 64 bits alone eight requests take 151 us against 149, 2,048 rows after 30,000 tokens 660 against 649.
+constexpr int kLeast = 512;  // least cost of a block's range, where there are no more items than such ranges
+template <class C>
+struct Ranges : Sequences {
+  using Cost = C;
+  C lo, hi;        // this block's range
+  C share, extra;  // all ranges: `extra` of them are one longer than `share`
+  // the sequence at hand
+  int b, a, len, kv0, past;
+  C start, of_head;  // where it begins, a head's cost
+  int h, place;      // the next item
+  C at;              // where it begins
+
+  __device__ Ranges() {}
+  __device__ explicit Ranges(const Sequences& s) : Sequences(s) {}
+  // total, of_lane, items: of Sequences::cost
+  __device__ void init(C total, C of_lane, unsigned items) {
+    const C pieces = (total + (kLeast - 1)) / kLeast, most = pieces < (C)items ? (C)items : pieces;
+    const int blocks = most < (C)gridDim.x ? (int)most : (int)gridDim.x;
     lo = hi = at = 0;
     len = 0;
-    if ((int)blockIdx.x >= blocks) return blocks;
-    share = total / blocks;
-    extra = total % blocks;
+    if ((int)blockIdx.x >= blocks) return;
+    share = total / (C)blocks;
+    extra = total - share * (C)blocks;
     lo = begin_of(blockIdx.x);
     hi = begin_of(blockIdx.x + 1);
     // the sequence that holds cost lo
     start = 0;
     for (int w = 0;; w += 32) {
       const int s = w + lane;
-      long long c = of_first;
+      C c = of_lane;
       if (w > 0) {
         int qa, n, ka, before;
-        const unsigned keep = bits;  // reported by the pass above
-        c = s < B && sequence(s, qa, n, ka, before) ? heads * head_cost(n, before) : 0;
+        const unsigned keep = bits;  // reported with the cost
+        c = s < B && sequence(s, qa, n, ka, before) ? (C)heads * head_cost<C>(n, before) : 0;
         bits = keep;
       }
-      long long x = c;
+      C x = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const C y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       const unsigned over = __ballot_sync(0xffffffffu, start + x > lo);
@@ -507,19 +536,18 @@ struct Ranges {
       start += __shfl_sync(0xffffffffu, x, 31);
     }
     h = (int)((lo - start) / of_head);
-    const long long rest = lo - start - h * of_head;
+    const C rest = lo - start - (C)h * of_head;
     int p0 = 0, p1 = (len + pair - 1) / pair - 1;  // the last place that begins at or before it
     while (p0 < p1) {
       const int m = (p0 + p1 + 1) >> 1;
-      if (before_place(m, past) <= rest) p0 = m; else p1 = m - 1;
+      if (before_place<C>(m, past) <= rest) p0 = m; else p1 = m - 1;
     }
     place = p0;
-    at = start + h * of_head + before_place(place, past);
-    return blocks;
+    at = start + (C)h * of_head + before_place<C>(place, past);
   }
-  __device__ long long begin_of(int block) const { return block * share + min((long long)block, extra); }
-  __device__ int block_of(long long cost) const {
-    const long long longer = extra * (share + 1);
+  __device__ C begin_of(int block) const { return (C)block * share + ((C)block < extra ? (C)block : extra); }
+  __device__ int block_of(C cost) const {
+    const C longer = extra * (share + 1);
     return (int)(cost < longer ? cost / (share + 1) : extra + (cost - longer) / share);
   }
   __device__ void take_sequence(int s) {
@@ -527,17 +555,18 @@ struct Ranges {
     const unsigned keep = bits;
     sequence(s, a, len, kv0, past);
     bits = keep;
-    of_head = len > 0 ? head_cost(len, past) : 0;
+    of_head = len > 0 ? head_cost<C>(len, past) : 0;
     h = place = 0;
   }
   // The tile at which a border inside an item cuts it, `cost` behind its beginning; half: its second query tile is empty.
-  __device__ int cut(long long cost, int tiles, bool half) const {
-    const int j = (int)min(max((half ? cost + cost / 7 : cost) - kItemCost, 0ll) / kTile, (long long)tiles);
+  __device__ int cut(int cost, int tiles, bool half) const {
+    const int j = min(max((half ? cost + cost / 7 : cost) - kItemCost, 0) / kTile, tiles);
     return j < 2 ? 0 : tiles - j < 2 ? tiles : j;
   }
-  // This block's next part (row0 -1: there are no more).  tail: of an item that goes on behind this block's range.
-  __device__ Piece next(int* last) {
-    *last = -1;
+  // This block's next part (row0 -1: there are no more).  end: where its item ends, of one that goes on behind this block's
+  // range and begins in it, else 0.
+  __device__ Piece next(C* end) {
+    *end = 0;
     while (at < hi) {
       Piece it;
       it.row0 = a;
@@ -548,9 +577,9 @@ struct Ranges {
       it.past = past;
       const int tiles = max(tiles_of(it, 0, per), tiles_of(it, 1, per));
       const bool half = it.tok0 + per >= len;
-      const long long from = at, to = start + h * of_head + before_place(place, past) + item_cost(place, len, past);
+      const C from = at, to = start + (C)h * of_head + before_place<C>(place, past) + item_cost<C>(place, len, past);
       at = to;
-      if (++place * (long long)pair >= len) {
+      if (++place * pair >= len) {
         place = 0;
         if (++h == heads) {
           h = 0;
@@ -559,11 +588,11 @@ struct Ranges {
           while (len == 0 && at < hi) take_sequence(b + 1);  // below hi there is another one
         }
       }
-      it.j0 = from < lo ? cut(lo - from, tiles, half) : 0;
-      it.j1 = to > hi ? cut(hi - from, tiles, half) : tiles;
+      it.j0 = from < lo ? cut((int)(lo - from), tiles, half) : 0;
+      it.j1 = to > hi ? cut((int)(hi - from), tiles, half) : tiles;
       it.whole = it.j0 == 0 && it.j1 == tiles;
       if (it.j0 >= it.j1) continue;
-      if (it.j0 == 0 && !it.whole) *last = block_of(to - 1);
+      if (it.j0 == 0 && !it.whole) *end = to;
       return it;
     }
     Piece none = {};
@@ -578,16 +607,23 @@ template <class It>
 __device__ __noinline__ void give_back(int sequences, int heads, int G, const int* row_start, int n_rows, const uint16_t* v,
                                        size_t v_stride, uint16_t* out, size_t out_stride, Parts parts) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = kTile / G, tokens = 2 * per;
-  std::conditional_t<std::is_same_v<It, Item>, Schedule, Ranges> sch;
-  if constexpr (std::is_same_v<It, Item>) sch.init(row_start, sequences, n_rows, tokens, lane);
-  else sch.init(row_start, parts, sequences, n_rows, per, heads, lane);
+  std::conditional_t<std::is_same_v<It, Item>, Schedule, Ranges<long long>> sch;
+  if constexpr (std::is_same_v<It, Item>) {
+    sch.init(row_start, sequences, n_rows, tokens, lane);
+  } else {
+    sch.set(row_start, parts, sequences, n_rows, per, heads, lane);
+    long long of_lane;
+    unsigned items;
+    const long long total = sch.cost(&of_lane, &items);
+    sch.init(total, of_lane, items);
+  }
   for (int k = 0;; ++k) {
     It it;
     if constexpr (std::is_same_v<It, Item>) {
       it = sch.item(k, heads);
     } else {
-      int last;
-      it = sch.next(&last);
+      long long end;
+      it = sch.next(&end);
     }
     if (it.row0 < 0) return;
     if (k % 8 != warp) continue;
@@ -608,7 +644,7 @@ __device__ __noinline__ void give_back(int sequences, int heads, int G, const in
         if constexpr (!std::is_same_v<It, Item>) {
           if (!it.whole) {
             const int i = (t - it.tok0) / per, r = i * kTile + (t - it.tok0 - i * per) * G + g;
-            float4* dst = reinterpret_cast<float4*>(parts.o + parts.row(blockIdx.x, it.j0 == 0, r) * kD) + lane;
+            float4* dst = reinterpret_cast<float4*>(parts.o_at(blockIdx.x, it.j0 == 0, r, lane * 4));
             const float4 o = *dst;
             *dst = make_float4(o.x + sum[0], o.y + sum[1], o.z + sum[2], o.w + sum[3]);
             continue;
@@ -623,23 +659,19 @@ __device__ __noinline__ void give_back(int sequences, int heads, int G, const in
   }
 }
 
-// The scheduler warp: hands out the block's items, and looks over the V tiles with tokens that not all rows of an item
-// attend.  False: a wait gave up.  Out of the kernel's own code (56 registers of the warp's 88): inlined, it crowded
-// the other roles, and the whole kernel took 4 to 5% longer.
-template <class It>
-__device__ __noinline__ bool schedule(Bars<It>* bars, uint8_t* ring, int sequences, int heads, int per, const int* row_start,
-                                      int n_rows, Parts parts, unsigned* err) {
+// Hands out the block's items, and looks over the V tiles with tokens that not all rows of an item attend.  False: a
+// wait gave up.
+template <class It, class Sch>
+__device__ __forceinline__ bool hand_out(Sch& sch, Bars<It>* bars, uint8_t* ring, int heads, int per, const Parts& parts,
+                                         unsigned* err) {
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
   };
   bool ok = true;
-  std::conditional_t<std::is_same_v<It, Item>, Schedule, Ranges> sch;
   Tail tail = {};
   tail.last = -1;
-  if constexpr (std::is_same_v<It, Item>) sch.init(row_start, sequences, n_rows, 2 * per, lane);
-  else sch.init(row_start, parts, sequences, n_rows, per, heads, lane);
   unsigned slot = 0, raw_uses = 0;  // ring places of the items before, uses of raw_full (odd: 1)
   // Rows behind the sequence's last token become zeros, infinities and NaN after the item's first token too.
   auto look_over = [&](const It& it) {
@@ -675,23 +707,9 @@ __device__ __noinline__ bool schedule(Bars<It>* bars, uint8_t* ring, int sequenc
   // An item's tiles are looked over when the next item is out, so that the producer need not wait for it.
   for (int k = 0;; ++k) {
     It it;
-    if constexpr (std::is_same_v<It, Item>) {
-      it = sch.item(k, heads);
-    } else {
-      int last;
-      it = sch.next(&last);
-      if (it.row0 >= 0 && !it.whole) {
-        tail.tiles[it.j0 == 0] = make_int2(it.j0, it.j1);
-        if (last >= 0) {
-          tail.row0 = it.row0;
-          tail.len = it.len;
-          tail.tok0 = it.tok0;
-          tail.h = it.h;
-          tail.past = it.past;
-          tail.last = last;
-        }
-      }
-    }
+    [[maybe_unused]] typename Sch::Cost end = 0;
+    if constexpr (std::is_same_v<It, Item>) it = sch.item(k, heads);
+    else it = sch.next(&end);
     const int st = k % kItems;
     if (!wait_all(&bars->item_empty[st], ((k / kItems) & 1) ^ 1)) {
       ok = false;
@@ -702,6 +720,19 @@ __device__ __noinline__ bool schedule(Bars<It>* bars, uint8_t* ring, int sequenc
       mbar_arrive(&bars->item_full[st]);
     }
     __syncwarp();
+    if constexpr (!std::is_same_v<It, Item>) {
+      if (it.row0 >= 0 && !it.whole) {
+        tail.tiles[it.j0 == 0] = make_int2(it.j0, it.j1);
+        if (end != 0) {
+          tail.row0 = it.row0;
+          tail.len = it.len;
+          tail.tok0 = it.tok0;
+          tail.h = it.h;
+          tail.past = it.past;
+          tail.last = sch.block_of(end - 1);
+        }
+      }
+    }
     if (k > 0 && !look_over(bars->items[(k - 1) % kItems])) {
       ok = false;
       break;
@@ -715,6 +746,33 @@ __device__ __noinline__ bool schedule(Bars<It>* bars, uint8_t* ring, int sequenc
     if (lane == 0) parts.tails[blockIdx.x] = tail;
   }
   return ok;
+}
+
+// The scheduler warp.  Out of the kernel's own code (56 registers of the warp's 88): inlined, it crowded the other roles, and
+// the whole kernel took 4 to 5% longer.
+template <class It>
+__device__ __noinline__ bool schedule(Bars<It>* bars, uint8_t* ring, int sequences, int heads, int per, const int* row_start,
+                                      int n_rows, Parts parts, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (std::is_same_v<It, Item>) {
+    Schedule sch;
+    sch.init(row_start, sequences, n_rows, 2 * per, lane);
+    return hand_out(sch, bars, ring, heads, per, parts, err);
+  } else {
+    Sequences all;
+    all.set(row_start, parts, sequences, n_rows, per, heads, lane);
+    long long of_lane;
+    unsigned items;
+    const long long total = all.cost(&of_lane, &items);
+    if (total >> 31 == 0) {
+      Ranges<unsigned> sch(all);
+      sch.init((unsigned)total, (unsigned)of_lane, items);
+      return hand_out(sch, bars, ring, heads, per, parts, err);
+    }
+    Ranges<long long> sch(all);
+    sch.init(total, of_lane, items);
+    return hand_out(sch, bars, ring, heads, per, parts, err);
+  }
 }
 
 // It: Item, or Piece where keys lie before the new rows (row_start: of the query rows, parts: the rest).
@@ -891,9 +949,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
       const float total = (a + b) + (d + e);
       if constexpr (std::is_same_v<It, Piece>) {
         if (!it.whole) {
-          const size_t at = parts.row(blockIdx.x, it.j0 == 0, i * kTile + row);
           const bool mine = row < per * G && tok < it.len;
-          if (mine) parts.stats[at] = make_float2(ref, total);
+          if (mine) parts.stats[parts.row(blockIdx.x, it.j0 == 0, i * kTile + row)] = make_float2(ref, total);
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
             uint32_t o[32];
@@ -901,7 +958,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             tmem_wait_ld();
             if (mine) {
 #pragma unroll
-              for (int q = 0; q < 32; q += 8) store32(parts.o + at * kD + c + q, o + q);
+              for (int q = 0; q < 32; q += 8) store32(parts.o_at(blockIdx.x, it.j0 == 0, i * kTile + row, c + q), o + q);
             }
           }
           tc_fence_before();
@@ -1123,66 +1180,56 @@ __device__ __forceinline__ float4 load16f(const float* p) {
   return v;
 }
 
-// kRows rows of an item to a warp, from `row` on, `step` apart: a lane has four dimensions.  tails: from the item's first block.
+// kRows rows of an item to a warp, from `row` on: neighbouring rows lie together eight dimensions at a time, so a lane has
+// four dimensions of eight in kRows places of one row.  tails: from the item's first block.
 template <int kRows>
-__device__ __forceinline__ void join_rows(const Parts& parts, const Tail* tails, int first, int row, int step, int rows, int count,
-                                          int per, int G, uint16_t* out, size_t out_stride) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void join_rows(const Parts& parts, const Tail* tails, int first, int row, int rows, int count, int per,
+                                          int G, uint16_t* out, size_t out_stride) {
+  constexpr int kPlaces = kD / 8 / kRows;  // pieces of eight dimensions that one load of the warp spans
+  const int lane = threadIdx.x & 31, mine = row + (lane >> 1) % kRows, c0 = lane / (2 * kRows) * 8 + (lane & 1) * 4;
   const Tail& tail = tails[0];
-  float top[kRows], sum[kRows];
+  const int at = min(mine, rows - 1), i = at / G / per, r = at + i * (kTile - per * G);  // behind the last row: that again
+  Piece item = {};
+  item.len = tail.len;
+  item.tok0 = tail.tok0;
+  item.past = tail.past;
+  const int tiles = tiles_of(item, i, per);
+  float top = neg_inf(), sum = 0.f;
   float4 o[kRows];
-  int r[kRows], tiles[kRows];
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int at = min(row + k * step, rows - 1), i = at / G / per;  // behind the last row: that again
-    Piece item = {};
-    item.len = tail.len;
-    item.tok0 = tail.tok0;
-    item.past = tail.past;
-    r[k] = at + i * (kTile - per * G);
-    tiles[k] = tiles_of(item, i, per);
-    top[k] = neg_inf();
-    sum[k] = 0.f;
-    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int k = 0; k < kRows; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kAtOnce = 8 / kRows;  // parts whose loads are in flight together
-  for (int c0 = 0; c0 < count; c0 += kAtOnce) {
-    float2 st[kAtOnce][kRows];
+  for (int p0 = 0; p0 < count; p0 += kAtOnce) {
+    float2 st[kAtOnce];
     float4 x[kAtOnce][kRows];
 #pragma unroll
     for (int d = 0; d < kAtOnce; ++d) {
-      const int c = min(c0 + d, count - 1);
+      const int p = min(p0 + d, count - 1);
+      st[d] = load8(parts.stats + parts.row(first + p, p == 0, r));
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const size_t at = parts.row(first + c, c == 0, r[k]);
-        st[d][k] = load8(parts.stats + at);
-        x[d][k] = load16f(parts.o + at * kD + lane * 4);
-      }
+      for (int k = 0; k < kRows; ++k) x[d][k] = load16f(parts.o_at(first + p, p == 0, r, c0 + k * kPlaces * 8));
     }
 #pragma unroll
     for (int d = 0; d < kAtOnce; ++d) {
-      const int c = min(c0 + d, count - 1);
-      const int2 part = tails[c].tiles[c == 0];
+      const int p = min(p0 + d, count - 1);
+      const int2 part = tails[p].tiles[p == 0];
+      if (p0 + d >= count || min(part.y, tiles) <= part.x) continue;  // no part, or one without tiles of this row
+      const float next = fmaxf(top, st[d].x), f0 = ex2(top - next), f1 = ex2(st[d].x - next);
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        if (c0 + d >= count || min(part.y, tiles[k]) <= part.x) continue;  // no part, or one without tiles of this row
-        const float next = fmaxf(top[k], st[d][k].x), f0 = ex2(top[k] - next), f1 = ex2(st[d][k].x - next);
+      for (int k = 0; k < kRows; ++k)
         o[k] = make_float4(fmaf(o[k].x, f0, x[d][k].x * f1), fmaf(o[k].y, f0, x[d][k].y * f1),
                            fmaf(o[k].z, f0, x[d][k].z * f1), fmaf(o[k].w, f0, x[d][k].w * f1));
-        sum[k] = fmaf(sum[k], f0, st[d][k].y * f1);
-        top[k] = next;
-      }
+      sum = fmaf(sum, f0, st[d].y * f1);
+      top = next;
     }
   }
+  if (mine >= rows) return;
+  const float inv = 1.0f / sum;
+  uint16_t* dst = out + (size_t)(tail.row0 + tail.tok0 + at / G) * out_stride + (size_t)(tail.h * G + at % G) * kD + c0;
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int at = row + k * step;
-    if (at >= rows) continue;
-    const float inv = 1.0f / sum[k];
-    *reinterpret_cast<uint2*>(out + (size_t)(tail.row0 + tail.tok0 + at / G) * out_stride +
-                              (size_t)(tail.h * G + at % G) * kD + lane * 4) =
+  for (int k = 0; k < kRows; ++k)
+    *reinterpret_cast<uint2*>(dst + k * kPlaces * 8) =
         make_uint2(pack_bf16x2(o[k].x * inv, o[k].y * inv), pack_bf16x2(o[k].z * inv, o[k].w * inv));
-  }
 }
 
 // Joins the parts of items that go on in a later block.  Every thread block lists the items (a tail to a thread); their rows
@@ -1200,7 +1247,7 @@ prompt_join_kernel(PagedShape s, Parts parts, int blocks, uint16_t* out, size_t 
     if (tails[tid].last >= 0) rows = rows_of(tails[tid]);
   }
   const int items = __syncthreads_count(rows > 0);
-  const int turns = items * 2 * kTile >= (int)gridDim.x * 2 * kJoinWarps ? 4 : 1;  // rows of a warp
+  const int turns = items * 2 * kTile >= (int)gridDim.x * 2 * kJoinWarps ? 4 : 2;  // rows of a warp
   int n = (rows + kJoinWarps * turns - 1) / (kJoinWarps * turns);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1223,11 +1270,11 @@ prompt_join_kernel(PagedShape s, Parts parts, int blocks, uint16_t* out, size_t 
       const int m = (first + hi) >> 1;
       if (unit_end[m] > u) hi = m; else first = m + 1;
     }
-    const int row = (u - (first ? unit_end[first - 1] : 0)) * kJoinWarps * turns + warp;
+    const int row = ((u - (first ? unit_end[first - 1] : 0)) * kJoinWarps + warp) * turns;
     const int all = rows_of(tails[first]), count = min(tails[first].last, blocks - 1) - first + 1;
     if (row >= all) continue;
-    if (turns == 4) join_rows<4>(parts, tails + first, first, row, kJoinWarps, all, count, per, G, out, out_stride);
-    else join_rows<1>(parts, tails + first, first, row, kJoinWarps, all, count, per, G, out, out_stride);
+    if (turns == 4) join_rows<4>(parts, tails + first, first, row, all, count, per, G, out, out_stride);
+    else join_rows<2>(parts, tails + first, first, row, all, count, per, G, out, out_stride);
   }
 }
 
@@ -1310,7 +1357,8 @@ cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_
   // blocks that the largest cost of these sizes can use: every item with all keys
   const int pair = 2 * (kTile / s.G());
   const long long items = ((long long)n_rows / pair + (s.B < n_rows ? s.B : n_rows)) * s.Hkv;
-  const long long most = (items * (Ranges::kItemCost + (long long)n_kv_rows + pair) + Ranges::kLeast - 1) / Ranges::kLeast;
+  const long long pieces = (items * (Sequences::kItemCost + (long long)n_kv_rows + pair) + kLeast - 1) / kLeast;
+  const long long most = pieces < items ? items : pieces;
   const int sms = sm_count() < kMostBlocks ? sm_count() : kMostBlocks, grid = most < sms ? (int)most : sms;
   const Parts parts = parts_of(ws, kv_start, n_kv_rows);
   // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between

@@ -81,6 +81,28 @@ def test_work_split_over_the_keys(hkv, G, past, new):
     _run(past, new, hkv, G, seed=new[0], sample=40)
 
 
+def test_items_of_more_keys_than_31_bits_count():
+    """135,000 new rows: the items of all heads have 2.3e9 keys to read between them."""
+    from paged_helpers import BF16_HALF_STEP, check_attention, ints
+
+    from sparse_decode_attention_oasis_gb300.paged import resume_attn
+
+    n, past, hkv, G = 135_000, 1_000, 8, 8
+    made = torch.Generator("cuda").manual_seed(9)
+    q = torch.randn((n, hkv * G, 128), generator=made, device="cuda", dtype=torch.bfloat16)
+    kv = torch.randn((past + n, 2 * hkv, 128), generator=made, device="cuda", dtype=torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    resume_attn(q, kv[:, :hkv], kv[:, hkv:], ints([0, n]), ints([0, past + n]), out=out)
+    assert not (out == 7).all(2).any() and out.isfinite().all()
+    rng = np.random.default_rng(9)
+    for i in [0, n - 1, *rng.integers(0, n, 14)]:
+        h = int(rng.integers(0, hkv))
+        one, k, v = (x.double().cpu().numpy() for x in (q[i:i + 1, h * G:h * G + G], kv[: past + i + 1, h:h + 1],
+                                                        kv[: past + i + 1, hkv + h:hkv + h + 1]))
+        want = ref.resume(one, k, v, [0, 1], [0, past + i + 1], SCALE)
+        check_attention(out[i:i + 1, h * G:h * G + G].double().cpu().numpy(), want[0], want[1], want[2], BF16_HALF_STEP)
+
+
 def test_split_results_are_the_same_every_time():
     from paged_helpers import bf16, ints
 

@@ -122,6 +122,7 @@ struct Tail {
 struct Parts {
   const int* kv_start;
   int n_kv_rows;
+  bool unsplit;   // no item is cut: there is no join
   float* o;       // [blocks][2][kD / 8][2 * kTile][8], not divided: what a warp's 32 rows store at once lies together
   float2* stats;  // [blocks][2][2 * kTile]: reference and sum of a row
   Tail* tails;    // [blocks]
@@ -416,6 +417,7 @@ struct Sequences {
   static constexpr int kItemCost = 400;
   const int *q_start, *kv_start;
   int B, n_rows, n_kv_rows, pair, per, heads, lane;
+  bool unsplit;  // every item costs 1: borders of equal ranges lie between items
   unsigned bits;
 
   __device__ void set(const int* qs, const Parts& parts, int b, int rows, int tokens, int hkv, int ln) {
@@ -424,6 +426,7 @@ struct Sequences {
     B = b;
     n_rows = rows;
     n_kv_rows = parts.n_kv_rows;
+    unsplit = parts.unsplit;
     per = tokens;
     pair = 2 * tokens;
     heads = hkv;
@@ -445,11 +448,13 @@ struct Sequences {
   }
   template <class C>
   __device__ C before_place(int p, int keys) const {  // cost of a head's items before place p
+    if (unsplit) return p;
     return (C)p * (C)(keys + kItemCost) + (C)pair * ((C)p * (C)(p + 1) / 2);
   }
   // The item at place p of a sequence with n rows.
   template <class C>
   __device__ C item_cost(int p, int n, int keys) const {
+    if (unsplit) return 1;
     const C c = (C)(keys + kItemCost) + (C)(p + 1) * (C)pair;
     return p * pair + per >= n ? c - c / 8 : c;
   }
@@ -477,6 +482,12 @@ struct Sequences {
     return total;
   }
 };
+
+// Where every item can have an SM and no sequence more than kUnsplit keys, no item is cut and no join launched: that costs a
+// long item's time and saves the parts and a launch.  32/8 heads, 4-bit pages, device time in a graph (time of a call alone):
+// 20 rows after 300 tokens 16.6 -> 14.0 us (39.6 -> 34.7), 500 without a context 24.3 -> 17.5 (45.5 -> 37.7), 100 after 900
+// 23.5 -> 21.6 (44.8 -> 42.5), but 60 after 1,400 24.0 -> 26.7 and after 1,900 25.1 -> 32.4.
+constexpr int kUnsplit = 1024;
 
 // The items cut into equal ranges of cost for the thread blocks.  A sequence's items follow each other head by head; an item
 // that crosses a range's border is cut at a tile there (not one tile from its ends).  There are as many ranges as pieces of
@@ -1320,7 +1331,7 @@ cudaError_t launch_attn(const PagedShape& s, const uint16_t* q, size_t q_stride,
 
 Parts parts_of(void* ws, const int* kv_start, int n_kv_rows) {
   const size_t rows = (size_t)sm_count() * 2 * (2 * kTile);
-  Parts p;
+  Parts p = {};
   p.kv_start = kv_start;
   p.n_kv_rows = n_kv_rows;
   p.o = static_cast<float*>(ws);
@@ -1360,13 +1371,14 @@ cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_
   const long long pieces = (items * (Sequences::kItemCost + (long long)n_kv_rows + pair) + kLeast - 1) / kLeast;
   const long long most = pieces < items ? items : pieces;
   const int sms = sm_count() < kMostBlocks ? sm_count() : kMostBlocks, grid = most < sms ? (int)most : sms;
-  const Parts parts = parts_of(ws, kv_start, n_kv_rows);
+  Parts parts = parts_of(ws, kv_start, n_kv_rows);
+  parts.unsplit = items <= sms && n_kv_rows <= kUnsplit;
   // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
   static std::mutex both[kMaxDevicesCached];
   std::lock_guard<std::mutex> lock(both[current_device()]);
   cudaError_t e = launch_attn<Piece>(s, q, q_stride, k, k_stride, v, v_stride, q_start, n_rows, n_kv_rows, scale, out, out_stride,
                                      parts, grid, err, stream);
-  if (e != cudaSuccess || grid == 1) return e;
+  if (e != cudaSuccess || grid == 1 || parts.unsplit) return e;
   return launch_chained(prompt_join_kernel, dim3(kJoinPerSm * sm_count()), dim3(kJoinThreads), 0, stream, 1, s, parts, grid, out,
                         out_stride);
 }

@@ -81,6 +81,13 @@ def test_work_split_over_the_keys(hkv, G, past, new):
     _run(past, new, hkv, G, seed=new[0], sample=40)
 
 
+@pytest.mark.parametrize("past,new,kv_pad", [([900], [124], 0), ([900], [124], 1), ([0, 300], [700, 24], 0), ([10] * 18, [40] * 18, 0),
+                                             ([10] * 20, [40] * 20, 0), ([10] * 20, [40] * 20, 24), ([0], [1024], 0)])
+def test_few_keys(past, new, kv_pad):
+    """Around 1,024 keys and an item to an SM, up to which no item is cut."""
+    _run(past, new, 8, 4, kv_pad=kv_pad, seed=len(new), sample=60)
+
+
 def test_items_of_more_keys_than_31_bits_count():
     """135,000 new rows: the items of all heads have 2.3e9 keys to read between them."""
     from paged_helpers import BF16_HALF_STEP, check_attention, ints

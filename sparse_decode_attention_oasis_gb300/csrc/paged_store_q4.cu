@@ -13,8 +13,8 @@
 // Two rows of one head to a warp's instruction: 16 lanes of 16 bytes cover a row, a pair of lanes a
 // group.  Rows are independent, so there is no order to keep and nothing is read but the rows.
 // Bound: HBM, 656 B for a row, head, K and V, with the instructions close behind.  15,600 rows of 8 heads (82 MB):
-// 16.8 us, 4.9 TB/s, 0.73 of the measured copy rate (20.2 with two divisions for each group and quotients
-// one by one); 32 rows of a decode step: 1.4 us.
+// 15.6 us, 5.3 TB/s, 0.79 of the measured copy rate (20.2 with two divisions for each group and quotients
+// one by one); 4, 16 and 32 rows to a warp take 17.5, 17.9 and 19.6; 32 rows of a decode step: 1.4 us.
 #include <cuda_fp16.h>
 
 #include "paged.cuh"
@@ -23,7 +23,7 @@ namespace oasis {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;  // rows of a warp in long calls
+constexpr int kRows = 8;  // rows of a warp in long calls
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -71,8 +71,12 @@ store_kv_q4_kernel(PagedShape s, const uint16_t* k, size_t k_stride, const uint1
   const uint16_t* src = (which ? v : k) + (size_t)h * kD + col * 8;
   const size_t stride = which ? v_stride : k_stride;
   const long long r0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kPer;
-  const int n_slots = s.n_pages * kBS;
+  const unsigned n_slots = (unsigned)s.n_pages * kBS;
   unsigned bits = 0;
+  // of page 0, token 0; a page further is `page_bytes`, `scale_bytes` on
+  uint8_t* const codes = pages + (size_t)h * kHeadPageBytes4 + which * (kBS * kD / 2) + col * 4;
+  uint8_t* const to = scales + (size_t)h * kHeadScaleBytes4 + which * (kBS * kGroups) + (col >> 1) * (which ? kBS : 1);
+  const unsigned page_bytes = s.Hkv * kHeadPageBytes4, scale_bytes = s.Hkv * kHeadScaleBytes4, step = which ? 1 : kGroups;
   if (r0 >= n_rows) return;
   uint4 x[kPer / 2];
   int slot[kPer / 2];
@@ -99,18 +103,11 @@ store_kv_q4_kernel(PagedShape s, const uint16_t* k, size_t k_stride, const uint1
 #pragma unroll
     for (int d = 0; d < 4; ++d) quotients(w[d], inv2, y[2 * d], y[2 * d + 1]);  // all zeros where b is 0
     const uint32_t code = nan ? 0u : codes8(y);
-    if (slot[i] < 0 || slot[i] >= n_slots) {
-      if (slot[i] != -1) bits |= OASIS_EW_BAD_SLOT;
-      continue;  // no shuffle follows in this turn
-    }
-    const int pos = slot[i] % kBS;
-    const long long head_page = (long long)(slot[i] / kBS) * s.Hkv + h;
-    uint8_t* dst = pages + head_page * kHeadPageBytes4 + which * (kBS * kD / 2) + pos * (kD / 2);
-    *reinterpret_cast<uint32_t*>(dst + col * 4) = code;
-    if ((col & 1) == 0) {
-      uint8_t* to = scales + head_page * kHeadScaleBytes4 + which * (kBS * kGroups);
-      to[which ? (col >> 1) * kBS + pos : pos * kGroups + (col >> 1)] = (uint8_t)(nan ? kScaleByteNaN : b);
-    }
+    const unsigned at = (unsigned)slot[i], page = at / kBS, pos = at % kBS;
+    const bool good = at < n_slots;
+    bits |= good || slot[i] == -1 ? 0u : (unsigned)OASIS_EW_BAD_SLOT;
+    if (good) *reinterpret_cast<uint32_t*>(codes + (size_t)page * page_bytes + pos * (kD / 2)) = code;
+    if (good && (col & 1) == 0) to[(size_t)page * scale_bytes + pos * step] = (uint8_t)(nan ? kScaleByteNaN : b);
   }
   if (blockIdx.y == 0) set_err(err, bits);
 }
@@ -121,7 +118,7 @@ cudaError_t launch_store_kv_q4(const PagedShape& s, const uint16_t* k, size_t k_
                                const int* slot_map, int n_rows, uint8_t* pages, uint8_t* scales, unsigned* err,
                                cudaStream_t stream) {
   if (n_rows == 0) return cudaSuccess;
-  // Two rows to a warp while all those warps are resident at once; long calls take 16 for the loads in flight.
+  // Two rows to a warp while all those warps are resident at once; long calls take kRows for the loads in flight.
   const long long resident = (long long)sm_count() * 64;
   const bool few = ((long long)n_rows + 1) / 2 * s.Hkv * 2 <= resident;
   const int per = few ? 2 : kRows;

@@ -118,6 +118,27 @@ def test_slices_of_a_fused_buffer():
     assert (c.kv[0].cpu().numpy() == want[0]).all() and (c.scale[0].cpu().numpy() == want[1]).all()
 
 
+@pytest.mark.parametrize("first,stride", [(8, 1024 * 2), (0, 1024 * 2 + 8), (24, 1024 * 2 + 40)])
+@pytest.mark.parametrize("rows", [5, 4003])
+def test_rows_on_16_byte_boundaries_only(rows, first, stride):
+    from paged_helpers import ints
+    from q4_helpers import cache_q4, random_pages_q4
+
+    rng = np.random.default_rng(rows)
+    n_pages = rows // 16 + 1
+    buf = _bf16(rng, (rows * stride + 1024,))
+    k = buf.as_strided((rows, 8, 128), (stride, 128, 1), first)
+    v = buf.as_strided((rows, 8, 128), (stride, 128, 1), first + 512)
+    kv, scale = random_pages_q4(rng, n_pages, 8)
+    c = cache_q4(kv, scale, np.zeros((1, 1), int), 8)
+    slots = rng.permutation(n_pages * 16)[:rows]
+    on_gpu = buf.cuda()
+    c.store(on_gpu.as_strided(k.shape, k.stride(), first), on_gpu.as_strided(k.shape, k.stride(), first + 512), ints(slots))
+    want_kv, want_scale, _ = ref.store_q4(kv, scale, k.double().numpy(), v.double().numpy(), slots)
+    assert (c.scale[0].cpu().numpy() == want_scale).all() and (c.kv[0].cpu().numpy() == want_kv).all()
+    assert int(c.err) == 0
+
+
 def test_refusals():
     from paged_helpers import ints
     from sparse_decode_attention_oasis_gb300.paged import PagedKV

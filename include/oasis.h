@@ -661,6 +661,7 @@ OASIS_API oasis_status oasis_trace_set(void* dev_buf, int32_t capacity);
  *   oasis_read_kv_q8, _q4           held tokens as packed bf16 rows, new rows behind
  *   oasis_prompt_attn               causal attention over packed prompts (bf16 K/V)
  *   oasis_resume_attn               the same where keys lie before the new rows
+ *   oasis_resume_kv_q8, _q4         the same where those keys are held in pages
  *
  * A page holds bs = 16 tokens of one layer, all KV heads.  In 8 bits:
  *   kv_pages  device e4m3 [n_pages][Hkv][2][bs][d]   [..][0] keys, [..][1] values
@@ -951,6 +952,43 @@ OASIS_API oasis_status oasis_resume_attn(const oasis_paged_shape* shape, const v
                                          const int32_t* kv_start, int32_t n_kv_rows, float scale,
                                          void* workspace, size_t ws_bytes, void* out,
                                          size_t out_stride, uint32_t* err_word, oasis_stream_t stream);
+
+/*
+ * The same over a cache, in one call: oasis_read_kv (only_new) into the workspace, then
+ * oasis_resume_attn.  With held_b = ctx_len[b], row i of request b (rows row_start[b] ..
+ * row_start[b+1] - 1 of q, k and v) attends the first held_b tokens of its pages, as
+ * they are stored, and rows 0 .. i of its own in k and v, as they are given.
+ *   row_start  device int32 [B+1]: new_start of oasis_read_kv, q_start of
+ *              oasis_resume_attn (the row_start of oasis_extend_tables)
+ *   ctx_len    device int32 [B]; clamped to [0, nb_max*bs].  Held tokens on a page
+ *              outside the pool count as zeros (OASIS_EW_BAD_SLOT).
+ *   n_held     at least the sum of ctx_len over the requests with new rows; the first
+ *              request whose tokens do not fit and all behind it are skipped with
+ *              OASIS_EW_BAD_COUNT.  n_rows + n_held is 0 .. 2^26.
+ *   workspace  device scratch, 32-byte aligned, ws_bytes >=
+ *              oasis_resume_kv_workspace_bytes(shape, n_rows, n_held), which is
+ *              4 * Hkv * d for each row and held token and a part that depends on the shape
+ *              alone; otherwise as for oasis_resume_attn
+ * The other arguments, roundings, infinities, NaN and errors are those of the two.
+ */
+OASIS_API size_t oasis_resume_kv_workspace_bytes(const oasis_paged_shape* shape, int32_t n_rows,
+                                                 int32_t n_held);
+OASIS_API oasis_status oasis_resume_kv_q8(const oasis_paged_shape* shape, const void* q, size_t q_stride,
+                                          const void* k, size_t k_stride, const void* v,
+                                          size_t v_stride, const int32_t* row_start, int32_t n_rows,
+                                          const void* kv_pages, const float* kv_scale,
+                                          const int32_t* block_table, const int32_t* ctx_len,
+                                          int32_t n_held, float scale, void* workspace,
+                                          size_t ws_bytes, void* out, size_t out_stride,
+                                          uint32_t* err_word, oasis_stream_t stream);
+OASIS_API oasis_status oasis_resume_kv_q4(const oasis_paged_shape* shape, const void* q, size_t q_stride,
+                                          const void* k, size_t k_stride, const void* v,
+                                          size_t v_stride, const int32_t* row_start, int32_t n_rows,
+                                          const void* kv_pages, const void* kv_scale,
+                                          const int32_t* block_table, const int32_t* ctx_len,
+                                          int32_t n_held, float scale, void* workspace,
+                                          size_t ws_bytes, void* out, size_t out_stride,
+                                          uint32_t* err_word, oasis_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -119,6 +119,10 @@ _SIGS = {
                                     ctypes.c_float, _VP, ctypes.c_size_t, _VP, _VP, _VP], ctypes.c_int),
     **{f"oasis_read_kv_{bits}": ([_PS, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32,
                                   ctypes.c_int32, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP], ctypes.c_int) for bits in ("q8", "q4")},
+    "oasis_resume_kv_workspace_bytes": ([_PS, ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+    **{f"oasis_resume_kv_{bits}": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32,
+                                    _VP, _VP, _VP, _VP, ctypes.c_int32, ctypes.c_float, _VP, ctypes.c_size_t, _VP,
+                                    ctypes.c_size_t, _VP, _VP], ctypes.c_int) for bits in ("q8", "q4")},
     "oasis_resume_attn_workspace_bytes": ([_PS], ctypes.c_size_t),
     "oasis_resume_attn": ([_PS, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, ctypes.c_int32, _VP,
                            ctypes.c_int32, ctypes.c_float, _VP, ctypes.c_size_t, _VP, ctypes.c_size_t, _VP, _VP], ctypes.c_int),
@@ -485,3 +489,27 @@ def oasis_resume_attn(shape: PagedShape, q, q_stride: int, k, k_stride: int, v, 
         ctypes.byref(shape), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q_start), n_rows,
         _ptr(kv_start), n_kv_rows, scale, _ptr(workspace), ws_bytes, _ptr(out), out_stride, _ptr(err_word),
         _stream(stream)))
+
+
+def oasis_resume_kv_workspace_bytes(shape: PagedShape, n_rows: int, n_held: int) -> int:
+    return int(load().oasis_resume_kv_workspace_bytes(ctypes.byref(shape), n_rows, n_held))
+
+
+def oasis_resume_kv_q8(shape: PagedShape, q, q_stride: int, k, k_stride: int, v, v_stride: int, row_start, n_rows: int,
+                       kv_pages, kv_scale, block_table, ctx_len, n_held: int, scale: float, workspace, ws_bytes: int, out,
+                       out_stride: int, err_word=None, stream=None):
+    """Attention of new rows over what their requests hold in 8-bit pages, and over each other."""
+    _check("oasis_resume_kv_q8", load().oasis_resume_kv_q8(
+        ctypes.byref(shape), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(row_start), n_rows,
+        _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len), n_held, scale, _ptr(workspace), ws_bytes,
+        _ptr(out), out_stride, _ptr(err_word), _stream(stream)))
+
+
+def oasis_resume_kv_q4(shape: PagedShape, q, q_stride: int, k, k_stride: int, v, v_stride: int, row_start, n_rows: int,
+                       kv_pages, kv_scale, block_table, ctx_len, n_held: int, scale: float, workspace, ws_bytes: int, out,
+                       out_stride: int, err_word=None, stream=None):
+    """Attention of new rows over what their requests hold in 4-bit pages, and over each other."""
+    _check("oasis_resume_kv_q4", load().oasis_resume_kv_q4(
+        ctypes.byref(shape), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(row_start), n_rows,
+        _ptr(kv_pages), _ptr(kv_scale), _ptr(block_table), _ptr(ctx_len), n_held, scale, _ptr(workspace), ws_bytes,
+        _ptr(out), out_stride, _ptr(err_word), _stream(stream)))

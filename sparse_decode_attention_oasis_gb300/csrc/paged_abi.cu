@@ -135,6 +135,63 @@ oasis_status read_kv(const char* fn, int bits, const oasis_paged_shape* shape, c
   return finish(fn, c, e);
 }
 
+// The pieces of a resume's workspace: keys, values, the attention's own, where each request's rows begin.
+struct Held {
+  size_t v, attn, kv_start, bytes;
+  Held(const PagedShape& s, int n_rows, int n_held) {
+    v = ((size_t)n_rows + n_held) * s.Hkv * (oasis::kD * 2);
+    attn = 2 * v;
+    kv_start = attn + (oasis::resume_workspace_bytes() + 255) / 256 * 256;
+    bytes = kv_start + ((size_t)s.B + 1) * sizeof(int);
+  }
+};
+
+void check_held(Call* c, int32_t n_rows, int32_t n_held) {
+  c->refuse(n_rows < 0 || n_held < 0 || (long long)n_rows + n_held > (1 << 26),
+            "n_rows and n_held must be >= 0 and at most 2^26 together");
+}
+
+oasis_status resume_kv(const char* fn, int bits, const oasis_paged_shape* shape, const void* q, size_t q_stride, const void* k,
+                       size_t k_stride, const void* v, size_t v_stride, const int32_t* row_start, int32_t n_rows,
+                       const void* kv_pages, const void* kv_scale, const int32_t* block_table, const int32_t* ctx_len,
+                       int32_t n_held, float scale, void* workspace, size_t ws_bytes, void* out, size_t out_stride,
+                       uint32_t* err_word, oasis_stream_t stream) {
+  Call c;
+  const PagedShape s = check_shape(shape, &c);
+  check_held(&c, n_rows, n_held);
+  c.refuse(!ints(row_start) || !ints(block_table) || !ints(ctx_len),
+           "row_start, block_table and ctx_len must be 4-byte aligned and non-NULL");
+  c.refuse(!kv_pages || !aligned(kv_pages, 16) || !kv_scale || !aligned(kv_scale, bits == 8 ? 8 : 16),
+           "kv_pages and kv_scale must be 16-byte (in 8 bits kv_scale 8-byte) aligned device pointers");
+  if (n_rows > 0) {
+    c.refuse(!rows_ok(q, q_stride, s.Hq * oasis::kD) || !rows_ok(out, out_stride, s.Hq * oasis::kD),
+             "q and out must be 16-byte aligned with strides that are multiples of 8 and at least Hq * d");
+    c.refuse(!rows_ok(k, k_stride, s.Hkv * oasis::kD) || !rows_ok(v, v_stride, s.Hkv * oasis::kD),
+             "k and v must be 16-byte aligned with strides that are multiples of 8 and at least Hkv * d");
+    c.refuse(!workspace || !aligned(workspace, 32), "workspace must be a 32-byte aligned device pointer");
+    c.refuse(c.status == OASIS_OK && ws_bytes < Held(s, n_rows, n_held).bytes,
+             "workspace too small (see oasis_resume_kv_workspace_bytes)");
+  }
+  c.refuse(!scale_ok(scale), "scale must be a positive finite number");
+  c.refuse(!aligned(err_word, 4), "err_word must be 4-byte aligned");
+  cudaError_t e = cudaSuccess;
+  if (c.status == OASIS_OK && n_rows > 0) {
+    const Held at(s, n_rows, n_held);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint16_t *k_all = reinterpret_cast<uint16_t*>(ws), *v_all = reinterpret_cast<uint16_t*>(ws + at.v);
+    int* kv_start = reinterpret_cast<int*>(ws + at.kv_start);
+    const size_t width = (size_t)s.Hkv * oasis::kD;
+    e = oasis::launch_read_kv(bits, s, (const uint8_t*)kv_pages, kv_scale, block_table, ctx_len, (const uint16_t*)k, k_stride,
+                              (const uint16_t*)v, v_stride, row_start, n_rows, true, kv_start, k_all, v_all, n_rows + n_held,
+                              err_word, (cudaStream_t)stream);
+    if (e == cudaSuccess)
+      e = oasis::launch_resume_attn(s, (const uint16_t*)q, q_stride, k_all, width, v_all, width, row_start, n_rows, kv_start,
+                                    n_rows + n_held, scale, ws + at.attn, (uint16_t*)out, out_stride, err_word,
+                                    (cudaStream_t)stream);
+  }
+  return finish(fn, c, e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -347,6 +404,31 @@ oasis_status oasis_resume_attn(const oasis_paged_shape* shape, const void* q, si
                                   q_start, n_rows, kv_start, n_kv_rows, scale, workspace, (uint16_t*)out, out_stride,
                                   err_word, (cudaStream_t)stream);
   return finish(fn, c, e);
+}
+
+size_t oasis_resume_kv_workspace_bytes(const oasis_paged_shape* shape, int32_t n_rows, int32_t n_held) {
+  Call c;
+  const PagedShape s = check_shape(shape, &c);
+  check_held(&c, n_rows, n_held);
+  return finish("oasis_resume_kv_workspace_bytes", c, cudaSuccess) == OASIS_OK ? Held(s, n_rows, n_held).bytes : 0;
+}
+
+oasis_status oasis_resume_kv_q8(const oasis_paged_shape* shape, const void* q, size_t q_stride, const void* k, size_t k_stride,
+                                const void* v, size_t v_stride, const int32_t* row_start, int32_t n_rows, const void* kv_pages,
+                                const float* kv_scale, const int32_t* block_table, const int32_t* ctx_len, int32_t n_held,
+                                float scale, void* workspace, size_t ws_bytes, void* out, size_t out_stride,
+                                uint32_t* err_word, oasis_stream_t stream) {
+  return resume_kv("oasis_resume_kv_q8", 8, shape, q, q_stride, k, k_stride, v, v_stride, row_start, n_rows, kv_pages, kv_scale,
+                   block_table, ctx_len, n_held, scale, workspace, ws_bytes, out, out_stride, err_word, stream);
+}
+
+oasis_status oasis_resume_kv_q4(const oasis_paged_shape* shape, const void* q, size_t q_stride, const void* k, size_t k_stride,
+                                const void* v, size_t v_stride, const int32_t* row_start, int32_t n_rows, const void* kv_pages,
+                                const void* kv_scale, const int32_t* block_table, const int32_t* ctx_len, int32_t n_held,
+                                float scale, void* workspace, size_t ws_bytes, void* out, size_t out_stride,
+                                uint32_t* err_word, oasis_stream_t stream) {
+  return resume_kv("oasis_resume_kv_q4", 4, shape, q, q_stride, k, k_stride, v, v_stride, row_start, n_rows, kv_pages, kv_scale,
+                   block_table, ctx_len, n_held, scale, workspace, ws_bytes, out, out_stride, err_word, stream);
 }
 
 }  // extern "C"

@@ -475,7 +475,7 @@ struct Sequences {
       int qa, n, ka, before;
       const long long c = sequence(s, qa, n, ka, before) ? heads * head_cost<long long>(n, before) : 0;
       total += c;
-      many = min(many + (unsigned)(heads * ((n + pair - 1) / pair)), 1u << 20);
+      many = min(many + (unsigned)heads * (unsigned)((n + pair - 1) / pair), 1u << 20);
       if (s == lane) *of_lane = c;
     }
     *items = __reduce_add_sync(0xffffffffu, many);

@@ -221,7 +221,8 @@ class PagedKV:
         self._shape = ctypes.byref(self.shape)
         self._kv_bytes, self._scale_bytes = self.kv.stride(0), self.scale.element_size() * self.scale.stride(0)  # of a layer
         self._scratch = {}  # decode's, by stream
-        self._resume_bytes = -(-B.oasis_resume_attn_workspace_bytes(self.shape) // 256) * 256
+        with torch.cuda.device(self._index):  # resume's scratch, and 4 * Hkv * 128 for each row and held token
+            self._resume_bytes = B.oasis_resume_kv_workspace_bytes(self.shape, 0, 0)
 
     def adopt(self, **tensors: torch.Tensor) -> None:
         """Use the caller's tensors in place of kv, scale, table, free, n_free or lens (same
@@ -412,24 +413,16 @@ class PagedKV:
         out_stride = _rows("out", out, hq, n, device)
         if n == 0:
             return out
-        # one piece of scratch: keys, values, the workspace, kv_start, each a multiple of 256 bytes
-        m = n_held + n
-        kv_bytes, ws_bytes = m * hkv * D * 2, self._resume_bytes
-        scratch = torch.empty(2 * kv_bytes + ws_bytes + 4 * (b + 1), dtype=torch.uint8, device=device)
-        k_at = scratch.data_ptr()
-        v_at, ws_at, start_at = k_at + kv_bytes, k_at + 2 * kv_bytes, k_at + 2 * kv_bytes + ws_bytes
-        lib, stream, err = B._lib or B.load(), _current_stream(self._index), self.err.data_ptr()
-        st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
-            self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
-            self.table.data_ptr(), self.lens.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, row_start, n, 1, start_at, k_at,
-            v_at, m, err, stream)
+        ws_bytes = self._resume_bytes + (n + n_held) * hkv * D * 4
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        lib = B._lib or B.load()
+        st = (lib.oasis_resume_kv_q8 if self.bits == 8 else lib.oasis_resume_kv_q4)(
+            self._shape, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, row_start, n,
+            self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
+            self.table.data_ptr(), self.lens.data_ptr(), n_held, _SCALE if scale is None else scale, ws.data_ptr(), ws_bytes,
+            out.data_ptr(), out_stride, self.err.data_ptr(), _current_stream(self._index))
         if st:
-            B._check(f"oasis_read_kv_q{self.bits}", st)
-        st = lib.oasis_resume_attn(
-            self._shape, q.data_ptr(), qs, k_at, hkv * D, v_at, hkv * D, row_start, n, start_at, m,
-            _SCALE if scale is None else scale, ws_at, ws_bytes, out.data_ptr(), out_stride, err, stream)
-        if st:
-            B._check("oasis_resume_attn", st)
+            B._check(f"oasis_resume_kv_q{self.bits}", st)
         return out
 
     def check(self) -> None:

@@ -266,6 +266,33 @@ def test_through_the_cache(bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+def test_one_call_gives_what_the_two_give(bits):
+    """oasis_resume_kv_*, then oasis_read_kv_* and oasis_resume_attn on rows of its own."""
+    from paged_helpers import bf16, cache_of, ints, random_pages, shuffled_table
+    from q4_helpers import cache_q4, random_pages_q4
+
+    from sparse_decode_attention_oasis_gb300 import binding as B
+    from sparse_decode_attention_oasis_gb300.paged import resume_attn
+
+    rng = np.random.default_rng(bits)
+    ctx, new = [700, 0, 33, 3000], [5, 90, 0, 17]
+    table = shuffled_table(rng, ctx, 200, 300)
+    kv, scale = random_pages(rng, 300, 2) if bits == 8 else random_pages_q4(rng, 300, 2)
+    c = (cache_of if bits == 8 else cache_q4)(kv, scale, table, 8)
+    start, lens = ints(np.concatenate([[0], np.cumsum(new)])), ints(ctx)
+    q, _ = bf16(rng, (112, 8, 128), 1.5)
+    k, _ = bf16(rng, (112, 2, 128))
+    v, _ = bf16(rng, (112, 2, 128))
+    out = torch.zeros_like(q)
+    n = B.oasis_resume_kv_workspace_bytes(c.shape, 112, 3700)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    call = B.oasis_resume_kv_q8 if bits == 8 else B.oasis_resume_kv_q4
+    call(c.shape, q, 1024, k, 256, v, 256, start, 112, c.kv, c.scale, c.table, lens, 3700, SCALE, ws, n, out, 1024, c.err)
+    rows = c.read(3812, lens, new=(k, v, start), only_new=True)
+    assert torch.equal(out, resume_attn(q, rows.k, rows.v, start, rows.row_start)) and int(c.err) == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 def test_the_caches_resume_captured_and_replayed(bits):
     """The whole call in a graph, replayed after the cache has grown, beside an eager call; against the eager call's bits."""
     from paged_helpers import bf16, ints

@@ -39,6 +39,12 @@ def _resume(lib, s, q=16, qs=4096, k=16, ks=1024, v=16, vs=1024, start=16, n=5, 
     return lib.oasis_resume_attn(ctypes.byref(s), q, qs, k, ks, v, vs, start, n, kstart, m, scale, ws, nb, out, os, err, None)
 
 
+def _resume_kv(lib, s, q=16, qs=4096, k=16, ks=1024, v=16, vs=1024, start=16, n=50, kv=16, sc=16, table=16, ctx=16, held=9, scale=0.1,
+               ws=32, nb=1 << 30, out=16, os=4096, err=None, bits=4):
+    call = lib.oasis_resume_kv_q4 if bits == 4 else lib.oasis_resume_kv_q8
+    return call(ctypes.byref(s), q, qs, k, ks, v, vs, start, n, kv, sc, table, ctx, held, scale, ws, nb, out, os, err, None)
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(Hq=30), 1), (dict(B=0), 1), (dict(n_pages=0), 1), (dict(d=64), 4), (dict(bs=32), 4), (dict(Hq=72), 4),
     (dict(B=65536), 4), (dict(nb_max=(1 << 24) + 1), 4), (dict(n_pages=1 << 27), 4)])
@@ -109,3 +115,34 @@ def test_the_python_layer_refuses_cpu_tensors():
     start = torch.tensor([0, 4], dtype=torch.int32)
     with pytest.raises(ValueError):
         resume_attn(q, q[:, :1], q[:, :1], start, start)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(Hq=30), 1), (dict(B=0), 1), (dict(n_pages=0), 1), (dict(d=64), 4), (dict(bs=32), 4), (dict(Hq=72), 4),
+    (dict(B=65536), 4), (dict(nb_max=(1 << 24) + 1), 4), (dict(n_pages=1 << 27), 4)])
+def test_resume_over_pages_checks_the_shape(lib, kw, status):
+    s = _shape(**kw)
+    assert _resume_kv(lib, s) == _resume_kv(lib, s, bits=8) == status
+    assert lib.oasis_last_error().startswith(b"oasis_resume_kv_q8")
+    assert lib.oasis_resume_kv_workspace_bytes(ctypes.byref(s), 5, 5) == 0
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(q=8), dict(qs=4095), dict(k=None), dict(ks=1020), dict(v=24), dict(vs=0), dict(start=None), dict(start=18),
+    dict(n=-1), dict(n=(1 << 26) + 1), dict(held=-1), dict(held=(1 << 26) + 1), dict(kv=None), dict(kv=8), dict(sc=None), dict(sc=4),
+    dict(table=None), dict(table=2), dict(ctx=None), dict(scale=0.0), dict(scale=NAN), dict(ws=None), dict(ws=16), dict(nb=16),
+    dict(out=None), dict(out=8), dict(os=4088), dict(err=2)])
+def test_resume_over_pages_refusals(lib, bits, kw):
+    assert _resume_kv(lib, _shape(), bits=bits, **kw) == 1
+
+
+def test_the_workspace_over_pages(lib):
+    s = ctypes.byref(_shape())
+    none = lib.oasis_resume_kv_workspace_bytes(s, 0, 0)
+    assert none >= lib.oasis_resume_attn_workspace_bytes(s) > 0
+    assert lib.oasis_resume_kv_workspace_bytes(s, 33, 1000) == none + 1033 * 4 * 8 * 128
+    for n, held in ((-1, 0), (0, -1), (1 << 26, 1)):
+        assert lib.oasis_resume_kv_workspace_bytes(s, n, held) == 0
+    assert _resume_kv(lib, _shape(), n=50, held=9, nb=none + 59 * 4 * 8 * 128 - 1) == 1
+    assert _resume_kv(lib, _shape(), q=None, k=None, v=None, out=None, ws=None, nb=0, n=0) == 0  # nothing to do

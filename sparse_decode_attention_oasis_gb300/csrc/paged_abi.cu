@@ -1,6 +1,7 @@
 // C ABI entry points of the paged cache: argument validation, then the launches.
 // No exception leaves an entry point: a message that cannot be built is a failed call.
 #include <cmath>
+#include <mutex>
 #include <string>
 
 #include "paged.cuh"
@@ -181,6 +182,9 @@ oasis_status resume_kv(const char* fn, int bits, const oasis_paged_shape* shape,
     uint16_t *k_all = reinterpret_cast<uint16_t*>(ws), *v_all = reinterpret_cast<uint16_t*>(ws + at.v);
     int* kv_start = reinterpret_cast<int*>(ws + at.kv_start);
     const size_t width = (size_t)s.Hkv * oasis::kD;
+    // the attention reads what the read-back left in the workspace: of two threads that share a stream, none comes between
+    static std::mutex both[oasis::kMaxDevicesCached];
+    std::lock_guard<std::mutex> lock(both[oasis::current_device()]);
     e = oasis::launch_read_kv(bits, s, (const uint8_t*)kv_pages, kv_scale, block_table, ctx_len, (const uint16_t*)k, k_stride,
                               (const uint16_t*)v, v_stride, row_start, n_rows, true, kv_start, k_all, v_all, n_rows + n_held,
                               err_word, (cudaStream_t)stream);

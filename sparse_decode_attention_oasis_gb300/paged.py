@@ -35,9 +35,10 @@ A prompt that continues a context attends what its request holds as well as itse
     cache.commit(plan)
 
 Calls run on the current stream of the tensors' device and can be captured into a CUDA
-graph; nothing is kept between calls but the tensors above and decode's scratch, one for
-each stream (resume takes its own from PyTorch's memory at each call; calls on one stream follow each other, those of several host threads as well:
-the library keeps a call's launches together).  A captured call takes scratch of its
+graph; nothing is kept between calls but the tensors above and the scratch of decode and of resume,
+one for each stream (calls on one stream follow each other, those of several host threads as well:
+the library keeps a call's launches together; resume keeps at most 256 MB, and takes more from PyTorch's memory for
+the call alone).  A captured call takes scratch of its
 own from the graph's memory pool, so graphs, and calls on other streams, never share it.
 
 The methods call the library directly with addresses and sizes: for a decode step's small
@@ -58,6 +59,7 @@ D = 128
 BS = 16
 _SCALE = 1.0 / math.sqrt(D)
 _BF16, _INT32 = torch.bfloat16, torch.int32
+_KEPT = 256 << 20  # bytes of resume's scratch that stay (an allocation is 3 us of a short call's 17 on the host)
 
 
 class Rows(NamedTuple):
@@ -220,7 +222,7 @@ class PagedKV:
         self._index = _cuda(self.device)
         self._shape = ctypes.byref(self.shape)
         self._kv_bytes, self._scale_bytes = self.kv.stride(0), self.scale.element_size() * self.scale.stride(0)  # of a layer
-        self._scratch = {}  # decode's, by stream
+        self._scratch, self._resume_scratch = {}, {}  # decode's, resume's, by stream
         with torch.cuda.device(self._index):  # resume's scratch, and 4 * Hkv * 128 for each row and held token
             self._resume_bytes = B.oasis_resume_kv_workspace_bytes(self.shape, 0, 0)
 
@@ -414,13 +416,19 @@ class PagedKV:
         if n == 0:
             return out
         ws_bytes = self._resume_bytes + (n + n_held) * hkv * D * 4
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        stream = _current_stream(self._index)
+        keep = ws_bytes <= _KEPT and not torch._C._cuda_isCurrentStreamCapturing()
+        ws = self._resume_scratch.get(stream) if keep else None
+        if ws is None or ws.shape[0] < ws_bytes:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            if keep:
+                self._resume_scratch[stream] = ws
         lib = B._lib or B.load()
         st = (lib.oasis_resume_kv_q8 if self.bits == 8 else lib.oasis_resume_kv_q4)(
             self._shape, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, row_start, n,
             self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
             self.table.data_ptr(), self.lens.data_ptr(), n_held, _SCALE if scale is None else scale, ws.data_ptr(), ws_bytes,
-            out.data_ptr(), out_stride, self.err.data_ptr(), _current_stream(self._index))
+            out.data_ptr(), out_stride, self.err.data_ptr(), stream)
         if st:
             B._check(f"oasis_resume_kv_q{self.bits}", st)
         return out

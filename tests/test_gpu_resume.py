@@ -292,6 +292,73 @@ def test_one_call_gives_what_the_two_give(bits):
     assert torch.equal(out, resume_attn(q, rows.k, rows.v, start, rows.row_start)) and int(c.err) == 0
 
 
+def test_two_threads_resume_on_one_stream():
+    """They share the stream's scratch: read-back, attention and join of a call stay together."""
+    import threading
+
+    from paged_helpers import bf16, ints, shuffled_table
+    from q4_helpers import cache_q4, random_pages_q4
+
+    from sparse_decode_attention_oasis_gb300.paged import Plan
+
+    rng = np.random.default_rng(1)
+    held, calls = [6000, 900, 40], 600
+    kv, scale = random_pages_q4(rng, 450, 2)
+    c = cache_q4(kv, scale, shuffled_table(rng, held, 400, 450), 8)
+    c.lens.copy_(ints(held))
+    work = []
+    for new in ([3, 40, 0], [0, 7, 200]):
+        rows = sum(new)
+        q, k, v = (bf16(rng, (rows, h, 128), 1.5)[0] for h in (8, 2, 2))
+        work.append((q, k, v, Plan(None, None, ints(np.concatenate([[0], np.cumsum(new)])), None)))
+    want = [c.resume(*w, sum(held)).clone() for w in work]
+    torch.cuda.synchronize()
+    outs, failed, start = [[], []], [], threading.Barrier(2)
+
+    def loop(i):
+        try:
+            start.wait()
+            for _ in range(calls):
+                outs[i].append(c.resume(*work[i], sum(held)))
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and int(c.err) == 0
+    for i in range(2):
+        wrong = (torch.stack(outs[i]) != want[i]).flatten(1).any(1).sum()
+        assert int(wrong) == 0, f"thread {i}: {int(wrong)} of {calls} outputs differ"
+
+
+def test_the_scratch_grows_and_is_not_kept_past_its_limit(monkeypatch):
+    from paged_helpers import bf16, ints, shuffled_table
+    from q4_helpers import cache_q4, random_pages_q4
+
+    from sparse_decode_attention_oasis_gb300 import paged
+
+    rng = np.random.default_rng(2)
+    kv, scale = random_pages_q4(rng, 130, 2)
+    c = cache_q4(kv, scale, shuffled_table(rng, [2000], 130, 130), 8)
+    c.lens.copy_(ints([2000]))
+    q, k, v = (bf16(rng, (20, h, 128))[0] for h in (8, 2, 2))
+    plan = paged.Plan(None, None, ints([0, 20]), None)
+    first = c.resume(q, k, v, plan, 2000)
+    (kept,) = c._resume_scratch.values()
+    assert torch.equal(c.resume(q, k, v, plan, 3000), first)
+    (more,) = c._resume_scratch.values()
+    assert more.numel() == kept.numel() + 1000 * 4 * 2 * 128
+    assert torch.equal(c.resume(q, k, v, plan, 2000), first)
+    monkeypatch.setattr(paged, "_KEPT", 1 << 20)
+    assert torch.equal(c.resume(q, k, v, plan, 4000), first)
+    (still,) = c._resume_scratch.values()
+    assert still is more and int(c.err) == 0
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_the_caches_resume_captured_and_replayed(bits):
     """The whole call in a graph, replayed after the cache has grown, beside an eager call; against the eager call's bits."""

@@ -353,7 +353,8 @@ class PagedKV:
         of them; stored values are bf16 exactly.  new = (k, v, row_start) puts the rows row_start[b] ..
         row_start[b+1] - 1 of k and v [rows, Hkv, 128] behind request b's; with only_new requests without new
         rows have no rows at all.  out = (k, v): contiguous bf16
-        [n_rows, Hkv, 128] to write to; rows behind the last request's are left as they are."""
+        [n_rows, Hkv, 128] to write to, or (k, v, row_start) with int32 [batch + 1] as well (an earlier call's Rows);
+        rows behind the last request's are left as they are."""
         if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.read(n_rows, ctx_len, layer, new, out, only_new)
@@ -373,13 +374,19 @@ class PagedKV:
             ks, vs = _rows("k", k, h, n_new, device), _rows("v", v, h, n_new, device)
             k_at, v_at = k.data_ptr(), v.data_ptr()
             start_at = _ints("row_start", row_start, (b + 1,), device).data_ptr()
+        kv_start = None
         if out is None:
             out = (torch.empty((n_rows, h, D), dtype=_BF16, device=device), torch.empty((n_rows, h, D), dtype=_BF16, device=device))
         else:
-            for t in out:
+            if len(out) not in (2, 3):
+                raise ValueError("out must be (k, v) or (k, v, row_start)")
+            if len(out) == 3:
+                kv_start = _ints("out's row_start", out[2], (b + 1,), device)
+            for t in out[:2]:
                 if t.dtype is not _BF16 or t.shape != (n_rows, h, D) or t.device != device or not t.is_contiguous():
                     raise ValueError(f"out must be two contiguous bfloat16 [{n_rows}, {h}, {D}] on {device}")
-        kv_start = torch.empty(b + 1, dtype=_INT32, device=device)
+        if kv_start is None:
+            kv_start = torch.empty(b + 1, dtype=_INT32, device=device)
         lib = B._lib or B.load()
         st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
             self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,

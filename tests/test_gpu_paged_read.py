@@ -176,3 +176,20 @@ def test_refusals():
                 dict(out=(out.transpose(0, 1), out))):
         with pytest.raises(ValueError):
             c.read(**{"n_rows": 5, **bad})
+
+
+def test_the_rows_of_an_earlier_call_as_out():
+    from paged_helpers import ints, shuffled_table
+    from q4_helpers import cache_q4, random_pages_q4
+
+    rng = np.random.default_rng(6)
+    kv, scale = random_pages_q4(rng, 12, 2)
+    c = cache_q4(kv, scale, shuffled_table(rng, [70, 0, 40], 6, 12), 4)
+    rows = c.read(120, ints([70, 0, 40]))
+    want = c.read(120, ints([33, 0, 17]))
+    again = c.read(120, ints([33, 0, 17]), out=rows)
+    assert all(x is y for x, y in zip(again, rows))
+    assert again.row_start.tolist() == [0, 33, 33, 50] and torch.equal(again.k[:50], want.k[:50]) and torch.equal(again.v[:50], want.v[:50])
+    for bad in (rows[:1], (*rows, rows.k), (rows.k, rows.v, rows.row_start[:3]), (rows.k, rows.v, rows.row_start.long())):
+        with pytest.raises(ValueError):
+            c.read(120, ints([33, 0, 17]), out=bad)

@@ -193,3 +193,25 @@ def test_the_rows_of_an_earlier_call_as_out():
     for bad in (rows[:1], (*rows, rows.k), (rows.k, rows.v, rows.row_start[:3]), (rows.k, rows.v, rows.row_start.long())):
         with pytest.raises(ValueError):
             c.read(120, ints([33, 0, 17]), out=bad)
+
+
+def test_starts_of_many_calls_on_two_streams():
+    """Every call's row_start is its own, however many there are."""
+    from paged_helpers import ints, shuffled_table
+    from q4_helpers import cache_q4, random_pages_q4
+
+    rng = np.random.default_rng(8)
+    kv, scale = random_pages_q4(rng, 12, 1)
+    c = cache_q4(kv, scale, shuffled_table(rng, [70, 0, 40], 6, 12), 2)
+    lens = [(int(rng.integers(0, 71)), 0, int(rng.integers(0, 41))) for _ in range(100)]
+    on_gpu = [ints(n) for n in lens]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    rows = []
+    for i, n in enumerate(on_gpu):
+        with torch.cuda.stream(side if i % 3 else torch.cuda.current_stream()):
+            rows.append(c.read(110, n))
+    torch.cuda.synchronize()
+    assert len({r.row_start.data_ptr() for r in rows}) == 100
+    for r, (x, _, y) in zip(rows, lens):
+        assert r.row_start.tolist() == [0, x, x, x + y] and r.row_start.is_contiguous()

@@ -59,7 +59,7 @@ D = 128
 BS = 16
 _SCALE = 1.0 / math.sqrt(D)
 _BF16, _INT32 = torch.bfloat16, torch.int32
-_KEPT = 256 << 20  # bytes of resume's scratch that stay (an allocation is 3 us of a short call's 17 on the host)
+_KEPT = 256 << 20  # bytes of resume's scratch that stay (allocated at each call, a short one takes 17.5 us, else 12.8)
 
 
 class Rows(NamedTuple):

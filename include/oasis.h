@@ -803,7 +803,8 @@ OASIS_API oasis_status oasis_store_kv_q8(const oasis_paged_shape* shape, const v
  *   workspace device scratch, 16-byte aligned, ws_bytes >=
  *             oasis_paged_attn_workspace_bytes(shape); contents on entry are
  *             ignored; calls that may overlap need different ones (calls
- *             on one stream do not, from whichever host threads they come)
+ *             on one stream do not, from whichever host threads they come:
+ *             this one, oasis_resume_attn and oasis_resume_kv in any mixture)
  *   out       device bf16 [B][Hq][d], 16-byte aligned: the activation type that the
  *             output projection reads
  *   err_word  device uint32 [1] or NULL
@@ -938,8 +939,8 @@ OASIS_API oasis_status oasis_read_kv_q4(const oasis_paged_shape* shape, const vo
  *   scale      softmax scale, > 0 and finite
  *   workspace  device scratch, 32-byte aligned, ws_bytes >=
  *              oasis_resume_attn_workspace_bytes(shape); contents on entry are
- *              ignored; calls that may overlap need different ones (calls
- *              on one stream do not, from whichever host threads they come)
+ *              ignored; calls that may overlap need different ones (as for
+ *              oasis_paged_decode_attn_q8)
  *   err_word   device uint32 [1] or NULL; OASIS_EW_TIMEOUT as for oasis_prompt_attn
  * Only B, Hq, Hkv and d of the shape are used; the others are checked as for
  * every call.

@@ -123,6 +123,13 @@ cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// Held by a call while it issues launches that read what its earlier ones left in the workspace: of two host threads that
+// share a stream and a workspace, in whichever of the paged cache's calls, none comes between.
+inline std::mutex& workspace_lock() {
+  static std::mutex locks[kMaxDevicesCached];
+  return locks[current_device()];
+}
+
 __device__ __forceinline__ void set_err(unsigned* err, unsigned bits) {
   if (err != nullptr && bits) atomicOr(err, bits);
 }

@@ -182,9 +182,7 @@ oasis_status resume_kv(const char* fn, int bits, const oasis_paged_shape* shape,
     uint16_t *k_all = reinterpret_cast<uint16_t*>(ws), *v_all = reinterpret_cast<uint16_t*>(ws + at.v);
     int* kv_start = reinterpret_cast<int*>(ws + at.kv_start);
     const size_t width = (size_t)s.Hkv * oasis::kD;
-    // the attention reads what the read-back left in the workspace: of two threads that share a stream, none comes between
-    static std::mutex both[oasis::kMaxDevicesCached];
-    std::lock_guard<std::mutex> lock(both[oasis::current_device()]);
+    std::lock_guard<std::mutex> lock(oasis::workspace_lock());
     e = oasis::launch_read_kv(bits, s, (const uint8_t*)kv_pages, kv_scale, block_table, ctx_len, (const uint16_t*)k, k_stride,
                               (const uint16_t*)v, v_stride, row_start, n_rows, true, kv_start, k_all, v_all, n_rows + n_held,
                               err_word, (cudaStream_t)stream);
@@ -403,10 +401,12 @@ oasis_status oasis_resume_attn(const oasis_paged_shape* shape, const void* q, si
   c.refuse(!scale_ok(scale), "scale must be a positive finite number");
   c.refuse(!aligned(err_word, 4), "err_word must be 4-byte aligned");
   cudaError_t e = cudaSuccess;
-  if (c.status == OASIS_OK)
+  if (c.status == OASIS_OK) {
+    std::lock_guard<std::mutex> lock(oasis::workspace_lock());
     e = oasis::launch_resume_attn(s, (const uint16_t*)q, q_stride, (const uint16_t*)k, k_stride, (const uint16_t*)v, v_stride,
                                   q_start, n_rows, kv_start, n_kv_rows, scale, workspace, (uint16_t*)out, out_stride,
                                   err_word, (cudaStream_t)stream);
+  }
   return finish(fn, c, e);
 }
 

@@ -946,8 +946,6 @@ size_t paged_attn_workspace_bytes(const PagedShape& s) {
 
 namespace {
 
-std::mutex both_launches[kMaxDevicesCached];
-
 template <int kBits>
 cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint8_t* pages, const void* scales,
                           const int* table, const int* ctx, const int* sel, const int* nsel, int sel_max, float scale,
@@ -986,8 +984,7 @@ cudaError_t launch_decode(const PagedShape& s, const uint16_t* q, size_t q_strid
   static int attr_cache[kMaxDevicesCached] = {};
   cudaError_t e = ensure_dyn_smem((const void*)paged_decode_attn_kernel<false, kBits>, smem, attr_cache);
   if (e != cudaSuccess) return e;
-  // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
-  std::lock_guard<std::mutex> lock(both_launches[current_device()]);
+  std::lock_guard<std::mutex> lock(workspace_lock());  // the join reads what the kernel before it left in the workspace
   e = launch_chained(paged_decode_attn_kernel<false, kBits>, dim3(grid), dim3(kThreads), smem, stream, 1, s, a);
   if (e != cudaSuccess || grid == 1) return e;
   if constexpr (kBits == 4) {

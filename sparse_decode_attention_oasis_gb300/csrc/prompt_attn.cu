@@ -1361,6 +1361,7 @@ size_t resume_workspace_bytes() {
   return blocks * (2 * (2 * kTile) * (kD * sizeof(float) + sizeof(float2)) + sizeof(Tail));
 }
 
+// The join reads what the kernel before it left in the workspace: the caller holds workspace_lock.
 cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_stride, const uint16_t* k, size_t k_stride,
                                const uint16_t* v, size_t v_stride, const int* q_start, int n_rows, const int* kv_start,
                                int n_kv_rows, float scale, void* ws, uint16_t* out, size_t out_stride, unsigned* err,
@@ -1375,9 +1376,6 @@ cudaError_t launch_resume_attn(const PagedShape& s, const uint16_t* q, size_t q_
   const int sms = sm_count() < kMostBlocks ? sm_count() : kMostBlocks, grid = most < sms ? (int)most : sms;
   Parts parts = parts_of(ws, kv_start, n_kv_rows);
   parts.unsplit = items <= sms && n_kv_rows <= kUnsplit;
-  // the join reads what the kernel before it left in the workspace: of two threads that share a stream, none comes between
-  static std::mutex both[kMaxDevicesCached];
-  std::lock_guard<std::mutex> lock(both[current_device()]);
   cudaError_t e = launch_attn<Piece>(s, q, q_stride, k, k_stride, v, v_stride, q_start, n_rows, n_kv_rows, scale, out, out_stride,
                                      parts, grid, err, stream);
   if (e != cudaSuccess || grid == 1 || parts.unsplit) return e;

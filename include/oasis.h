@@ -900,7 +900,8 @@ OASIS_API oasis_status oasis_paged_decode_attn_q4(const oasis_paged_shape* shape
  *   new_start  device int32 [B+1], or NULL: no new rows
  *   only_new   1: a request without new rows has none at all (oasis_resume_attn has
  *              no use for its held tokens); 0: it has its held ones
- *   kv_start   device int32 [B+1]    out
+ *   kv_start   device int32 [B+1]    out; must not overlap block_table, ctx_len or
+ *              new_start, which all thread blocks read while one writes it
  *   k_out, v_out   device bf16 [n_rows][Hkv][d], 32-byte aligned; must not overlap
  *              k_new or v_new
  *   n_rows     0 .. 2^28

@@ -83,6 +83,8 @@ PagedShape check_shape(const oasis_paged_shape* sh, Call* c) {
 // int32 arrays that must be there
 bool ints(const void* p) { return p && aligned(p, 4); }
 
+bool overlap(const int32_t* a, size_t na, const int32_t* b, size_t nb) { return a < b + nb && b < a + na; }
+
 // rows of `width` elements of bf16, `stride` apart
 bool rows_ok(const void* p, size_t stride, int width) {
   return p && aligned(p, 16) && stride % 8 == 0 && stride >= (size_t)width && stride < (size_t(1) << 32);
@@ -128,6 +130,12 @@ oasis_status read_kv(const char* fn, int bits, const oasis_paged_shape* shape, c
              "k_new and v_new must be 16-byte aligned with strides that are multiples of 8 and at least Hkv * d");
   c.refuse(n_rows > 0 && (!k_out || !v_out || !aligned(k_out, 32) || !aligned(v_out, 32)),
            "k_out and v_out must be 32-byte aligned device pointers");
+  if (c.status == OASIS_OK) {  // one thread block writes it, all read the others
+    const size_t B = (size_t)s.B;
+    c.refuse(overlap(kv_start, B + 1, ctx_len, B) || overlap(kv_start, B + 1, block_table, B * s.nb_max) ||
+                 (new_start && overlap(kv_start, B + 1, new_start, B + 1)),
+             "kv_start must not overlap block_table, ctx_len or new_start");
+  }
   cudaError_t e = cudaSuccess;
   if (c.status == OASIS_OK)
     e = oasis::launch_read_kv(bits, s, (const uint8_t*)kv_pages, kv_scale, block_table, ctx_len, (const uint16_t*)k_new, k_stride,
@@ -212,7 +220,6 @@ oasis_status oasis_extend_tables(const oasis_paged_shape* shape, const int32_t* 
   c.refuse(n_rows > 0 && !ints(slot_map), "slot_map must be 4-byte aligned and non-NULL");
   c.refuse(!aligned(err_word, 4), "err_word must be 4-byte aligned");
   if (c.status == OASIS_OK) {
-    auto overlap = [&](const int32_t* a, size_t na, const int32_t* b, size_t nb) { return a < b + nb && b < a + na; };
     const size_t B = (size_t)s.B;
     c.refuse(overlap(len_out, B, old_len, B) || overlap(len_out, B, new_len, B) || overlap(len_out, B, n_free, 1) ||
                  overlap(n_free_out, 1, old_len, B) || overlap(n_free_out, 1, new_len, B) || n_free_out == n_free,

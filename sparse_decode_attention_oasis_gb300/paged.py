@@ -366,8 +366,8 @@ class PagedKV:
         of them; stored values are bf16 exactly.  new = (k, v, row_start) puts the rows row_start[b] ..
         row_start[b+1] - 1 of k and v [rows, Hkv, 128] behind request b's; with only_new requests without new
         rows have no rows at all.  out = (k, v): contiguous bf16
-        [n_rows, Hkv, 128] to write to, or (k, v, row_start) with int32 [batch + 1] as well (an earlier call's Rows);
-        rows behind the last request's are left as they are."""
+        [n_rows, Hkv, 128] to write to, or (k, v, row_start) with int32 [batch + 1] as well (an earlier call's Rows),
+        none of which lies on what the call reads; rows behind the last request's are left as they are."""
         if _current_device() != self._index:
             with torch.cuda.device(self._index):
                 return self.read(n_rows, ctx_len, layer, new, out, only_new)

@@ -966,7 +966,8 @@ OASIS_API oasis_status oasis_resume_attn(const oasis_paged_shape* shape, const v
  *              outside the pool count as zeros (OASIS_EW_BAD_SLOT).
  *   n_held     at least the sum of ctx_len over the requests with new rows; the first
  *              request whose tokens do not fit and all behind it are skipped with
- *              OASIS_EW_BAD_COUNT.  n_rows + n_held is 0 .. 2^26.
+ *              OASIS_EW_BAD_COUNT.  n_rows + n_held is 0 .. 2^26.  A larger n_held than
+ *              needed changes no bit of the output.
  *   workspace  device scratch, 32-byte aligned, ws_bytes >=
  *              oasis_resume_kv_workspace_bytes(shape, n_rows, n_held), which is
  *              4 * Hkv * d for each row and held token and a part that depends on the shape

@@ -55,7 +55,7 @@
 //
 // Keys before the new rows (Piece for Item): few rows may read many keys, so all items' tiles form one sequence, cut into
 // ranges of equal cost (Ranges), one for each block; parts of items that cross a border leave their accumulators,
-// reference and sum in fp32, and a second kernel joins them.  Two parts at most for a block, 266 KB each, so
+// reference and sum in fp32, and a second kernel joins them.  Two parts at most for a block, 266 KB in all, so
 // the workspace does not depend on the sizes.  32/8 heads, with the read-back from 4-bit pages: 2,048 tokens after 30,000
 // 650 to 665 us (1.04 TFLOP, 1.9 PFLOP/s in the kernel's 540 to 565 us; read-back 25 to 30, join 12), 45 after 6,000
 // 28.4 us (6, 15 and 5), eight requests of 1 to 2,000 after up to 12,000 150 us (30, 105, 8); 64/8 heads, 511 after 8,100 and
@@ -124,7 +124,7 @@ struct Tail {
 struct Parts {
   const int* kv_start;
   int n_kv_rows;
-  bool unsplit;   // no item is cut: there is no join
+  bool unsplit;   // the bounds say that no item is cut: there is no join
   float* o;       // [blocks][2][kD / 8][2 * kTile][8], not divided: what a warp's 32 rows store at once lies together
   float2* stats;  // [blocks][2][2 * kTile]: reference and sum of a row
   Tail* tails;    // [blocks]
@@ -412,6 +412,15 @@ struct Schedule {
   }
 };
 
+// Where every item can have an SM and no sequence more than kUnsplit keys, no item is cut: that costs a
+// long item's time and saves the parts.  Sequences::cost decides it from the starts, so that the caller's bounds and
+// padding change no bit of the output; where these alone say so, no join is launched either.  32/8 heads, 4-bit
+// pages, device time in a graph (time of a call alone), with no join:
+// 20 rows after 300 tokens 16.6 -> 14.0 us (39.6 -> 34.7), 500 without a context 24.3 -> 17.5 (45.5 -> 37.7), 100 after 900
+// 23.5 -> 21.6 (44.8 -> 42.5), but 60 after 1,400 24.0 -> 26.7 and after 1,900 25.1 -> 32.4.  With a join that finds
+// nothing: 8 x 20 after 600 25.1 -> 22.8, 12 x 10 after 1,000 32.8 -> 29.7, 100 after 900 in a call with room for 4,000 22.7 -> 24.8.
+constexpr int kUnsplit = 1024;
+
 // A call with keys before its new rows: its sequences, and what their items cost in keys: past + the keys of the item's last
 // row (whole tiles of rows) + kItemCost for its ends, and an eighth less for an item whose second query tile has no token
 // (measured: 1.3 us for a K/V tile and both query tiles, 1.1 for one, 2.8 to 3.9 for an item's ends, 1.3 us being 128 keys).
@@ -419,7 +428,7 @@ struct Sequences {
   static constexpr int kItemCost = 400;
   const int *q_start, *kv_start;
   int B, n_rows, n_kv_rows, pair, per, heads, lane;
-  bool unsplit;  // every item costs 1: borders of equal ranges lie between items
+  bool unsplit;  // no item is cut: every item costs 1, borders of equal ranges lie between items
   unsigned bits;
 
   __device__ void set(const int* qs, const Parts& parts, int b, int rows, int tokens, int hkv, int ln) {
@@ -465,31 +474,38 @@ struct Sequences {
     const int last = (n - 1) / pair;
     return before_place<C>(last, keys) + item_cost<C>(last, n, keys);
   }
-  // The cost of all items; of_lane: of sequence `lane`; items: how many there are, at most 2^25.
+  // The cost of all items, and whether they are cut (unsplit); of_lane: of sequence `lane`; items: how many there are, at
+  // most 2^25.
   __device__ long long cost(long long* of_lane, unsigned* items) {
     long long total = 0;
-    unsigned many = 0;
+    unsigned many = 0, mine = 0;
+    int most = 0;  // keys of a sequence
     *of_lane = 0;
 #pragma unroll 4
     for (int s = lane; s < B; s += 32) {
       int qa, n, ka, before;
-      const long long c = sequence(s, qa, n, ka, before) ? heads * head_cost<long long>(n, before) : 0;
+      const bool some = sequence(s, qa, n, ka, before);
+      const long long c = some ? heads * head_cost<long long>(n, before) : 0;
+      const unsigned here = (unsigned)heads * (unsigned)((n + pair - 1) / pair);
       total += c;
-      many = min(many + (unsigned)heads * (unsigned)((n + pair - 1) / pair), 1u << 20);
-      if (s == lane) *of_lane = c;
+      many = min(many + here, 1u << 20);
+      most = max(most, some ? before + n : 0);
+      if (s == lane) {
+        *of_lane = c;
+        mine = here;
+      }
     }
     *items = __reduce_add_sync(0xffffffffu, many);
+    if (!unsplit && *items <= gridDim.x && (int)__reduce_max_sync(0xffffffffu, (unsigned)most) <= kUnsplit) {
+      unsplit = true;
+      *of_lane = mine;
+      return *items;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     return total;
   }
 };
-
-// Where every item can have an SM and no sequence more than kUnsplit keys, no item is cut and no join launched: that costs a
-// long item's time and saves the parts and a launch.  32/8 heads, 4-bit pages, device time in a graph (time of a call alone):
-// 20 rows after 300 tokens 16.6 -> 14.0 us (39.6 -> 34.7), 500 without a context 24.3 -> 17.5 (45.5 -> 37.7), 100 after 900
-// 23.5 -> 21.6 (44.8 -> 42.5), but 60 after 1,400 24.0 -> 26.7 and after 1,900 25.1 -> 32.4.
-constexpr int kUnsplit = 1024;
 
 // The items cut into equal ranges of cost for the thread blocks.  A sequence's items follow each other head by head; an item
 // that crosses a range's border is cut at a tile there (not one tile from its ends).  There are as many ranges as pieces of

@@ -414,7 +414,7 @@ class PagedKV:
                scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Causal attention of a plan's rows over what their requests hold (lens, before the plan's commit) and
         over each other: q [rows, Hq, 128], k and v [rows, Hkv, 128] in bf16.  n_held: at least the tokens
-        that the requests with new rows hold in all, which sizes the scratch (a request that does not fit is
+        that the requests with new rows hold in all, which sizes the scratch and nothing else (a request that does not fit is
         reported to :meth:`check`; its rows and those of requests behind it stay as they are).  Rows of no
         request stay as they are in out (zero where out is allocated here).  The held tokens are read back from
         the pages (:meth:`read`), the new ones are taken as given: call it before :meth:`store`, which in 8

@@ -923,7 +923,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const float big = scale_log2 * max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
         if (j == 0) {
           ref = fmaxf(big, kLowest) + kDrop;
-        } else if (__any_sync(0xffffffffu, big > ref + (kSlack - kDrop))) {
+        } else if (__any_sync(0xffffffffu, row < per * G && tok < it.len && big > ref + (kSlack - kDrop))) {
+          // rows of no sequence do not ask, whatever they hold: no bit of the others depends on them
           // S_j is there, so the product with V_(j-1) is complete and O is at rest until P_j is handed over
           const float next = fmaxf(ref, big + kDrop), f = ex2(ref - next);
           ref = next;

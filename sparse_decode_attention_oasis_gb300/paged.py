@@ -222,7 +222,7 @@ class PagedKV:
         self._index = _cuda(self.device)
         self._shape = ctypes.byref(self.shape)
         self._kv_bytes, self._scale_bytes = self.kv.stride(0), self.scale.element_size() * self.scale.stride(0)  # of a layer
-        self._scratch, self._resume_scratch, self._starts = {}, {}, {}  # decode's, resume's, read's next starts, by stream
+        self._scratch, self._resume_scratch = {}, {}  # decode's, resume's, by stream
         with torch.cuda.device(self._index):  # resume's scratch, and 4 * Hkv * 128 for each row and held token
             self._resume_bytes = B.oasis_resume_kv_workspace_bytes(self.shape, 0, 0)
 
@@ -347,19 +347,6 @@ class PagedKV:
             B._check(f"oasis_paged_decode_attn_q{self.bits}", st)
         return out
 
-    def _new_start(self, stream: int) -> torch.Tensor:
-        """An int32 [batch + 1] that no other call has: allocated 32 at a time, which takes the host 1 us each instead of
-        5 beside a launch; by stream, as PyTorch's memory is."""
-        if torch._C._cuda_isCurrentStreamCapturing():
-            return torch.empty(self.batch + 1, dtype=_INT32, device=self.device)
-        try:
-            return self._starts[stream].pop()
-        except (KeyError, IndexError):  # none yet, or none left (another host thread may have taken the last)
-            left = list(torch.empty((32, self.batch + 1), dtype=_INT32, device=self.device).unbind(0))
-            start = left.pop()
-            self._starts[stream] = left
-            return start
-
     def read(self, n_rows: int, ctx_len: Optional[torch.Tensor] = None, layer: int = 0, new=None, out=None,
              only_new: bool = False) -> Rows:
         """The first ctx_len tokens of every request (lens by default) as packed bf16 rows, at most n_rows
@@ -398,14 +385,13 @@ class PagedKV:
             for t in out[:2]:
                 if t.dtype is not _BF16 or t.shape != (n_rows, h, D) or t.device != device or not t.is_contiguous():
                     raise ValueError(f"out must be two contiguous bfloat16 [{n_rows}, {h}, {D}] on {device}")
-        stream = _current_stream(self._index)
         if kv_start is None:
-            kv_start = self._new_start(stream)
+            kv_start = torch.empty(b + 1, dtype=_INT32, device=device)
         lib = B._lib or B.load()
         st = (lib.oasis_read_kv_q8 if self.bits == 8 else lib.oasis_read_kv_q4)(
             self._shape, self.kv.data_ptr() + layer * self._kv_bytes, self.scale.data_ptr() + layer * self._scale_bytes,
             self.table.data_ptr(), ctx_len.data_ptr(), k_at, ks, v_at, vs, start_at, n_new, only_new, kv_start.data_ptr(),
-            out[0].data_ptr(), out[1].data_ptr(), n_rows, self.err.data_ptr(), stream)
+            out[0].data_ptr(), out[1].data_ptr(), n_rows, self.err.data_ptr(), _current_stream(self._index))
         if st:
             B._check(f"oasis_read_kv_q{self.bits}", st)
         return Rows(out[0], out[1], kv_start)

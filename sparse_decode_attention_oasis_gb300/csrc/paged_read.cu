@@ -11,8 +11,8 @@
 // (254 MB, 4 bits): 45 us, 5.7 TB/s, 0.85 of the measured copy rate; 1,000 tokens: 5.3 us, four loads that wait for one
 // another.  Blocks of 16 units, so that the ones that finish early make room: one range for each place of the GPU 49 us;
 // one unit to a warp 46; two blocks an SM 46 (1,000 tokens: 4.5), four 57.  These are figures of 4 bits; in 8 the same
-46,700 tokens (296 MB) take 64 us, 4.6 TB/s, 0.69: at three blocks an SM its 80 registers spill 124 bytes.  In a cache of
-512 slots of which two hold tokens the call takes 10.0 us against 9.3 without the others, of 4,096 25.
+// 46,700 tokens (296 MB) take 64 us, 4.6 TB/s, 0.69: at three blocks an SM its 80 registers spill 124 bytes.  In a cache of
+// 512 slots of which two hold tokens the call takes 10.0 us against 9.3 without the others, of 4,096 25.
 #include <cuda_fp16.h>
 
 #include "paged.cuh"

@@ -58,7 +58,7 @@
 // reference and sum in fp32, and a second kernel joins them.  Two parts at most for a block, 266 KB in all, so
 // the workspace does not depend on the sizes.  32/8 heads, with the read-back from 4-bit pages: 2,048 tokens after 30,000
 // 630 to 665 us in a graph of 12 calls (1.04 TFLOP, 1.9 PFLOP/s in the kernel's 540 to 565 us; read-back 25 to 30, join 12), up
-to 680 in calls that follow each other for a second, when the power cap has the SM clock at 1.72 GHz, 45 after 6,000
+// to 680 in calls that follow each other for a second, when the power cap has the SM clock at 1.72 GHz, 45 after 6,000
 // 28.4 us (6, 15 and 5), eight requests of 1 to 2,000 after up to 12,000 150 us (30, 105, 8); 64/8 heads, 511 after 8,100 and
 // 900 after 700 from 8-bit pages 146 us.  Beside the tiles a block pays 5 to 7 us before its first scores and 3 to 4 at
 // an item's ends.  The join moves what the parts hold (40 MB where every block has two) at the rate of the L2 and HBM.
